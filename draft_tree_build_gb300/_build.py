@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libbastion.so")
 SOURCES = ["api.cu", "topk_marginals.cu", "build_tree.cu", "verify_greedy.cu", "tree_attention.cu",
            "verify_noalloc.cu", "verify_sample.cu", "calibrate.cu",
-           "build_tree_mixture.cu", "lm_head_topk.cu"]
+           "build_tree_mixture.cu", "lm_head_topk.cu",
+           "api_cache.cu", "paged_append.cu", "paged_attention.cu", "paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,7 +33,7 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "bastion.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")]
     return files
 
 

@@ -1,5 +1,5 @@
-"""Python binding of the C ABI in ``include/bastion.h`` (ctypes; argument
-marshalling only).  Every function takes CUDA tensors, passes their device
+"""Python binding of the C ABI in ``include/bastion.h`` and
+``include/bastion_cache.h`` (ctypes; argument marshalling only).  Every function takes CUDA tensors, passes their device
 pointers and the current stream to ``libbastion.so``, and raises on a negative
 return code.  All computation happens in the library's kernels; there is no
 fallback path: if the library cannot be loaded, every call raises.
@@ -16,6 +16,7 @@ from . import _build
 
 BASTION_F32 = 0
 BASTION_BF16 = 1
+BASTION_F16 = 2
 
 STATUS_NONFINITE = 1
 STATUS_EMPTY_ROW = 2
@@ -23,6 +24,8 @@ STATUS_BAD_COST = 4
 STATUS_KV_OVERFLOW = 8
 STATUS_BAD_TREE = 16
 STATUS_BAD_WEIGHT = 32
+STATUS_BAD_PAGE = 64
+STATUS_BAD_ROW = 128
 STATUS_TIMEOUT = 1 << 30
 
 # the exported C symbols, in header order
@@ -38,9 +41,25 @@ SYMBOLS = (
     "bastion_verify_greedy_noalloc",
 )
 
+# the exported C symbols of the paged cache (include/bastion_cache.h), in header order
+CACHE_SYMBOLS = (
+    "bastion_paged_append_workspace_bytes", "bastion_paged_append",
+    "bastion_paged_attention_workspace_bytes", "bastion_paged_attention",
+    "bastion_paged_evict_workspace_bytes", "bastion_paged_evict",
+)
+
 
 class BastionError(RuntimeError):
     pass
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    """bastion_paged_cache of include/bastion_cache.h."""
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("stride_page", ctypes.c_int64), ("stride_slot", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -100,6 +119,20 @@ def lib(build_if_missing: bool = True):
     L.bastion_verify_greedy_noalloc.restype = i32
     L.bastion_verify_greedy_noalloc.argtypes = [vp, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp, vp,
                                                 vp, vp, vp, vp]
+    pc = ctypes.POINTER(_PagedCacheStruct)
+    L.bastion_paged_append_workspace_bytes.restype = sz
+    L.bastion_paged_append_workspace_bytes.argtypes = [i32]
+    L.bastion_paged_append.restype = i32
+    L.bastion_paged_append.argtypes = [pc, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+                                       vp, sz, vp, vp]
+    L.bastion_paged_attention_workspace_bytes.restype = sz
+    L.bastion_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i32]
+    L.bastion_paged_attention.restype = i32
+    L.bastion_paged_attention.argtypes = [pc, vp, i32, i64, vp, f32, vp, vp, vp, vp, vp, sz, vp, vp]
+    L.bastion_paged_evict_workspace_bytes.restype = sz
+    L.bastion_paged_evict_workspace_bytes.argtypes = [i32, i32, i64]
+    L.bastion_paged_evict.restype = i32
+    L.bastion_paged_evict.argtypes = [pc, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
     _lib = L
     return L
 
@@ -324,6 +357,150 @@ def bastion_verify_greedy_noalloc(target_logits, b, n_nodes, parent, token, argm
     _check(rc, "bastion_verify_greedy_noalloc")
 
 
+# --------------------------------------------------------------------------- paged cache
+
+_CACHE_DTYPES = {torch.bfloat16: BASTION_BF16, torch.float16: BASTION_F16}
+
+
+def _need(name, t, dtype, shape):
+    """A contiguous tensor of that type and shape (the library reads its bytes as such)."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise BastionError(f"paged cache: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
+                           f"{list(t.shape)}, strides {t.stride()}")
+
+
+def _on_device(workspace, *tensors):
+    """All on the current CUDA device: the launches go there."""
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace)")
+    dev = workspace.device
+    if dev.type != "cuda":
+        raise BastionError("tensor must live on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise BastionError(f"paged cache: tensors on {t.device} and {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise BastionError(f"paged cache: the tensors are on {dev}, the current device is "
+                           f"cuda:{torch.cuda.current_device()}")
+
+
+def _cache(k_pool, v_pool, page_table):
+    """The cache's struct; pools [n_pages, page_size, Hkv, D] of any strides (a head-major pool is a
+    transposed view), page_table [B, max_pages] int32."""
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
+        raise BastionError("paged cache: the pools must be [n_pages, page_size, Hkv, D], of one shape and dtype")
+    dt = _CACHE_DTYPES.get(k_pool.dtype)
+    if dt is None:
+        raise BastionError(f"paged cache: the pools must be bfloat16 or float16, got {k_pool.dtype}")
+    shape, st = k_pool.shape, k_pool.stride()
+    if st[3] != 1 or st != v_pool.stride():
+        raise BastionError("paged cache: the pools must have equal strides and a contiguous last dimension")
+    if page_table.dim() != 2:
+        raise BastionError("paged cache: page_table must be [B, max_pages]")
+    _need("page_table", page_table, torch.int32, tuple(page_table.shape))
+    return _PagedCacheStruct(k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2],
+                             page_table.data_ptr(), dt, page_table.shape[0], shape[2], shape[3], shape[1],
+                             page_table.shape[1])
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def bastion_paged_append_workspace_bytes(B: int) -> int:
+    return int(lib().bastion_paged_append_workspace_bytes(B))
+
+
+def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, workspace, status,
+                         rows=None, n_new=None, acc=None, pos=None, n_seen=None, n_seen_out=None, stream=None):
+    """k_new/v_new [B, n_rows, Hkv, D] (equal strides, last dim contiguous) enter the cache's next slots: the
+    rows listed in rows [B, m] (a negative entry ends a list; Verify.accept_nodes fits), or the first n_new [B].
+    seq_len_out may be seq_len, n_seen_out n_seen."""
+    c = _cache(k_pool, v_pool, page_table)
+    B, cap = c.B, c.max_pages * c.page_size
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or tuple(k_new.shape[::2]) != (B, c.Hkv) \
+            or k_new.shape[3] != c.D or k_new.dtype != k_pool.dtype or v_new.dtype != k_pool.dtype:
+        raise BastionError("paged append: k_new and v_new must be [B, n_rows, Hkv, D] of the pools' dtype")
+    st = k_new.stride()
+    if st[3] != 1 or st != v_new.stride():
+        raise BastionError("paged append: k_new and v_new must have equal strides and a contiguous last dimension")
+    n_rows = k_new.shape[1]
+    m = n_rows
+    if rows is not None:
+        if rows.dim() != 2:
+            raise BastionError("paged append: rows must be [B, m]")
+        m = rows.shape[1]
+        _need("rows", rows, torch.int32, (B, m))
+    for name, t in (("seq_len", seq_len), ("seq_len_out", seq_len_out), ("status", status), ("n_new", n_new),
+                    ("n_seen", n_seen), ("n_seen_out", n_seen_out)):
+        if t is not None:
+            _need(name, t, torch.int32, (B,))
+    for name, t, dt in (("acc", acc, torch.float32), ("pos", pos, torch.int32)):
+        if t is not None:
+            _need(name, t, dt, (B, c.Hkv, cap))
+    _on_device(workspace, k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, status, rows, n_new, acc,
+               pos, n_seen, n_seen_out)
+    rc = lib().bastion_paged_append(ctypes.byref(c), k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
+                                    _ptr(rows), m, _ptr(n_new), seq_len.data_ptr(), seq_len_out.data_ptr(),
+                                    _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos), workspace.data_ptr(),
+                                    workspace.numel(), status.data_ptr(), _s(stream))
+    _check(rc, "bastion_paged_append")
+
+
+def bastion_paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, cap: int, weights: bool) -> int:
+    """cap: max_pages * page_size."""
+    return int(lib().bastion_paged_attention_workspace_bytes(B, Hq, Hkv, D, cap, int(bool(weights))))
+
+
+def bastion_paged_attention(q, k_pool, v_pool, page_table, seq_len, scale, out, workspace, status, lse=None,
+                            acc=None, acc_out=None, stream=None):
+    """q [B, Hq, D] (heads contiguous, any stride between requests), out [B, Hq, D] contiguous, lse [B, Hq]
+    float32 or None; acc/acc_out [B, Hkv, max_pages * page_size] float32 or None (acc_out may be acc)."""
+    c = _cache(k_pool, v_pool, page_table)
+    if q.dim() != 3 or q.dtype != k_pool.dtype or q.shape[0] != c.B or q.shape[2] != c.D:
+        raise BastionError("paged attention: q must be [B, Hq, D] of the pools' dtype")
+    Hq, st = q.shape[1], q.stride()
+    if st[2] != 1 or (Hq > 1 and st[1] != c.D):
+        raise BastionError("paged attention: the heads of q must be contiguous")
+    _need("out", out, q.dtype, tuple(q.shape))
+    _need("seq_len", seq_len, torch.int32, (c.B,))
+    _need("status", status, torch.int32, (c.B,))
+    if lse is not None:
+        _need("lse", lse, torch.float32, (c.B, Hq))
+    for name, t in (("acc", acc), ("acc_out", acc_out)):
+        if t is not None:
+            _need(name, t, torch.float32, (c.B, c.Hkv, c.max_pages * c.page_size))
+    _on_device(workspace, q, k_pool, v_pool, page_table, seq_len, out, status, lse, acc, acc_out)
+    rc = lib().bastion_paged_attention(ctypes.byref(c), q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale,
+                                       out.data_ptr(), _ptr(lse), _ptr(acc), _ptr(acc_out), workspace.data_ptr(),
+                                       workspace.numel(), status.data_ptr(), _s(stream))
+    _check(rc, "bastion_paged_attention")
+
+
+def bastion_paged_evict_workspace_bytes(B: int, Hkv: int, cap: int) -> int:
+    return int(lib().bastion_paged_evict_workspace_bytes(B, Hkv, cap))
+
+
+def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, budget, n_sink, n_recent,
+                        seq_len_out, acc_out, pos_out, workspace, status, stream=None):
+    """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
+    largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
+    c = _cache(k_pool, v_pool, page_table)
+    for name, t in (("seq_len", seq_len), ("n_seen", n_seen), ("seq_len_out", seq_len_out), ("status", status)):
+        _need(name, t, torch.int32, (c.B,))
+    shape = (c.B, c.Hkv, c.max_pages * c.page_size)
+    for name, t, dt in (("acc", acc, torch.float32), ("acc_out", acc_out, torch.float32),
+                        ("pos", pos, torch.int32), ("pos_out", pos_out, torch.int32)):
+        _need(name, t, dt, shape)
+    _on_device(workspace, k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, seq_len_out, acc_out, pos_out,
+               status)
+    rc = lib().bastion_paged_evict(ctypes.byref(c), seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(),
+                                   pos.data_ptr(), budget, n_sink, n_recent, seq_len_out.data_ptr(),
+                                   acc_out.data_ptr(), pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                   status.data_ptr(), _s(stream))
+    _check(rc, "bastion_paged_evict")
+
+
 # --------------------------------------------------------------------------- buffers
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -501,3 +678,60 @@ class TreeStep:
             step()
         self.graph = g
         return g
+
+
+class PagedCache:
+    """The paged key-value cache of one target layer for B requests, over preallocated device buffers (nothing
+    is allocated after construction, so a step that uses it can be captured in a CUDA graph).
+
+    page_table None: request r owns pages r * max_pages .. (r + 1) * max_pages - 1, i.e. the pools are a
+    contiguous cache [B, max_pages * page_size, Hkv, D], which ``contiguous()`` gives to bastion_tree_attention.
+    weights: keep the accumulated attention weight and the position of every slot, which evict() needs."""
+
+    def __init__(self, B, Hq, Hkv, D, page_size, max_pages, device, dtype=torch.bfloat16, page_table=None,
+                 n_pages=None, weights=False):
+        self.B, self.Hq, self.Hkv, self.D, self.page_size, self.max_pages = B, Hq, Hkv, D, page_size, max_pages
+        self.cap, self.device = max_pages * page_size, device
+        self.identity = page_table is None
+        if page_table is None:
+            n_pages = B * max_pages
+            page_table = torch.arange(n_pages, dtype=torch.int32).view(B, max_pages)
+        elif n_pages is None:
+            raise BastionError("paged cache: a page_table needs n_pages")
+        self.page_table = page_table.to(device=device, dtype=torch.int32).contiguous()
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=device)  # noqa: E731
+        self.k_pool = torch.zeros(n_pages, page_size, Hkv, D, dtype=dtype, device=device)
+        self.v_pool = torch.zeros_like(self.k_pool)
+        self.seq_len, self.n_seen, self.status = i32(B), i32(B), i32(B)
+        self.acc = torch.zeros(B, Hkv, self.cap, device=device) if weights else None
+        self.pos = i32(B, Hkv, self.cap) if weights else None
+        self.ws_append = workspace(bastion_paged_append_workspace_bytes(B), device)
+        self.ws_attend = workspace(bastion_paged_attention_workspace_bytes(B, Hq, Hkv, D, self.cap, weights), device)
+        self.ws_evict = workspace(bastion_paged_evict_workspace_bytes(B, Hkv, self.cap), device) if weights else None
+
+    def contiguous(self):
+        """(k, v) [B, cap, Hkv, D]: the same memory as a contiguous cache."""
+        if not self.identity:
+            raise BastionError("paged cache: its pages are not in order")
+        shape = (self.B, self.cap, self.Hkv, self.D)
+        return self.k_pool.view(shape), self.v_pool.view(shape)
+
+    def append(self, k_new, v_new, rows=None, n_new=None, stream=None):
+        """The rows of k_new/v_new [B, n_rows, Hkv, D] (all, the first n_new, or those listed in rows) enter the
+        next slots; rows = Verify.accept_nodes commits the accepted path of a verified tree."""
+        bastion_paged_append(k_new, v_new, self.k_pool, self.v_pool, self.page_table, self.seq_len, self.seq_len,
+                             self.ws_append, self.status, rows, n_new, self.acc, self.pos, self.n_seen, self.n_seen,
+                             stream)
+
+    def attend(self, q, scale, out, lse=None, stream=None):
+        """out [B, Hq, D] = attention of q over the used slots; adds the weights to acc where they are kept."""
+        bastion_paged_attention(q, self.k_pool, self.v_pool, self.page_table, self.seq_len, scale, out,
+                                self.ws_attend, self.status, lse, self.acc, self.acc, stream)
+
+    def evict(self, budget, n_sink=0, n_recent=0, stream=None):
+        """Keeps budget slots per request and KV head."""
+        if self.acc is None:
+            raise BastionError("paged cache: evict needs weights=True")
+        bastion_paged_evict(self.k_pool, self.v_pool, self.page_table, self.seq_len, self.n_seen, self.acc, self.pos,
+                            budget, n_sink, n_recent, self.seq_len, self.acc, self.pos, self.ws_evict, self.status,
+                            stream)

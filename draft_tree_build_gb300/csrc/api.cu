@@ -80,6 +80,8 @@ const char *bastion_status_string(int code) {
     case BASTION_STATUS_KV_OVERFLOW: return "ctx_len + n_nodes exceeds the KV cache capacity";
     case BASTION_STATUS_BAD_TREE: return "n_nodes outside [1, n_max]";
     case BASTION_STATUS_BAD_WEIGHT: return "a mixture weight is negative or not finite";
+    case BASTION_STATUS_BAD_PAGE: return "a used page table entry outside the pool";
+    case BASTION_STATUS_BAD_ROW: return "an appended row index outside the new rows";
     case BASTION_STATUS_TIMEOUT: return "a bounded device wait ran out";
     default: return "unknown code";
   }

@@ -1,0 +1,41 @@
+// What the kernels of the paged cache share: its geometry on the device.
+#pragma once
+
+#include "bastion_cache.h"
+#include "common.cuh"
+
+namespace bastion {
+
+struct Paged {
+  uint16_t *k, *v;
+  int64_t n_pages, st_page, st_slot, st_head;
+  const int32_t *table;
+  int B, Hkv, D, page, shift, max_pages;  // page = 1 << shift
+  int cap;                                // max_pages * page
+};
+
+// The used slots of a request, in [0, cap]; a length outside it sets the status bit.
+__device__ __forceinline__ int paged_len(const Paged &c, const int32_t *seq_len, int r, int32_t *status) {
+  const int n = seq_len[r];
+  if (n >= 0 && n <= c.cap) return n;
+  atomicOr(&status[r], BASTION_STATUS_KV_OVERFLOW);
+  return n < 0 ? 0 : c.cap;
+}
+
+// The page that holds slot j < cap of request r, or -1 (and the status bit)
+// when the table's entry is not a page of the pool.
+__device__ __forceinline__ int paged_page(const Paged &c, int r, int j, int32_t *status) {
+  const int p = c.table[(size_t)r * c.max_pages + (j >> c.shift)];
+  if (p >= 0 && p < c.n_pages) return p;
+  atomicOr(&status[r], BASTION_STATUS_BAD_PAGE);
+  return -1;
+}
+
+// Element offset of slot j's row of head h, given its page.
+__device__ __forceinline__ int64_t paged_row(const Paged &c, int page, int j, int h) {
+  return page * c.st_page + (int64_t)(j & (c.page - 1)) * c.st_slot + h * c.st_head;
+}
+
+Paged paged_args(const bastion_paged_cache &c);
+
+}  // namespace bastion

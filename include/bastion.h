@@ -31,7 +31,8 @@
  *    returns the counters to zero, so the same workspace serves the next call
  *    without clearing.  Calls that may run concurrently need separate
  *    workspaces.
- *  - dtype: BASTION_F32 (float) or BASTION_BF16 (bfloat16 bits).
+ *  - dtype: BASTION_F32 (float) or BASTION_BF16 (bfloat16 bits); the paged
+ *    cache of bastion_cache.h takes BASTION_BF16 or BASTION_F16 (IEEE half).
  */
 #ifndef BASTION_H_
 #define BASTION_H_
@@ -45,7 +46,7 @@ extern "C" {
 
 typedef struct CUstream_st *bastion_stream_t; /* the same handle as cudaStream_t */
 
-enum { BASTION_F32 = 0, BASTION_BF16 = 1 };
+enum { BASTION_F32 = 0, BASTION_BF16 = 1, BASTION_F16 = 2 };
 
 enum {
   BASTION_OK = 0,
@@ -65,6 +66,8 @@ enum {
   BASTION_STATUS_KV_OVERFLOW = 8,  /* ctx_len + n_nodes > L_cap, or ctx_len < 0 */
   BASTION_STATUS_BAD_TREE = 16,    /* n_nodes outside [1, n_max] */
   BASTION_STATUS_BAD_WEIGHT = 32,  /* a mixture weight pi is negative or not finite */
+  BASTION_STATUS_BAD_PAGE = 64,    /* a page table entry outside [0, n_pages) is in use */
+  BASTION_STATUS_BAD_ROW = 128,    /* an appended row index outside [0, n_rows) */
   BASTION_STATUS_TIMEOUT = 1 << 30 /* a bounded device wait ran out */
 };
 

@@ -1,0 +1,197 @@
+"""Refusals of the paged cache's calls: the C ABI's host checks (fake pointers,
+never dereferenced: every call fails before a launch) and the binding's."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NULL, SIZE, DTYPE, ALIGN, WORKSPACE, UNSUPPORTED = -1, -2, -3, -4, -5, -6
+vp = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def b():
+    from draft_tree_build_gb300 import bastion
+    bastion.lib()
+    return bastion
+
+
+def _declared():
+    src = open(os.path.join(ROOT, "include", "bastion_cache.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    return {m.group(1): m.group(2).count(",") + 1 for m in re.finditer(r"\b(bastion_\w+)\s*\(([^)]*)\)\s*;", src)}
+
+
+def test_header_and_binding_agree(b):
+    names = _declared()
+    assert tuple(names) == b.CACHE_SYMBOLS
+    for n, args in names.items():
+        assert len(getattr(b.lib(), n).argtypes) == args, n
+    for code in (b.STATUS_BAD_PAGE, b.STATUS_BAD_ROW):
+        assert b.bastion_status_string(code) != "unknown code"
+
+
+def _struct(b, **over):
+    v = dict(k_pool=0x100000, v_pool=0x200000, n_pages=100, stride_page=16 * 8 * 128, stride_slot=8 * 128,
+             stride_head=128, page_table=0x300000, dtype=1, B=4, Hkv=8, D=128, page_size=16, max_pages=20)
+    v.update(over)
+    return ctypes.byref(b._PagedCacheStruct(*(v[n] for n, _ in b._PagedCacheStruct._fields_)))
+
+
+APPEND = dict(k_new=vp(0x400000), v_new=vp(0x500000), n_rows=16, sb=16 * 1024, sr=1024, sh=128, rows=None, m=16,
+              n_new=None, seq_len=vp(0x600000), seq_len_out=vp(0x600000), n_seen=vp(0x700000),
+              n_seen_out=vp(0x700000), acc=vp(0x800000), pos=vp(0x900000), ws=vp(0xa00000), ws_bytes=1 << 20,
+              status=vp(0xb00000), stream=None)
+ATTEND = dict(q=vp(0x400000), Hq=32, q_stride_b=32 * 128, seq_len=vp(0x500000), scale=ctypes.c_float(0.1),
+              out=vp(0x600000), lse=None, acc=vp(0x10000000), acc_out=vp(0x20000000), ws=vp(0xa00000),
+              ws_bytes=1 << 30, status=vp(0xb00000), stream=None)
+EVICT = dict(seq_len=vp(0x400000), n_seen=vp(0x500000), acc=vp(0x10000000), pos=vp(0x20000000), budget=64, sink=4,
+             recent=16, seq_len_out=vp(0x400000), acc_out=vp(0x10000000), pos_out=vp(0x20000000), ws=vp(0xa00000),
+             ws_bytes=1 << 30, status=vp(0xb00000), stream=None)
+CALLS = {"append": ("bastion_paged_append", APPEND), "attend": ("bastion_paged_attention", ATTEND),
+         "evict": ("bastion_paged_evict", EVICT)}
+
+
+def _call(b, which, cache=None, **over):
+    name, args = CALLS[which]
+    assert set(over) <= set(args)
+    return getattr(b.lib(), name)(_struct(b, **(cache or {})), *{**args, **over}.values())
+
+
+CACHE_REFUSALS = [
+    (dict(k_pool=None), NULL), (dict(v_pool=None), NULL), (dict(page_table=None), NULL),
+    (dict(dtype=0), DTYPE), (dict(dtype=7), DTYPE),
+    (dict(B=0), SIZE), (dict(B=4097), SIZE), (dict(Hkv=0), SIZE), (dict(B=4096, Hkv=17), SIZE),
+    (dict(n_pages=0), SIZE), (dict(n_pages=1 << 31), SIZE), (dict(max_pages=0), SIZE),
+    (dict(max_pages=(1 << 24) + 1), SIZE), (dict(D=0), SIZE), (dict(page_size=0), SIZE),
+    (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED), (dict(page_size=4), UNSUPPORTED),
+    (dict(page_size=24), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED),
+    (dict(stride_page=16 * 1024 + 4), SIZE), (dict(stride_slot=64), SIZE), (dict(stride_head=0), SIZE),
+    (dict(stride_slot=-1024), SIZE),
+    (dict(k_pool=0x100008), ALIGN), (dict(v_pool=0x200002), ALIGN),
+]
+
+
+@pytest.mark.parametrize("which", list(CALLS))
+@pytest.mark.parametrize("over,code", CACHE_REFUSALS)
+def test_cache_refusals(b, which, over, code):
+    assert _call(b, which, over) == code
+
+
+@pytest.mark.parametrize("which,over,code", [
+    ("append", dict(k_new=None), NULL), ("append", dict(seq_len=None), NULL), ("append", dict(status=None), NULL),
+    ("append", dict(ws=None), NULL), ("append", dict(acc=None), NULL), ("append", dict(pos=None), NULL),
+    ("append", dict(n_seen=None), NULL), ("append", dict(n_seen=None, n_seen_out=None), NULL),
+    ("append", dict(m=0), SIZE), ("append", dict(m=17), SIZE), ("append", dict(n_rows=0), SIZE),
+    ("append", dict(rows=vp(0xc00000), m=1025), SIZE), ("append", dict(sr=1028), SIZE), ("append", dict(sh=-128), SIZE),
+    ("append", dict(k_new=vp(0x400008)), ALIGN), ("append", dict(ws=vp(0xa00010)), ALIGN),
+    ("append", dict(ws_bytes=16), WORKSPACE), ("append", dict(seq_len_out=vp(0x600004)), UNSUPPORTED),
+    ("append", dict(n_seen_out=vp(0x6ffffc)), UNSUPPORTED),
+    ("attend", dict(q=None), NULL), ("attend", dict(out=None), NULL), ("attend", dict(acc=None), NULL),
+    ("attend", dict(acc_out=None), NULL), ("attend", dict(Hq=33), SIZE), ("attend", dict(Hq=0), SIZE),
+    ("attend", dict(Hq=136), UNSUPPORTED), ("attend", dict(scale=ctypes.c_float(0.0)), SIZE),
+    ("attend", dict(scale=ctypes.c_float(float("nan"))), SIZE), ("attend", dict(scale=ctypes.c_float(float("inf"))), SIZE),
+    ("attend", dict(q_stride_b=4100), SIZE), ("attend", dict(q=vp(0x400008)), ALIGN),
+    ("attend", dict(out=vp(0x600008)), ALIGN), ("attend", dict(ws_bytes=1024), WORKSPACE),
+    ("attend", dict(acc_out=vp(0x10000040)), UNSUPPORTED),
+    ("evict", dict(acc=None), NULL), ("evict", dict(pos_out=None), NULL), ("evict", dict(n_seen=None), NULL),
+    ("evict", dict(budget=0), SIZE), ("evict", dict(sink=-1), SIZE), ("evict", dict(recent=-1), SIZE),
+    ("evict", dict(sink=40, recent=25), SIZE), ("evict", dict(ws_bytes=64), WORKSPACE),
+    ("evict", dict(acc_out=vp(0x10000004)), UNSUPPORTED), ("evict", dict(pos_out=vp(0x1fffff00)), UNSUPPORTED),
+    ("evict", dict(ws=vp(0xa00080)), ALIGN),
+])
+def test_call_refusals(b, which, over, code):
+    assert _call(b, which, **over) == code
+
+
+def test_workspace_queries(b):
+    assert b.bastion_paged_append_workspace_bytes(4) > 0
+    assert b.bastion_paged_append_workspace_bytes(0) == 0 == b.bastion_paged_append_workspace_bytes(4097)
+    w = b.bastion_paged_attention_workspace_bytes
+    assert 0 < w(4, 32, 8, 128, 4096, False) < w(4, 32, 8, 128, 4096, True)
+    assert w(4, 33, 8, 128, 4096, False) == w(4, 32, 8, 96, 4096, False) == w(4, 32, 1, 128, 4096, False) == 0
+    assert w(4, 32, 8, 128, (1 << 28) + 1, False) == 0
+    assert b.bastion_paged_evict_workspace_bytes(4, 8, 4096) > 0
+    assert b.bastion_paged_evict_workspace_bytes(4096, 17, 4096) == 0
+
+
+def _tensors(B=2, Hq=8, Hkv=2, D=128, page=16, pages=6, max_pages=3):
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    return dict(k=bf(pages, page, Hkv, D), v=bf(pages, page, Hkv, D), table=i32(B, max_pages), lens=i32(B), st=i32(B),
+                q=bf(B, Hq, D), out=bf(B, Hq, D), acc=torch.zeros(B, Hkv, max_pages * page),
+                pos=i32(B, Hkv, max_pages * page), new=bf(B, 4, Hkv, D), ws=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def _attend(b, t, **kw):
+    b.bastion_paged_attention(t["q"], t["k"], t["v"], t["table"], t["lens"], 0.1, t["out"], t["ws"], t["st"], **kw)
+
+
+@pytest.mark.parametrize("change,match", [
+    (lambda t: t.update(k=t["k"].float()), "one shape and dtype"),
+    (lambda t: t.update(k=t["k"].float(), v=t["v"].float()), "bfloat16 or float16"),
+    (lambda t: t.update(k=t["k"][:5]), "one shape"),
+    (lambda t: t.update(v=t["v"].transpose(1, 2).contiguous().transpose(1, 2)), "equal strides"),
+    (lambda t: t.update(k=t["k"][0], v=t["v"][0]), "n_pages"),
+    (lambda t: t.update(table=t["table"].long()), "page_table"),
+    (lambda t: t.update(table=t["table"][0]), "page_table"),
+    (lambda t: t.update(q=t["q"].half()), "pools' dtype"),
+    (lambda t: t.update(q=t["q"][:, :, :64]), "q must be"),
+    (lambda t: t.update(q=t["q"].transpose(0, 1).contiguous().transpose(0, 1)), "heads of q"),
+    (lambda t: t.update(out=t["out"].float()), "out"),
+    (lambda t: t.update(lens=t["lens"].long()), "seq_len"),
+    (lambda t: t.update(st=t["st"][:1]), "status"),
+    (lambda t: t.update(ws=t["ws"].int()), "workspace"),
+    (lambda t: None, "CUDA device"),
+])
+def test_binding_refuses_attention_arguments(b, change, match):
+    t = _tensors()
+    change(t)
+    with pytest.raises(b.BastionError, match=match):
+        _attend(b, t)
+
+
+def test_binding_refuses_other_arguments(b):
+    t = _tensors()
+    with pytest.raises(b.BastionError, match="lse"):
+        _attend(b, t, lse=torch.zeros(2, 8, dtype=torch.float64))
+    with pytest.raises(b.BastionError, match="acc"):
+        _attend(b, t, acc=t["acc"][:, :, :40], acc_out=t["acc"])
+
+    def append(k=t["new"], v=t["new"], **kw):
+        b.bastion_paged_append(k, v, t["k"], t["v"], t["table"], t["lens"], t["lens"], t["ws"], t["st"], **kw)
+
+    with pytest.raises(b.BastionError, match="pools' dtype"):
+        append(k=t["new"].half())
+    with pytest.raises(b.BastionError, match="pools' dtype"):
+        append(k=t["new"][:, :, :1], v=t["new"][:, :, :1])
+    with pytest.raises(b.BastionError, match="equal strides"):
+        append(v=t["new"].transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(b.BastionError, match="rows"):
+        append(rows=torch.zeros(2, 4, dtype=torch.int64))
+    with pytest.raises(b.BastionError, match="rows"):
+        append(rows=torch.zeros(8, dtype=torch.int32))
+    with pytest.raises(b.BastionError, match="n_new"):
+        append(n_new=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(b.BastionError, match="pos"):
+        append(acc=t["acc"], pos=t["pos"].long())
+    with pytest.raises(b.BastionError, match="CUDA device"):
+        append()
+
+    def evict(**kw):
+        a = dict(seq_len=t["lens"], n_seen=t["lens"], acc=t["acc"], pos=t["pos"])
+        a.update(kw)
+        b.bastion_paged_evict(t["k"], t["v"], t["table"], a["seq_len"], a["n_seen"], a["acc"], a["pos"], 8, 0, 0,
+                              t["lens"], t["acc"], t["pos"], t["ws"], t["st"])
+
+    with pytest.raises(b.BastionError, match="n_seen"):
+        evict(n_seen=t["lens"].long())
+    with pytest.raises(b.BastionError, match="acc"):
+        evict(acc=t["acc"].double())
+    with pytest.raises(b.BastionError, match="CUDA device"):
+        evict()
+    with pytest.raises(b.BastionError, match="n_pages"):
+        b.PagedCache(1, 1, 1, 64, 8, 1, "cpu", page_table=torch.zeros(1, 1, dtype=torch.int32))
