@@ -66,6 +66,11 @@ size_t slots_bytes(const bastion_paged_cache *c) {  // of acc and of pos
   return (size_t)c->B * c->Hkv * (size_t)c->max_pages * c->page_size * 4;
 }
 
+// The batch's 128-key tiles are counted in 31 bits.
+bool tiles_ok(const bastion_paged_cache *c) {
+  return (int64_t)c->B * c->Hkv * (((int64_t)c->max_pages * c->page_size + 127) / 128) < (1LL << 31);
+}
+
 // Checks that every call makes of the cache.
 int check_cache(const bastion_paged_cache *c) {
   if (!c || !c->k_pool || !c->v_pool || !c->page_table) return BASTION_ERR_NULL;
@@ -133,6 +138,7 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
   if (rc != BASTION_OK) return rc;
   if (Hq < 1 || Hq % cache->Hkv || !(scale > 0.f) || !(scale < 1e30f)) return BASTION_ERR_SIZE;
   if (Hq / cache->Hkv > 16) return BASTION_ERR_UNSUPPORTED;
+  if (!tiles_ok(cache)) return BASTION_ERR_SIZE;
   if (!stride_ok(cache->B, q_stride_b, 0)) return BASTION_ERR_SIZE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return BASTION_ERR_ALIGN;
   if (acc && !same_or_apart(acc, acc_out, slots_bytes(cache))) return BASTION_ERR_UNSUPPORTED;

@@ -2,11 +2,44 @@
 //
 //   s_j = scale q.k_j, out = sum_j exp(s_j - lse) v_j, lse = log sum_j exp(s_j)
 //
-// One CTA per (request, query head): each warp takes every fourth key with a
-// running maximum m, sum l and output o (o and l are rescaled by 2^(m - m')
-// when the maximum moves), a lane holding D / 32 of the elements; the warps'
-// parts are joined at the end.  With weights, the scores are kept and a second
-// kernel adds sum_h exp(s - lse_h) to each slot's accumulated weight.
+// Bound by HBM: a token's key and value are read once for the G <= 16 query
+// heads of their KV head (2 G flops a byte).  What the design serves is
+// an uninterrupted stream of tiles from HBM to every SM:
+//
+//  * one persistent CTA per SM.  The batch is a list of 128-key tiles, request
+//    by request, KV head by KV head (a unit), and every CTA takes an equal
+//    contiguous share of it, whatever the lengths; a share is a few segments,
+//    each a run of tiles of one unit.  A unit that several CTAs share is joined
+//    by the last of them to finish, over the parts in tile order, so that the
+//    result does not depend on which one that is;
+//  * warp 0 streams key tiles and warp 1 value tiles through rings in shared
+//    memory with TMA, one box per page and 64-element column block (128-byte
+//    swizzle), across segment boundaries;
+//  * the products keep the cache's tiles as the M = 128 operand, so that G
+//    heads cost N = 16 columns instead of 128 rows: S^T = K Q^T (M: keys) and
+//    O^T += V^T P^T (M: elements of the head; V is read transposed by the
+//    descriptor).  Keys and values never pass through registers;
+//  * warps 4-7 take the softmax: thread = key, G scores each from TMEM.  The
+//    heads' reference maxima are common to the 128 threads; a tile whose scores
+//    stay below reference + 2^8 (one barrier vote) goes ahead without a
+//    maximum, otherwise the references move and O is rescaled.  Sums stay in
+//    the threads until the segment ends;
+//  * P is written as a high and a low 16-bit term in separate columns (N = 2 x 8
+//    or 2 x 16), which the tensor cores multiply alike: the weights keep
+//    16 bits or more, where one bf16 term would add 2^-9 of noise to the output.
+//    P is stored key by key (16 bytes a thread, an MN-major operand without
+//    swizzle).  Half precision weights are scaled by 2^6, so that those below
+//    2^-24 of the largest are not lost.
+//  * value rows past the sequence's end (a page's unused slots may hold NaN) are
+//    zeroed in shared memory; their scores are masked.
+//
+// With weights, the scores (in base 2) are kept and a second kernel adds
+// sum_h exp2(s - lse_h) to each slot's accumulated weight.
+//
+// Every wait is bounded (~1 s); after one ran out the CTA flags the request,
+// waits for its own copies and products (bounded), frees its TMEM and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -17,8 +50,13 @@ namespace bastion {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kMaxUnits = 65536;       // B * Hkv
+constexpr int kMaxUnits = 65536;  // B * Hkv: arrival counters
+constexpr int kMaxB = 4096;
+constexpr int kMaxGrid = 192;     // CTAs that may hold parts
+constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their references and sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 256;
+constexpr float kGrow = 8.0f;     // a score may exceed its head's reference by 2^8
 
 struct AttendArgs {
   const uint16_t *q;
@@ -30,68 +68,677 @@ struct AttendArgs {
   float *lse;
   const float *acc;
   float *acc_out;
-  float *lse2;    // [B, Hq] base-2 log of the sum, of the scores in base 2
-  float *scores;  // [B, Hkv, tiles, G, 128], in base 2
+  uint32_t *arrived;  // [kMaxUnits], zero between calls
+  float *parts;       // [2 * kMaxGrid, kPartFloats]
+  float *lse2;        // [B, Hq] base-2 log of the sum, of the scores in base 2
+  float *scores;      // [B, Hkv, tiles, G, 128], in base 2
   int tiles_cap;
+  int swap;           // tensor map dimensions 1 and 2: (head, slot) instead of (slot, head)
   int32_t *status;
 };
 
-template <bool kHalf>
-__device__ __forceinline__ float from16(uint16_t x) {
-  return kHalf ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+// --------------------------------------------------------------------------- shared memory
+
+// D elements a head, GP head columns (8 or 16).  The value ring comes first:
+// with D = 64 the transposed value operand has 64 rows, and the M = 128
+// instruction's other 64 rows read the memory one tile further on; those rows
+// of O are never used.
+template <int D, int GP>
+struct Layout {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kNP = 2 * GP;                              // high and low columns of P
+  static constexpr uint32_t kTile = kTileKeys * D * 2;
+  static constexpr uint32_t kBlock = kTileKeys * 128;             // 64-element column block of a tile
+  static constexpr uint32_t kQ = (D / 64) * 16 * 128;
+  static constexpr uint32_t kP = (kNP / 8) * kTileKeys * 16;
+  static constexpr uint32_t kOffV = 0;
+  static constexpr uint32_t kOffK = kStages * kTile;
+  static constexpr uint32_t kOffQ = 2 * kStages * kTile;
+  static constexpr uint32_t kOffP = kOffQ + 2 * kQ;
+  static constexpr uint32_t kOffList = kOffP + 2 * kP;
+  static constexpr uint32_t kOffMisc = kOffList + kMaxB * 2;
+};
+
+struct Misc {
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_empty[2], mma_done;
+  unsigned long long warp_sum[8];
+  float xm[4][16], xl[4][16];
+  int first_rank, off0;
+  uint32_t last;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int D, int GP>
+constexpr uint32_t smem_bytes() {
+  return Layout<D, GP>::kOffMisc + (uint32_t)sizeof(Misc) + 1024;
 }
+
+// --------------------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;        // descriptor version
+  d |= (uint64_t)swizzle << 61;  // 2: 128 bytes, 0: none
+  return d;
+}
+
+// kind::f16: fp32 accumulators, A and B of one 16-bit type, M = 128, N = n.
+template <bool kHalf>
+__device__ __forceinline__ constexpr uint32_t idesc(bool a_mn, bool b_mn, int n) {
+  return (1u << 4) | (kHalf ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"(accum));
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// N consecutive TMEM columns of the thread's lane, as one load or store per 8.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  uint32_t x[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]),
+                   "=r"(x[i + 6]), "=r"(x[i + 7])
+                 : "r"(taddr + (uint32_t)i));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(x[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr + (uint32_t)i),
+                 "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), "r"(__float_as_uint(v[i + 2])),
+                 "r"(__float_as_uint(v[i + 3])), "r"(__float_as_uint(v[i + 4])), "r"(__float_as_uint(v[i + 5])),
+                 "r"(__float_as_uint(v[i + 6])), "r"(__float_as_uint(v[i + 7]))
+                 : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Whether any of the 128 softmax threads says so; a barrier among them.
+__device__ __forceinline__ bool vote128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Bounded wait that also honours the CTA's abort flag.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  uint32_t spins = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++spins & 63u) == 0u) {
+      if (*abort) return false;
+      if (global_ns() - t0 > 1000000000ull) {
+        *abort = 1;
+        atomicOr(status, BASTION_STATUS_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// p as two 16-bit terms: hi = round(p), lo = round(p - hi), two heads a word.
+template <bool kHalf>
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+  if (kHalf) {
+    const __half2 h = __floats2half2_rn(p0, p1);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(p0 - f.x, p1 - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+  } else {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
+    const float l0 = p0 - bf16lo(hi), l1 = p1 - bf16hi(hi);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
+  }
+}
+
 template <bool kHalf>
 __device__ __forceinline__ uint16_t to16(float x) {
   return kHalf ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-template <bool kHalf>
-__global__ void __launch_bounds__(128) paged_attention_kernel(Paged c, AttendArgs a) {
+// --------------------------------------------------------------------------- the shares
+
+__device__ __forceinline__ int clamped_len(const Paged &c, const AttendArgs &a, int r) {
+  return min(max(a.seq_len[r], 0), c.cap);
+}
+
+// A CTA's tiles, one after the other: tile t of the unit (request r, KV head g).
+struct Walk {
+  const uint16_t *list;  // the share's requests that have tiles
+  int li, r, n, tiles, g, t, left;
+  bool first;  // the first tile of its segment
+  __device__ __forceinline__ void load(const Paged &c, const AttendArgs &a) {
+    r = list[li];
+    n = clamped_len(c, a, r);
+    tiles = (n + kTileKeys - 1) / kTileKeys;
+  }
+  __device__ __forceinline__ void start(const Paged &c, const AttendArgs &a, const uint16_t *l, int off, int count) {
+    list = l;
+    li = 0;
+    left = count;
+    first = true;
+    if (left > 0) {
+      load(c, a);
+      g = off / tiles;
+      t = off - g * tiles;
+    }
+  }
+  __device__ __forceinline__ void step(const Paged &c, const AttendArgs &a) {
+    first = false;
+    --left;
+    if (++t == tiles) {
+      t = 0;
+      first = true;
+      if (++g == c.Hkv) {
+        g = 0;
+        ++li;
+        if (left > 0) load(c, a);
+      }
+    }
+  }
+  __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == 1; }
+};
+
+template <bool kHalf, int D, int GP>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Paged c,
+                           AttendArgs a) {
+  using Lay = Layout<D, GP>;
+  constexpr int kStages = Lay::kStages, kNP = Lay::kNP, kBlocks = D / 64;
+  constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Misc &ms = *reinterpret_cast<Misc *>(smem + Lay::kOffMisc);
+  uint16_t *list = reinterpret_cast<uint16_t *>(smem + Lay::kOffList);
+  volatile int *abort = &ms.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ms.k_full[s], 1);
+      mbar_init(&ms.k_empty[s], 1);
+      mbar_init(&ms.v_full[s], 1);
+      mbar_init(&ms.v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms.s_full[s], 1);
+      mbar_init(&ms.s_free[s], 4);
+      mbar_init(&ms.p_full[s], 128);
+      mbar_init(&ms.pv_done[s], 1);
+      mbar_init(&ms.q_full[s], 32);
+      mbar_init(&ms.q_empty[s], 1);
+    }
+    mbar_init(&ms.mma_done, 1);
+    ms.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 64;" ::"r"(smem_u32(&ms.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, g = h / a.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = paged_len(c, a.seq_len, r, a.status);
-  const int e = c.D >> 5;  // elements per lane: d = lane + 32 i
-  float q[4], o[4] = {};
-  for (int i = 0; i < e; ++i) q[i] = from16<kHalf>(a.q[r * a.q_st_b + h * c.D + lane + 32 * i]) * a.scale_log2;
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < n; j += 4) {
-    const int p = paged_page(c, r, j, a.status);
-    if (p < 0) continue;
-    const int64_t row = paged_row(c, p, j, g);
-    float s = 0.f;
-    for (int i = 0; i < e; ++i) s += q[i] * from16<kHalf>(c.k[row + lane + 32 * i]);
+
+  // ------------------------------------------------------------ this CTA's share
+  // prefix sums over the requests of (requests with tiles, tiles), 24 and 40 bits
+  const int chunk = (c.B + kThreads - 1) / kThreads, b0 = min(c.B, tid * chunk), b1 = min(c.B, b0 + chunk);
+  unsigned long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = blockIdx.x == 0 ? paged_len(c, a.seq_len, b, a.status) : clamped_len(c, a, b);
+    const int t = (n + kTileKeys - 1) / kTileKeys;
+    mine += (unsigned long long)t | ((unsigned long long)(t > 0) << 40);
+  }
+  unsigned long long incl = mine;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-    if (a.scores && lane == 0)
-      a.scores[((((size_t)r * c.Hkv + g) * a.tiles_cap + j / kTileKeys) * a.G + h % a.G) * kTileKeys + j % kTileKeys] = s;
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = s == -INFINITY ? 0.f : exp2f(s - mn);
-    l = l * f + w;
-    for (int i = 0; i < e; ++i) o[i] = o[i] * f + w * from16<kHalf>(c.v[row + lane + 32 * i]);
-    m = mn;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
   }
-  __shared__ float s_m[4], s_l[4], s_o[4][128];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  for (int i = 0; i < e; ++i) s_o[warp][lane + 32 * i] = o[i];
+  if (lane == 31) ms.warp_sum[warp] = incl;
+  tc_fence_before();
   __syncthreads();
-  const float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float L = 0.f, O = 0.f;
-  const int d = threadIdx.x;
-  for (int w = 0; w < 4; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-    L += s_l[w] * f;
-    if (d < c.D) O += s_o[w][d] * f;
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  unsigned long long before = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) before += ms.warp_sum[w];
+    all += ms.warp_sum[w];
   }
-  const float lse2 = L == 0.f ? -INFINITY : M + log2f(L);
-  if (d < c.D) a.out[((size_t)r * a.Hq + h) * c.D + d] = to16<kHalf>(L == 0.f ? 0.f : O / L);
-  if (d == 0) {
-    if (a.lse) a.lse[(size_t)r * a.Hq + h] = lse2 * kLn2;
-    if (a.acc) a.lse2[(size_t)r * a.Hq + h] = lse2;
+  constexpr unsigned long long kLow = (1ull << 40) - 1;
+  const long long total = (long long)(all & kLow) * c.Hkv;
+  const long long n_cta = total < (long long)gridDim.x ? total : (long long)gridDim.x;
+  long long f0 = 0, f1 = 0;
+  if ((long long)blockIdx.x < n_cta) {
+    f0 = total * blockIdx.x / n_cta;
+    f1 = total * (blockIdx.x + 1) / n_cta;
+  }
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {  // find the first request of the share, then list them
+    unsigned long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int t = (clamped_len(c, a, b) + kTileKeys - 1) / kTileKeys;
+      const long long lo = (long long)(at & kLow) * c.Hkv, hi = lo + (long long)t * c.Hkv;
+      const int rank = (int)(at >> 40);
+      if (t > 0 && lo < f1 && hi > f0) {
+        if (pass == 0 && lo <= f0) {
+          ms.first_rank = rank;
+          ms.off0 = (int)(f0 - lo);
+        }
+        if (pass == 1) list[rank - ms.first_rank] = (uint16_t)b;
+      }
+      at += (unsigned long long)t | ((unsigned long long)(t > 0) << 40);
+    }
+    __syncthreads();
+  }
+  const int share = (int)(f1 - f0);
+  Walk w;
+  w.start(c, a, list, ms.off0, share);
+
+  if (warp < 2) {
+    // ------------------------------------------------------------ TMA: warp 0 keys, warp 1 values
+    const CUtensorMap *map = warp == 0 ? &tm_k : &tm_v;
+    uint64_t *full = warp == 0 ? ms.k_full : ms.v_full, *empty = warp == 0 ? ms.k_empty : ms.v_empty;
+    unsigned char *ring = smem + (warp == 0 ? Lay::kOffK : Lay::kOffV);
+    const int pages_tile = kTileKeys >> c.shift, blk = lane & (kBlocks - 1), pg = lane / kBlocks;
+    // the page of this lane's box; -1: the tile has no such page
+    auto page_of = [&](const Walk &x) {
+      if (x.left <= 0 || pg >= pages_tile || x.t * kTileKeys + (pg << c.shift) >= x.n) return -1;
+      const int p = paged_page(c, x.r, x.t * kTileKeys + (pg << c.shift), a.status);
+      return p < 0 ? 0 : p;
+    };
+    int page = page_of(w), slot = 0, phase = 0, issued = 0;
+    while (w.left > 0) {
+      Walk nx = w;
+      nx.step(c, a);
+      const int page_n = page_of(nx);  // its load is in flight during the wait
+      const bool ok = __all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]));
+      if (!ok) break;
+      if (lane == 0) {
+        const int keys = min(kTileKeys, w.n - w.t * kTileKeys), np = (keys + c.page - 1) >> c.shift;
+        mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+      }
+      __syncwarp();
+      if (page >= 0)
+        tma_load_4d(ring + slot * Lay::kTile + blk * Lay::kBlock + (pg << c.shift) * 128, map, blk * 64,
+                    a.swap ? w.g : 0, a.swap ? 0 : w.g, page, &full[slot]);
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+      ++issued;
+      w = nx;
+      page = page_n;
+    }
+    // our last copies have landed (bounded) before the CTA may exit
+    if (lane == 0) {
+      for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
+        mbar_wait_bounded(&full[u % kStages], (uint32_t)(u / kStages) & 1u);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc<kHalf>(false, false, 16), id_o = idesc<kHalf>(true, true, kNP);
+      const uint32_t sk0 = smem_u32(smem + Lay::kOffK), sv0 = smem_u32(smem + Lay::kOffV);
+      const uint32_t sq0 = smem_u32(smem + Lay::kOffQ), sp0 = smem_u32(smem + Lay::kOffP);
+      const uint32_t o_col = tmem + 32u;
+      bool ok = true, prev_first = false;
+      int i = 0, seg = 0, ks = 0, kph = 0, vs = 0, vph = 0;
+      // O += V^T P^T over the 128 keys of tile j
+      auto pv = [&](int j, bool fresh, int r) {
+        const int s = j & 1;
+        if (!wait_bar(&ms.p_full[s], (uint32_t)(j >> 1) & 1u, abort, &a.status[r])) return false;
+        if (!wait_bar(&ms.v_full[vs], (uint32_t)vph, abort, &a.status[r])) return false;
+        tc_fence_after();
+        const uint32_t sv = sv0 + (uint32_t)vs * Lay::kTile, sp = sp0 + (uint32_t)s * Lay::kP;
+#pragma unroll
+        for (int x = 0; x < kTileKeys / 16; ++x)
+          mma(o_col, desc(sv + 2048u * x, Lay::kBlock, 1024, 2), desc(sp + 256u * x, 128, kTileKeys * 16, 0), id_o,
+              !(fresh && x == 0));
+        mma_commit(&ms.v_empty[vs]);
+        mma_commit(&ms.pv_done[s]);
+        if (++vs == kStages) {
+          vs = 0;
+          vph ^= 1;
+        }
+        return true;
+      };
+      int prev_r = 0;
+      for (; ok && w.left > 0; w.step(c, a), ++i) {
+        if (w.first) ok = wait_bar(&ms.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u, abort, &a.status[w.r]);
+        ok = ok && wait_bar(&ms.s_free[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, &a.status[w.r]);
+        ok = ok && wait_bar(&ms.k_full[ks], (uint32_t)kph, abort, &a.status[w.r]);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sk = sk0 + (uint32_t)ks * Lay::kTile, sq = sq0 + (uint32_t)(seg & 1) * Lay::kQ;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma(tmem + 16u * (uint32_t)(i & 1), desc(sk + (x >> 2) * Lay::kBlock + (x & 3) * 32u, 16, 1024, 2),
+              desc(sq + (x >> 2) * 2048u + (x & 3) * 32u, 16, 1024, 2), id_s, x > 0);
+        mma_commit(&ms.s_full[i & 1]);
+        mma_commit(&ms.k_empty[ks]);
+        if (++ks == kStages) {
+          ks = 0;
+          kph ^= 1;
+        }
+        if (w.last()) {
+          mma_commit(&ms.q_empty[seg & 1]);
+          ++seg;
+        }
+        if (i > 0) ok = pv(i - 1, prev_first, prev_r);
+        prev_first = w.first;
+        prev_r = w.r;
+      }
+      if (ok && i > 0) pv(i - 1, prev_first, prev_r);
+      // every product that this thread issued has completed (bounded) before the CTA may free its TMEM
+      mma_commit(&ms.mma_done);
+      mbar_wait_bounded(&ms.mma_done, 0);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ queries of each segment; empty requests
+    int seg = 0;
+    for (; w.left > 0; w.step(c, a)) {
+      if (!w.first) continue;
+      const uint16_t *q = a.q + w.r * a.q_st_b + (int64_t)w.g * a.G * D;
+      uint4 v[D / 16];  // 16 rows of D / 8 vectors, 32 lanes
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const int id = lane + 32 * x, h = id / (D / 8), k = id % (D / 8);
+        v[x] = h < a.G ? *reinterpret_cast<const uint4 *>(q + h * D + k * 8) : make_uint4(0, 0, 0, 0);
+      }
+      if (!__all_sync(kFull, wait_bar(&ms.q_empty[seg & 1], ((uint32_t)(seg >> 1) & 1u) ^ 1u, abort, &a.status[w.r])))
+        break;
+      unsigned char *dst = smem + Lay::kOffQ + (seg & 1) * Lay::kQ;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const int id = lane + 32 * x, h = id / (D / 8), k = id % (D / 8);
+        *reinterpret_cast<uint4 *>(dst + (k >> 3) * 2048 + h * 128 + (((k & 7) ^ (h & 7)) << 4)) = v[x];
+      }
+      fence_async_smem();
+      mbar_arrive(&ms.q_full[seg & 1]);
+      ++seg;
+    }
+    for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+      if (clamped_len(c, a, b) > 0) continue;
+      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (size_t)b * a.Hq * D);
+      for (int x = lane; x < a.Hq * D / 8; x += 32) dst[x] = make_uint4(0, 0, 0, 0);
+      for (int h = lane; h < a.Hq; h += 32)
+        if (a.lse) a.lse[(size_t)b * a.Hq + h] = -INFINITY;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and joins
+    const int quad = warp - 4, kt = quad * 32 + lane;  // key of the tile = TMEM lane = element of O
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    float ref[GP], l[GP];
+    bool ok = true;
+    int i = 0, t_first = 0, vs = 0, vph = 0;
+    for (; w.left > 0; w.step(c, a), ++i) {
+      const int s = i & 1;
+      int32_t *st = &a.status[w.r];
+      if (w.first) {
+        t_first = w.t;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          ref[h] = -INFINITY;
+          l[h] = 0.f;
+        }
+      }
+      ok = __all_sync(kFull, ok && wait_bar(&ms.s_full[s], (uint32_t)(i >> 1) & 1u, abort, st));
+      float v[GP];
+      bool over = false;
+      const bool live = w.t * kTileKeys + kt < w.n;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld<GP>(lane_base + 16u * (uint32_t)s, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.s_free[s]);
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          v[h] = live ? v[h] * a.scale_log2 : -INFINITY;
+          over |= v[h] > ref[h] + (kBias + kGrow);
+        }
+        if (a.scores && live) {
+          float *dst = a.scores + (((size_t)w.r * c.Hkv + w.g) * a.tiles_cap + w.t) * a.G * kTileKeys + kt;
+#pragma unroll
+          for (int h = 0; h < GP; ++h)
+            if (h < a.G) dst[h * kTileKeys] = v[h];
+        }
+      }
+      if (vote128(over || !ok)) {
+        if (vote128(!ok)) {
+          ok = false;
+          break;  // all 128 threads
+        }
+        // the tile's maximum of each head; the references that it exceeds move to it
+        float mine_x = 0.f;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          float m = v[h];
+          asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v[h]));
+          if (lane == h) mine_x = m;
+        }
+        if (lane < GP) ms.xm[quad][lane] = mine_x;
+        bar128();
+        float alpha[GP];
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          const float m = fmaxf(fmaxf(ms.xm[0][h], ms.xm[1][h]), fmaxf(ms.xm[2][h], ms.xm[3][h]));
+          alpha[h] = 1.0f;
+          if (m > ref[h] + (kBias + kGrow)) {
+            const float to = m - kBias;
+            if (ref[h] != -INFINITY) {
+              alpha[h] = ex2f(ref[h] - to);
+              moved = true;
+            }
+            ref[h] = to;
+            l[h] *= alpha[h];
+          }
+        }
+        if (moved) {  // the same for all 128 threads; not in a segment's first tile
+          ok = __all_sync(kFull, wait_bar(&ms.pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort, st));
+          if (ok) {
+            tc_fence_after();
+            float o[kNP];
+            tmem_ld<kNP>(lane_base + 32u, o);
+#pragma unroll
+            for (int x = 0; x < kNP; ++x) o[x] *= alpha[x & (GP - 1)];
+            tmem_st<kNP>(lane_base + 32u, o);
+          }
+        }
+      }
+      // weights; P buffer s is free once tile i - 2 is multiplied
+      uint32_t hi[GP / 2], lo[GP / 2];
+#pragma unroll
+      for (int h = 0; h < GP; h += 2) {
+        const float p0 = ex2f(v[h] - (ref[h] == -INFINITY ? 0.f : ref[h]));
+        const float p1 = ex2f(v[h + 1] - (ref[h + 1] == -INFINITY ? 0.f : ref[h + 1]));
+        l[h] += p0;
+        l[h + 1] += p1;
+        split2<kHalf>(p0, p1, hi[h / 2], lo[h / 2]);
+      }
+      if (i >= 2) ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)((i - 2) >> 1) & 1u, abort, st));
+      if (ok) {
+        unsigned char *pb = smem + Lay::kOffP + s * Lay::kP + kt * 16;
+#pragma unroll
+        for (int x = 0; x < GP / 8; ++x) {
+          *reinterpret_cast<uint4 *>(pb + x * (kTileKeys * 16)) =
+              make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+          *reinterpret_cast<uint4 *>(pb + (GP / 8 + x) * (kTileKeys * 16)) =
+              make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+        }
+      }
+      if (w.n - w.t * kTileKeys < kTileKeys) {  // the rows past the end: zeros, whatever the page holds there
+        ok = __all_sync(kFull, ok && wait_bar(&ms.v_full[vs], (uint32_t)vph, abort, st));
+        if (ok && !live) {
+          unsigned char *row = smem + Lay::kOffV + vs * Lay::kTile + kt * 128;
+#pragma unroll
+          for (int x = 0; x < kBlocks * 8; ++x)
+            *reinterpret_cast<uint4 *>(row + (x >> 3) * Lay::kBlock + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (++vs == kStages) {
+        vs = 0;
+        vph ^= 1;
+      }
+      if (ok) {
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&ms.p_full[s]);
+      }
+      if (!w.last()) continue;
+
+      // ---------------------------------------------------------- the segment's end
+      float mine_l = 0.f;
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        float x = l[h];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (lane == h) mine_l = x;
+      }
+      if (lane < GP) ms.xl[quad][lane] = mine_l;
+      ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)(i >> 1) & 1u, abort, st));
+      if (vote128(!ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float o[GP];
+      {
+        float both[kNP];
+        tmem_ld<kNP>(lane_base + 32u, both);
+#pragma unroll
+        for (int h = 0; h < GP; ++h) o[h] = both[h] + both[GP + h];
+      }
+      tc_fence_before();  // the next segment's products overwrite O after this thread's next p_full arrival
+#pragma unroll
+      for (int h = 0; h < GP; ++h) l[h] = (ms.xl[0][h] + ms.xl[1][h]) + (ms.xl[2][h] + ms.xl[3][h]);
+      bool write = t_first == 0 && w.t == w.tiles - 1;
+      if (!write) {
+        // one of several parts of the unit: the last CTA to arrive joins them
+        const long long u0 = f0 + i - w.t, u1 = u0 + w.tiles;
+        const int c0 = (int)(((u0 + 1) * n_cta - 1) / total), c1 = (int)((u1 * n_cta - 1) / total);
+        const int unit = w.r * c.Hkv + w.g;
+        float *part = a.parts + (size_t)(2 * blockIdx.x + (u0 > f0)) * kPartFloats;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          if (h < a.G && kt < D) part[h * D + kt] = o[h];
+          if (kt == h) {
+            part[2048 + h] = ref[h];
+            part[2064 + h] = l[h];
+          }
+        }
+        __threadfence();
+        bar128();
+        if (kt == 0) ms.last = atomicAdd(&a.arrived[unit], 1u) == (uint32_t)(c1 - c0) ? 1u : 0u;
+        bar128();
+        if (ms.last) {
+          __threadfence();
+          if (kt == 0) a.arrived[unit] = 0;
+          float top[GP];
+#pragma unroll
+          for (int h = 0; h < GP; ++h) {
+            top[h] = -INFINITY;
+            o[h] = l[h] = 0.f;
+          }
+          auto part_of = [&](int cta) {
+            return a.parts + (size_t)(2 * cta + (u0 > total * cta / n_cta)) * kPartFloats;
+          };
+          for (int x = c0; x <= c1; ++x) {
+            const float *p = part_of(x) + 2048;
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+              const float m = __ldcg(p + h);
+              top[h] = m > top[h] || m != m ? m : top[h];
+            }
+          }
+          for (int x = c0; x <= c1; ++x) {
+            const float *p = part_of(x);
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+              if (h >= a.G) continue;
+              const float m = __ldcg(p + 2048 + h), f = m == -INFINITY ? 0.f : ex2f(m - top[h]);
+              l[h] += f * __ldcg(p + 2064 + h);
+              if (kt < D) o[h] += f * __ldcg(p + h * D + kt);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < GP; ++h) ref[h] = top[h];
+          write = true;
+        }
+      }
+      if (write) {
+        const size_t row = (size_t)w.r * a.Hq + (size_t)w.g * a.G;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          if (h >= a.G) continue;
+          const bool none = l[h] == 0.f;  // no key with a score above -inf
+          if (kt < D) a.out[(row + h) * D + kt] = to16<kHalf>(none ? 0.f : o[h] / l[h]);
+          if (kt == h) {
+            const float x = none ? -INFINITY : ref[h] + log2f(l[h]);
+            if (a.lse) a.lse[row + h] = x * kLn2;
+            if (a.acc) a.lse2[row + h] = x;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 64;" ::"r"(tmem));
   }
 }
 
@@ -117,14 +764,71 @@ __global__ void __launch_bounds__(256) paged_weights_kernel(Paged c, AttendArgs 
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The driver's tensor-map encoder, looked up once (a function-local static:
+// its initialisation is thread-safe, so concurrent first calls are too).
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+// A pool as (D, slot, head, page), or (D, head, slot, page) where the heads lie
+// closer together; a box is one page of one head, 64 elements wide.
+bool make_map(CUtensorMap *m, const uint16_t *base, const Paged &c, bool swap, bool half) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t slots = (cuuint64_t)c.page, heads = (cuuint64_t)c.Hkv;
+  cuuint64_t dims[4] = {(cuuint64_t)c.D, swap ? heads : slots, swap ? slots : heads, (cuuint64_t)c.n_pages};
+  const cuuint64_t ss = (cuuint64_t)c.st_slot * 2, sh = (cuuint64_t)c.st_head * 2;
+  cuuint64_t strides[3] = {swap ? sh : ss, swap ? ss : sh, (cuuint64_t)c.st_page * 2};
+  cuuint32_t box[4] = {64, swap ? 1u : (cuuint32_t)c.page, swap ? (cuuint32_t)c.page : 1u, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<uint16_t *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kHalf, int D, int GP>
+cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, int grid, const Paged &c, const AttendArgs &a,
+                       cudaStream_t stream) {
+  constexpr uint32_t smem = smem_bytes<D, GP>();
+  const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<kHalf, D, GP>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_attention_kernel<kHalf, D, GP>, dim3((unsigned)grid), dim3(kThreads), smem, stream, mk, mv,
+                    c, a);
+}
+
+template <bool kHalf>
+cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int grid, const Paged &c, const AttendArgs &a,
+                        cudaStream_t stream) {
+  if (c.D == 128)
+    return a.G <= 8 ? launch_one<kHalf, 128, 8>(mk, mv, grid, c, a, stream)
+                    : launch_one<kHalf, 128, 16>(mk, mv, grid, c, a, stream);
+  return a.G <= 8 ? launch_one<kHalf, 64, 8>(mk, mv, grid, c, a, stream)
+                  : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
+}
+
+constexpr size_t kArrivedBytes = kMaxUnits * sizeof(uint32_t);
+constexpr size_t kPartsBytes = (size_t)2 * kMaxGrid * kPartFloats * sizeof(float);
+
 }  // namespace
 
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t cap, int weights) {
+  (void)Hkv;
   (void)D;
-  size_t n = 256;
+  // the counters lie at the same place for every size, so that calls of all sizes share a workspace
+  size_t n = kArrivedBytes + up256(kPartsBytes);
   if (weights) {
     n += up256((size_t)B * Hq * sizeof(float));
-    n += (size_t)B * Hq * ((cap + kTileKeys - 1) / kTileKeys) * kTileKeys * sizeof(float);
+    n += (size_t)B * Hq * (size_t)((cap + kTileKeys - 1) / kTileKeys) * kTileKeys * sizeof(float);
   }
   return n;
 }
@@ -144,11 +848,22 @@ int launch_paged_attention(const Paged &c, bool half, const void *q, int Hq, int
   a.acc = acc;
   a.acc_out = acc_out;
   a.tiles_cap = (c.cap + kTileKeys - 1) / kTileKeys;
-  a.lse2 = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
-  a.scores = acc ? reinterpret_cast<float *>(static_cast<char *>(ws) + 256 + up256((size_t)c.B * Hq * 4)) : nullptr;
+  char *at = static_cast<char *>(ws);
+  a.arrived = reinterpret_cast<uint32_t *>(at);
+  a.parts = reinterpret_cast<float *>(at += kArrivedBytes);
+  a.lse2 = reinterpret_cast<float *>(at += up256(kPartsBytes));
+  a.scores = acc ? reinterpret_cast<float *>(at + up256((size_t)c.B * Hq * 4)) : nullptr;
+  a.swap = c.Hkv > 1 && c.st_head < c.st_slot;
   a.status = status;
-  cudaError_t e = launch_pdl(half ? paged_attention_kernel<true> : paged_attention_kernel<false>,
-                             dim3((unsigned)(c.B * Hq)), dim3(128), 0, stream, c, a);
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, c.k, c, a.swap, half) || !make_map(&mv, c.v, c, a.swap, half)) return BASTION_ERR_LAUNCH;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return BASTION_ERR_LAUNCH;
+  const int64_t most = (int64_t)c.B * c.Hkv * a.tiles_cap;  // tiles, at most
+  const int sm_grid = sms < kMaxGrid ? sms : kMaxGrid, grid = most < sm_grid ? (int)most : sm_grid;
+  cudaError_t e = half ? launch_half<true>(mk, mv, grid, c, a, stream) : launch_half<false>(mk, mv, grid, c, a, stream);
   if (e == cudaSuccess && acc)
     e = launch_pdl(paged_weights_kernel, dim3((unsigned)((c.cap + 255) / 256), (unsigned)(c.B * c.Hkv)), dim3(256), 0,
                    stream, c, a);

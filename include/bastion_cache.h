@@ -110,7 +110,8 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
  * Scores, sums and outputs are accumulated in 32 bits.  Results do not depend
  * on the order in which the parts of a split row finish.
  * Limits: Hq a multiple of Hkv (BASTION_ERR_SIZE), Hq / Hkv <= 16
- * (BASTION_ERR_UNSUPPORTED).
+ * (BASTION_ERR_UNSUPPORTED), B * Hkv * ceil(max_pages * page_size / 128) < 2^31
+ * (BASTION_ERR_SIZE).
  * Workspace: bastion_paged_attention_workspace_bytes(B, Hq, Hkv, D,
  * max_pages * page_size, acc != NULL) bytes.  One launch, two with acc.
  */
