@@ -112,7 +112,9 @@ struct Misc {
 
 template <int D, int GP>
 constexpr uint32_t smem_bytes() {
-  return Layout<D, GP>::kOffMisc + (uint32_t)sizeof(Misc) + 1024;
+  constexpr uint32_t n = Layout<D, GP>::kOffMisc + (uint32_t)sizeof(Misc) + 1024;  // + alignment slack
+  static_assert(n <= 227 * 1024, "shared memory of one CTA");
+  return n;
 }
 
 // --------------------------------------------------------------------------- PTX
@@ -679,42 +681,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             part[2064 + h] = l[h];
           }
         }
-        __threadfence();
         bar128();
-        if (kt == 0) ms.last = atomicAdd(&a.arrived[unit], 1u) == (uint32_t)(c1 - c0) ? 1u : 0u;
+        if (kt == 0) {
+          __threadfence();  // the CTA's part is visible before its arrival
+          const uint32_t last = atomicAdd(&a.arrived[unit], 1u) == (uint32_t)(c1 - c0) ? 1u : 0u;
+          __threadfence();
+          if (last) a.arrived[unit] = 0;
+          ms.last = last;
+        }
         bar128();
         if (ms.last) {
-          __threadfence();
-          if (kt == 0) a.arrived[unit] = 0;
-          float top[GP];
+          // factors 2^(reference - top) of every part and head first (thread: a head of every
+          // kRows-th part), then the parts' O, with the loads of several parts in flight; both
+          // in part order.  The P buffers hold the factors: no product reads them now.
+          constexpr int kRows = 128 / GP;
+          const int np = c1 - c0 + 1, fh = kt & (GP - 1), fy = kt / GP;
+          float *fac = reinterpret_cast<float *>(smem + Lay::kOffP);  // [np][GP]
+          float(*jm)[GP] = reinterpret_cast<float(*)[GP]>(fac + kMaxGrid * GP), (*jl)[GP] = jm + kRows;
+          static_assert((kMaxGrid + 2 * kRows) * GP * 4 <= 2 * Lay::kP, "the factors fit the P buffers");
+          // a CTA's first segment is in its slot 0, a later one in slot 1; only the unit's first
+          // CTA may have begun another unit before
+          const int p0 = 2 * c0 + (u0 > total * c0 / n_cta ? 1 : 0);
+          auto part_of = [&](int x) { return a.parts + (size_t)(x == 0 ? p0 : 2 * (c0 + x)) * kPartFloats; };
+          constexpr int kMine = (kMaxGrid + kRows - 1) / kRows;
+          float pm[kMine], top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int y = 0; y < kMine; ++y) {
+            const int x = fy + y * kRows;
+            if (y * kRows >= np) break;
+            pm[y] = x < np ? __ldcg(part_of(x) + 2048 + fh) : -INFINITY;
+            top = pm[y] > top || pm[y] != pm[y] ? pm[y] : top;
+          }
+          jm[fy][fh] = top;
+          bar128();
+#pragma unroll
+          for (int y = 0; y < kRows; ++y) {
+            const float m = jm[y][fh];
+            top = m > top || m != m ? m : top;
+          }
+#pragma unroll
+          for (int y = 0; y < kMine; ++y) {
+            const int x = fy + y * kRows;
+            if (y * kRows >= np) break;
+            if (x < np) {
+              const float f = pm[y] == -INFINITY ? 0.f : ex2f(pm[y] - top);
+              fac[x * GP + fh] = f;
+              sum += f * __ldcg(part_of(x) + 2064 + fh);
+            }
+          }
+          jl[fy][fh] = sum;
+          if (fy == 0) ms.xm[0][fh] = top;
+          bar128();
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
-            top[h] = -INFINITY;
             o[h] = l[h] = 0.f;
-          }
-          auto part_of = [&](int cta) {
-            return a.parts + (size_t)(2 * cta + (u0 > total * cta / n_cta)) * kPartFloats;
-          };
-          for (int x = c0; x <= c1; ++x) {
-            const float *p = part_of(x) + 2048;
 #pragma unroll
-            for (int h = 0; h < GP; ++h) {
-              const float m = __ldcg(p + h);
-              top[h] = m > top[h] || m != m ? m : top[h];
+            for (int y = 0; y < kRows; ++y) l[h] += jl[y][h];
+            ref[h] = ms.xm[0][h];
+          }
+          if (kt < D) {
+            constexpr int kAhead = GP == 8 ? 4 : 2;
+            for (int x = 0; x < np; x += kAhead) {
+              float in[kAhead][GP];
+#pragma unroll
+              for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+                for (int h = 0; h < GP; ++h)
+                  if (h < a.G) in[y][h] = x + y < np ? __ldcg(part_of(x + y) + h * D + kt) : 0.f;
+#pragma unroll
+              for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+                for (int h = 0; h < GP; ++h)
+                  if (h < a.G && x + y < np) o[h] += fac[(x + y) * GP + h] * in[y][h];
             }
           }
-          for (int x = c0; x <= c1; ++x) {
-            const float *p = part_of(x);
-#pragma unroll
-            for (int h = 0; h < GP; ++h) {
-              if (h >= a.G) continue;
-              const float m = __ldcg(p + 2048 + h), f = m == -INFINITY ? 0.f : ex2f(m - top[h]);
-              l[h] += f * __ldcg(p + 2064 + h);
-              if (kt < D) o[h] += f * __ldcg(p + h * D + kt);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < GP; ++h) ref[h] = top[h];
           write = true;
         }
       }
