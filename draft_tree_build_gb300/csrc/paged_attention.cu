@@ -51,11 +51,13 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kMaxUnits = 65536;  // B * Hkv: arrival counters
-constexpr int kMaxB = 4096;
+constexpr int kMaxB = 1024;
 constexpr int kMaxGrid = 192;     // CTAs that may hold parts
+constexpr int kGroup = 16;        // parts joined at a time
 constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their references and sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
+constexpr int kMinShare = 2;      // tiles
 constexpr float kGrow = 8.0f;     // a score may exceed its head's reference by 2^8
 
 struct AttendArgs {
@@ -68,7 +70,7 @@ struct AttendArgs {
   float *lse;
   const float *acc;
   float *acc_out;
-  uint32_t *arrived;  // [kMaxUnits], zero between calls
+  uint32_t *arrived;  // [2 * kMaxGrid + kMaxUnits], zero between calls
   float *parts;       // [2 * kMaxGrid, kPartFloats]
   float *lse2;        // [B, Hq] base-2 log of the sum, of the scores in base 2
   float *scores;      // [B, Hkv, tiles, G, 128], in base 2
@@ -96,15 +98,15 @@ struct Layout {
   static constexpr uint32_t kOffQ = 2 * kStages * kTile;
   static constexpr uint32_t kOffP = kOffQ + 2 * kQ;
   static constexpr uint32_t kOffList = kOffP + 2 * kP;
-  static constexpr uint32_t kOffMisc = kOffList + kMaxB * 2;
+  static constexpr uint32_t kOffMisc = kOffList + kMaxB * 8;
 };
 
 struct Misc {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_empty[2], mma_done;
-  unsigned long long warp_sum[8];
+  uint2 warp_sum[8];
   float xm[4][16], xl[4][16];
-  int first_rank, off0;
+  int li0, off0, f0, f1;
   uint32_t last;
   uint32_t tmem;
   int abort;
@@ -252,40 +254,96 @@ __device__ __forceinline__ int clamped_len(const Paged &c, const AttendArgs &a, 
 
 // A CTA's tiles, one after the other: tile t of the unit (request r, KV head g).
 struct Walk {
-  const uint16_t *list;  // the share's requests that have tiles
+  const int2 *list;  // the requests that have tiles: number and length
   int li, r, n, tiles, g, t, left;
   bool first;  // the first tile of its segment
-  __device__ __forceinline__ void load(const Paged &c, const AttendArgs &a) {
-    r = list[li];
-    n = clamped_len(c, a, r);
+  __device__ __forceinline__ void load() {
+    const int2 e = list[li];
+    r = e.x;
+    n = e.y;
     tiles = (n + kTileKeys - 1) / kTileKeys;
   }
-  __device__ __forceinline__ void start(const Paged &c, const AttendArgs &a, const uint16_t *l, int off, int count) {
+  __device__ __forceinline__ void start(const int2 *l, int index, int off, int count) {
     list = l;
-    li = 0;
+    li = index;
     left = count;
     first = true;
     if (left > 0) {
-      load(c, a);
+      load();
       g = off / tiles;
       t = off - g * tiles;
     }
   }
-  __device__ __forceinline__ void step(const Paged &c, const AttendArgs &a) {
+  __device__ __forceinline__ void step(int heads) {
     first = false;
     --left;
     if (++t == tiles) {
       t = 0;
       first = true;
-      if (++g == c.Hkv) {
+      if (++g == heads) {
         g = 0;
         ++li;
-        if (left > 0) load(c, a);
+        if (left > 0) load();
       }
     }
   }
   __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == 1; }
 };
+
+// The batch's tiles in equal shares: `big` CTAs of quot + 1 tiles, then shares
+// of quot; a boundary that lies within `snap` tiles of a unit's begin or end
+// moves there (a part that short costs more in the join than it saves).
+struct Shares {
+  int n, quot, big, snap;
+  __device__ __forceinline__ int begin(int cta) const { return cta * quot + min(cta, big); }
+  __device__ __forceinline__ int owner(int f) const {  // the share of tile f, before boundaries move
+    const int edge = big * (quot + 1);
+    return f < edge ? f / (quot + 1) : big + (f - edge) / quot;
+  }
+  // The first and last CTA of a unit of tiles [u0, u1).
+  __device__ __forceinline__ int first_cta(int u0, int u1) const { return owner(min(u0 + snap, u1 - 1)); }
+  __device__ __forceinline__ int last_cta(int u0, int u1) const {
+    return max(first_cta(u0, u1), owner(max(u1 - snap - 1, u0)));
+  }
+};
+
+// Value h of a small array by a thread's own index, without local memory.
+template <int N>
+__device__ __forceinline__ float pick(const float (&x)[N], int h) {
+  float y = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) y = h == i ? x[i] : y;
+  return y;
+}
+
+// Sums of N values over the warp; lane l gets that of value l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&x)[N], int lane) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x[i];
+  int o = 16;
+#pragma unroll
+  for (int m = N / 2; m > 0; m >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float give = up ? v[i] : v[i + m], keep = up ? v[i + m] : v[i];
+      v[i] = keep + __shfl_xor_sync(kFull, give, o);
+    }
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kFull, v[0], o);
+  return v[0];
+}
+
+// Adds 1 to a counter: what the thread (and, before a barrier, its CTA) wrote is
+// visible to whoever sees the sum, and what others wrote before adding to it is to the thread.
+__device__ __forceinline__ uint32_t arrive_gpu(uint32_t *p) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
 
 template <bool kHalf, int D, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -298,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *smem =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Misc &ms = *reinterpret_cast<Misc *>(smem + Lay::kOffMisc);
-  uint16_t *list = reinterpret_cast<uint16_t *>(smem + Lay::kOffList);
+  int2 *list = reinterpret_cast<int2 *>(smem + Lay::kOffList);
   volatile int *abort = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -314,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ms.s_full[s], 1);
       mbar_init(&ms.s_free[s], 4);
-      mbar_init(&ms.p_full[s], 128);
+      mbar_init(&ms.p_full[s], 4);
       mbar_init(&ms.pv_done[s], 1);
-      mbar_init(&ms.q_full[s], 32);
+      mbar_init(&ms.q_full[s], 1);
       mbar_init(&ms.q_empty[s], 1);
     }
     mbar_init(&ms.mma_done, 1);
@@ -331,60 +389,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   // ------------------------------------------------------------ this CTA's share
-  // prefix sums over the requests of (requests with tiles, tiles), 24 and 40 bits
-  const int chunk = (c.B + kThreads - 1) / kThreads, b0 = min(c.B, tid * chunk), b1 = min(c.B, b0 + chunk);
-  unsigned long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = blockIdx.x == 0 ? paged_len(c, a.seq_len, b, a.status) : clamped_len(c, a, b);
-    const int t = (n + kTileKeys - 1) / kTileKeys;
-    mine += (unsigned long long)t | ((unsigned long long)(t > 0) << 40);
+  // prefix sums over the requests of (requests with tiles, tiles); four requests a thread
+  constexpr int kMine = kMaxB / kThreads;
+  int n_req[kMine], cnt = 0, til = 0;
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) {
+    const int b = tid * kMine + x;
+    n_req[x] = b < c.B ? a.seq_len[b] : 0;
+    if (n_req[x] < 0 || n_req[x] > c.cap) {
+      if (blockIdx.x == 0) atomicOr(&a.status[b], BASTION_STATUS_KV_OVERFLOW);
+      n_req[x] = n_req[x] < 0 ? 0 : c.cap;
+    }
+    cnt += n_req[x] > 0;
+    til += (n_req[x] + kTileKeys - 1) / kTileKeys;
   }
-  unsigned long long incl = mine;
+  int cnt_i = cnt, til_i = til;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += y;
+    const int x = __shfl_up_sync(kFull, cnt_i, o), y = __shfl_up_sync(kFull, til_i, o);
+    if (lane >= o) {
+      cnt_i += x;
+      til_i += y;
+    }
   }
-  if (lane == 31) ms.warp_sum[warp] = incl;
+  if (lane == 31) ms.warp_sum[warp] = make_uint2((unsigned)cnt_i, (unsigned)til_i);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  unsigned long long before = incl - mine, all = 0;
+  int rank = cnt_i - cnt, at = til_i - til, total = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) before += ms.warp_sum[w];
-    all += ms.warp_sum[w];
-  }
-  constexpr unsigned long long kLow = (1ull << 40) - 1;
-  const long long total = (long long)(all & kLow) * c.Hkv;
-  const long long n_cta = total < (long long)gridDim.x ? total : (long long)gridDim.x;
-  long long f0 = 0, f1 = 0;
-  if ((long long)blockIdx.x < n_cta) {
-    f0 = total * blockIdx.x / n_cta;
-    f1 = total * (blockIdx.x + 1) / n_cta;
-  }
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {  // find the first request of the share, then list them
-    unsigned long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int t = (clamped_len(c, a, b) + kTileKeys - 1) / kTileKeys;
-      const long long lo = (long long)(at & kLow) * c.Hkv, hi = lo + (long long)t * c.Hkv;
-      const int rank = (int)(at >> 40);
-      if (t > 0 && lo < f1 && hi > f0) {
-        if (pass == 0 && lo <= f0) {
-          ms.first_rank = rank;
-          ms.off0 = (int)(f0 - lo);
-        }
-        if (pass == 1) list[rank - ms.first_rank] = (uint16_t)b;
-      }
-      at += (unsigned long long)t | ((unsigned long long)(t > 0) << 40);
+  for (int x = 0; x < 8; ++x) {
+    const uint2 y = ms.warp_sum[x];
+    if (x < warp) {
+      rank += (int)y.x;
+      at += (int)y.y;
     }
-    __syncthreads();
+    total += (int)y.y;
   }
-  const int share = (int)(f1 - f0);
+  total *= c.Hkv;
+  at *= c.Hkv;
+  Shares sh;
+  sh.n = min((int)gridDim.x, (total + kMinShare - 1) / kMinShare);
+  sh.quot = sh.n > 0 ? total / sh.n : 0;
+  sh.big = total - sh.quot * sh.n;
+  sh.snap = sh.quot >= 3 ? 1 : 0;
+  const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
+  const bool busy = (int)blockIdx.x < sh.n;
+  if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
+  if (busy) {
+#pragma unroll
+    for (int x = 0; x < kMine; ++x) {
+      if (n_req[x] == 0) continue;
+      const int t = (n_req[x] + kTileKeys - 1) / kTileKeys, end = at + t * c.Hkv;
+      list[rank] = make_int2(tid * kMine + x, n_req[x]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // the share's begin and end
+        const int f = k ? b1 : b0;
+        if (f < at || f >= end) continue;
+        const int off = (f - at) % t;
+        const int to = off <= sh.snap ? f - off : t - off <= sh.snap ? f - off + t : f;
+        if (k) {
+          ms.f1 = to;
+        } else {
+          ms.f0 = to;
+          ms.li0 = to == end ? rank + 1 : rank;  // the next request's begin
+          ms.off0 = to == end ? 0 : to - at;
+        }
+      }
+      ++rank;
+      at = end;
+    }
+  }
+  __syncthreads();
+  const int f0 = ms.f0;
   Walk w;
-  w.start(c, a, list, ms.off0, share);
+  w.start(list, ms.li0, ms.off0, busy ? ms.f1 - f0 : 0);
 
   if (warp < 2) {
     // ------------------------------------------------------------ TMA: warp 0 keys, warp 1 values
@@ -392,34 +472,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = warp == 0 ? ms.k_full : ms.v_full, *empty = warp == 0 ? ms.k_empty : ms.v_empty;
     unsigned char *ring = smem + (warp == 0 ? Lay::kOffK : Lay::kOffV);
     const int pages_tile = kTileKeys >> c.shift, blk = lane & (kBlocks - 1), pg = lane / kBlocks;
-    // the page of this lane's box; -1: the tile has no such page
-    auto page_of = [&](const Walk &x) {
-      if (x.left <= 0 || pg >= pages_tile || x.t * kTileKeys + (pg << c.shift) >= x.n) return -1;
-      const int p = paged_page(c, x.r, x.t * kTileKeys + (pg << c.shift), a.status);
-      return p < 0 ? 0 : p;
+    // table entry of this lane's box of a tile; -1: the tile has no such page
+    auto entry_of = [&](const Walk &x) {
+      const int j = x.t * kTileKeys + (pg << c.shift);
+      return x.left > 0 && pg < pages_tile && j < x.n ? c.table[(size_t)x.r * c.max_pages + (j >> c.shift)] : -1;
     };
-    int page = page_of(w), slot = 0, phase = 0, issued = 0;
-    while (w.left > 0) {
-      Walk nx = w;
-      nx.step(c, a);
-      const int page_n = page_of(nx);  // its load is in flight during the wait
-      const bool ok = __all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]));
-      if (!ok) break;
-      if (lane == 0) {
-        const int keys = min(kTileKeys, w.n - w.t * kTileKeys), np = (keys + c.page - 1) >> c.shift;
-        mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+    // entries are read kAhead tiles before their use: the reads' latency never holds up the copies
+    constexpr int kAhead = 3;
+    int entry[kAhead];
+    Walk ahead = w;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      entry[x] = entry_of(ahead);
+      if (ahead.left > 0) ahead.step(c.Hkv);
+    }
+    int slot = 0, phase = 0, issued = 0;
+    bool ok = true;
+    while (ok && w.left > 0) {
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (w.left <= 0) break;
+        int page = entry[x];
+        entry[x] = entry_of(ahead);
+        if (ahead.left > 0) ahead.step(c.Hkv);
+        ok = __all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]));
+        if (!ok) break;
+        const int keys = w.n - w.t * kTileKeys;
+        if (lane == 0) {
+          const int np = (min(kTileKeys, keys) + c.page - 1) >> c.shift;
+          mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+        }
+        __syncwarp();
+        if (pg < pages_tile && (pg << c.shift) < keys) {
+          if (page < 0 || page >= c.n_pages) {
+            atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
+            page = 0;
+          }
+          tma_load_4d(ring + slot * Lay::kTile + blk * Lay::kBlock + (pg << c.shift) * 128, map, blk * 64,
+                      a.swap ? w.g : 0, a.swap ? 0 : w.g, page, &full[slot]);
+        }
+        if (++slot == kStages) {
+          slot = 0;
+          phase ^= 1;
+        }
+        ++issued;
+        w.step(c.Hkv);
       }
-      __syncwarp();
-      if (page >= 0)
-        tma_load_4d(ring + slot * Lay::kTile + blk * Lay::kBlock + (pg << c.shift) * 128, map, blk * 64,
-                    a.swap ? w.g : 0, a.swap ? 0 : w.g, page, &full[slot]);
-      if (++slot == kStages) {
-        slot = 0;
-        phase ^= 1;
-      }
-      ++issued;
-      w = nx;
-      page = page_n;
     }
     // our last copies have landed (bounded) before the CTA may exit
     if (lane == 0) {
@@ -455,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       int prev_r = 0;
-      for (; ok && w.left > 0; w.step(c, a), ++i) {
+      for (; ok && w.left > 0; w.step(c.Hkv), ++i) {
         if (w.first) ok = wait_bar(&ms.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u, abort, &a.status[w.r]);
         ok = ok && wait_bar(&ms.s_free[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, &a.status[w.r]);
         ok = ok && wait_bar(&ms.k_full[ks], (uint32_t)kph, abort, &a.status[w.r]);
@@ -488,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ queries of each segment; empty requests
     int seg = 0;
-    for (; w.left > 0; w.step(c, a)) {
+    for (; w.left > 0; w.step(c.Hkv)) {
       if (!w.first) continue;
       const uint16_t *q = a.q + w.r * a.q_st_b + (int64_t)w.g * a.G * D;
       uint4 v[D / 16];  // 16 rows of D / 8 vectors, 32 lanes
@@ -506,7 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(dst + (k >> 3) * 2048 + h * 128 + (((k & 7) ^ (h & 7)) << 4)) = v[x];
       }
       fence_async_smem();
-      mbar_arrive(&ms.q_full[seg & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.q_full[seg & 1]);
       ++seg;
     }
     for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
@@ -523,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref[GP], l[GP];
     bool ok = true;
     int i = 0, t_first = 0, vs = 0, vph = 0;
-    for (; w.left > 0; w.step(c, a), ++i) {
+    for (; w.left > 0; w.step(c.Hkv), ++i) {
       const int s = i & 1;
       int32_t *st = &a.status[w.r];
       if (w.first) {
@@ -556,21 +655,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h < a.G) dst[h * kTileKeys] = v[h];
         }
       }
-      if (vote128(over || !ok)) {
-        if (vote128(!ok)) {
-          ok = false;
-          break;  // all 128 threads
-        }
+      // a segment's first tile always sets the references
+      if (w.first || vote128(over || !ok)) {
         // the tile's maximum of each head; the references that it exceeds move to it
         float mine_x = 0.f;
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          float m = v[h];
+          float m;
           asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v[h]));
           if (lane == h) mine_x = m;
         }
         if (lane < GP) ms.xm[quad][lane] = mine_x;
-        bar128();
+        if (vote128(!ok)) {
+          ok = false;
+          break;  // all 128 threads
+        }
         float alpha[GP];
         bool moved = false;
 #pragma unroll
@@ -636,20 +735,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         fence_async_smem();
         tc_fence_before();
-        mbar_arrive(&ms.p_full[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full[s]);
       }
       if (!w.last()) continue;
 
       // ---------------------------------------------------------- the segment's end
-      float mine_l = 0.f;
-#pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        float x = l[h];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-        if (lane == h) mine_l = x;
-      }
-      if (lane < GP) ms.xl[quad][lane] = mine_l;
+      const float part_l = warp_sums<GP>(l, lane);
+      if ((lane & (32 / GP - 1)) == 0) ms.xl[quad][lane / (32 / GP)] = part_l;
       ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)(i >> 1) & 1u, abort, st));
       if (vote128(!ok)) {
         ok = false;
@@ -668,108 +761,116 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = 0; h < GP; ++h) l[h] = (ms.xl[0][h] + ms.xl[1][h]) + (ms.xl[2][h] + ms.xl[3][h]);
       bool write = t_first == 0 && w.t == w.tiles - 1;
       if (!write) {
-        // one of several parts of the unit: the last CTA to arrive joins them
-        const long long u0 = f0 + i - w.t, u1 = u0 + w.tiles;
-        const int c0 = (int)(((u0 + 1) * n_cta - 1) / total), c1 = (int)((u1 * n_cta - 1) / total);
-        const int unit = w.r * c.Hkv + w.g;
-        float *part = a.parts + (size_t)(2 * blockIdx.x + (u0 > f0)) * kPartFloats;
+        // One of several parts of the unit.  Parts are joined in groups of kGroup consecutive
+        // CTAs, the groups' results then as parts of their own; each time by whoever arrives
+        // last, in the parts' order.  A CTA's first segment has slot 2 * cta, a later one the
+        // next; only a unit's first CTA can have begun another unit before.
+        const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
+        const int c0 = sh.first_cta(u0, u1), np = sh.last_cta(u0, u1) - c0 + 1;
+        auto slot_of = [&](int x) { return x == 0 ? 2 * c0 + 1 : 2 * (c0 + x); };  // of part x
+        auto put = [&](int slot) {
+          float *part = a.parts + (size_t)slot * kPartFloats;
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          if (h < a.G && kt < D) part[h * D + kt] = o[h];
-          if (kt == h) {
-            part[2048 + h] = ref[h];
-            part[2064 + h] = l[h];
+          for (int h = 0; h < GP; ++h)
+            if (h < a.G && kt < D) part[h * D + kt] = o[h];
+          if (kt < GP) reinterpret_cast<float2 *>(part + 2048)[kt] = make_float2(pick<GP>(ref, kt), pick<GP>(l, kt));
+        };
+        // whether this CTA is the last of `count` to add its part
+        auto arrive = [&](uint32_t *counter, int count) {
+          bar128();
+          if (kt == 0) {
+            const bool last = arrive_gpu(counter) == (uint32_t)(count - 1);
+            if (last) *counter = 0;
+            ms.last = last;
           }
-        }
-        bar128();
-        if (kt == 0) {
-          __threadfence();  // the CTA's part is visible before its arrival
-          const uint32_t last = atomicAdd(&a.arrived[unit], 1u) == (uint32_t)(c1 - c0) ? 1u : 0u;
-          __threadfence();
-          if (last) a.arrived[unit] = 0;
-          ms.last = last;
-        }
-        bar128();
-        if (ms.last) {
-          // factors 2^(reference - top) of every part and head first (thread: a head of every
-          // kRows-th part), then the parts' O, with the loads of several parts in flight; both
-          // in part order.  The P buffers hold the factors: no product reads them now.
-          constexpr int kRows = 128 / GP;
-          const int np = c1 - c0 + 1, fh = kt & (GP - 1), fy = kt / GP;
-          float *fac = reinterpret_cast<float *>(smem + Lay::kOffP);  // [np][GP]
-          float(*jm)[GP] = reinterpret_cast<float(*)[GP]>(fac + kMaxGrid * GP), (*jl)[GP] = jm + kRows;
-          static_assert((kMaxGrid + 2 * kRows) * GP * 4 <= 2 * Lay::kP, "the factors fit the P buffers");
-          // a CTA's first segment is in its slot 0, a later one in slot 1; only the unit's first
-          // CTA may have begun another unit before
-          const int p0 = 2 * c0 + (u0 > total * c0 / n_cta ? 1 : 0);
-          auto part_of = [&](int x) { return a.parts + (size_t)(x == 0 ? p0 : 2 * (c0 + x)) * kPartFloats; };
-          constexpr int kMine = (kMaxGrid + kRows - 1) / kRows;
-          float pm[kMine], top = -INFINITY, sum = 0.f;
+          bar128();
+          return ms.last != 0;
+        };
+        // o, l, ref = parts first, first + step, ... joined
+        auto merge = [&](int first, int step, int count) {
+          constexpr int kLoads = GP == 8 ? 4 : 2, kRows = 128 / GP;  // parts whose loads are in flight together
+          const int fh = kt & (GP - 1), fy = kt / GP;
+          // the parts' references and sums, then their factors; in the P buffers, which no product reads now
+          float2(*jml)[GP] = reinterpret_cast<float2(*)[GP]>(smem + Lay::kOffP);
+          static_assert(kGroup * GP * 8 <= 2 * Lay::kP, "the factors fit the P buffers");
+          float in[kLoads][GP];
+          auto fetch = [&](int y0) {
 #pragma unroll
-          for (int y = 0; y < kMine; ++y) {
-            const int x = fy + y * kRows;
-            if (y * kRows >= np) break;
-            pm[y] = x < np ? __ldcg(part_of(x) + 2048 + fh) : -INFINITY;
-            top = pm[y] > top || pm[y] != pm[y] ? pm[y] : top;
+            for (int y = 0; y < kLoads; ++y) {
+              const float *part = a.parts + (size_t)slot_of(first + min(y0 + y, count - 1) * step) * kPartFloats + kt;
+#pragma unroll
+              for (int h = 0; h < GP; ++h)
+                if (h < a.G && kt < D) in[y][h] = __ldcg(part + h * D);
+            }
+          };
+          float2 ml[kGroup / kRows];
+#pragma unroll
+          for (int k = 0; k < kGroup / kRows; ++k) {
+            const int y = fy + k * kRows;
+            ml[k] = y < count ? __ldcg(reinterpret_cast<const float2 *>(
+                                           a.parts + (size_t)slot_of(first + y * step) * kPartFloats + 2048) + fh)
+                              : make_float2(-INFINITY, 0.f);
           }
-          jm[fy][fh] = top;
+          fetch(0);
+#pragma unroll
+          for (int k = 0; k < kGroup / kRows; ++k) jml[fy + k * kRows][fh] = ml[k];
+          bar128();
+          float top = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < kGroup; ++y) top = fmaxf(top, jml[y][fh].x);
           bar128();
 #pragma unroll
-          for (int y = 0; y < kRows; ++y) {
-            const float m = jm[y][fh];
-            top = m > top || m != m ? m : top;
+          for (int k = 0; k < kGroup / kRows; ++k) {
+            const float f = ml[k].x == -INFINITY ? 0.f : ex2f(ml[k].x - top);
+            jml[fy + k * kRows][fh] = make_float2(f, f * ml[k].y);
           }
-#pragma unroll
-          for (int y = 0; y < kMine; ++y) {
-            const int x = fy + y * kRows;
-            if (y * kRows >= np) break;
-            if (x < np) {
-              const float f = pm[y] == -INFINITY ? 0.f : ex2f(pm[y] - top);
-              fac[x * GP + fh] = f;
-              sum += f * __ldcg(part_of(x) + 2064 + fh);
-            }
-          }
-          jl[fy][fh] = sum;
           if (fy == 0) ms.xm[0][fh] = top;
           bar128();
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
             o[h] = l[h] = 0.f;
-#pragma unroll
-            for (int y = 0; y < kRows; ++y) l[h] += jl[y][h];
             ref[h] = ms.xm[0][h];
           }
-          if (kt < D) {
-            constexpr int kAhead = GP == 8 ? 4 : 2;
-            for (int x = 0; x < np; x += kAhead) {
-              float in[kAhead][GP];
+          for (int y0 = 0; y0 < count; y0 += kLoads) {
 #pragma unroll
-              for (int y = 0; y < kAhead; ++y)
+            for (int y = 0; y < kLoads; ++y) {
+              if (y0 + y >= count) break;
 #pragma unroll
-                for (int h = 0; h < GP; ++h)
-                  if (h < a.G) in[y][h] = x + y < np ? __ldcg(part_of(x + y) + h * D + kt) : 0.f;
-#pragma unroll
-              for (int y = 0; y < kAhead; ++y)
-#pragma unroll
-                for (int h = 0; h < GP; ++h)
-                  if (h < a.G && x + y < np) o[h] += fac[(x + y) * GP + h] * in[y][h];
+              for (int h = 0; h < GP; ++h) {
+                const float2 f = jml[y0 + y][h];
+                l[h] += f.y;
+                if (h < a.G && kt < D) o[h] += f.x * in[y][h];
+              }
+            }
+            if (y0 + kLoads < count) fetch(y0 + kLoads);
+          }
+          bar128();  // jml and xm are read: the next merge or tile may write them
+        };
+        const int x = (int)blockIdx.x - c0, group = x / kGroup, groups = (np + kGroup - 1) / kGroup;
+        put(slot_of(x));
+        const int members = min(kGroup, np - group * kGroup);
+        if (arrive(&a.arrived[slot_of(group * kGroup)], members)) {
+          merge(group * kGroup, 1, members);
+          write = groups == 1;
+          if (!write) {
+            put(slot_of(group * kGroup));
+            if (arrive(&a.arrived[2 * kMaxGrid + w.r * c.Hkv + w.g], groups)) {
+              merge(0, kGroup, groups);
+              write = true;
             }
           }
-          write = true;
         }
       }
       if (write) {
         const size_t row = (size_t)w.r * a.Hq + (size_t)w.g * a.G;
 #pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          if (h >= a.G) continue;
-          const bool none = l[h] == 0.f;  // no key with a score above -inf
-          if (kt < D) a.out[(row + h) * D + kt] = to16<kHalf>(none ? 0.f : o[h] / l[h]);
-          if (kt == h) {
-            const float x = none ? -INFINITY : ref[h] + log2f(l[h]);
-            if (a.lse) a.lse[row + h] = x * kLn2;
-            if (a.acc) a.lse2[row + h] = x;
-          }
+        for (int h = 0; h < GP; ++h)
+          if (h < a.G && kt < D)  // no key with a score above -inf: 0
+            a.out[(row + h) * D + kt] = to16<kHalf>(l[h] == 0.f ? 0.f : __fdividef(o[h], l[h]));
+        if (kt < a.G) {
+          const float lh = pick<GP>(l, kt), x = lh == 0.f ? -INFINITY : pick<GP>(ref, kt) + log2f(lh);
+          if (a.lse) a.lse[row + kt] = x * kLn2;
+          if (a.acc) a.lse2[row + kt] = x;
         }
       }
     }
@@ -856,7 +957,7 @@ cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int grid, 
                   : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
 }
 
-constexpr size_t kArrivedBytes = kMaxUnits * sizeof(uint32_t);
+constexpr size_t kArrivedBytes = (2 * kMaxGrid + kMaxUnits) * sizeof(uint32_t);
 constexpr size_t kPartsBytes = (size_t)2 * kMaxGrid * kPartFloats * sizeof(float);
 
 }  // namespace

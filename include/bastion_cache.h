@@ -28,7 +28,7 @@
  *
  * Limits of every call: dtype BASTION_BF16 or BASTION_F16, D = 64 or 128,
  * page_size a power of two in [8, 128] (BASTION_ERR_UNSUPPORTED otherwise);
- * 1 <= B <= 4096, 1 <= Hkv, B * Hkv <= 65536, n_pages < 2^31,
+ * 1 <= B <= 1024, 1 <= Hkv, B * Hkv <= 65536, n_pages < 2^31,
  * max_pages * page_size <= 2^28; strides of dimensions longer than 1 are
  * multiples of 8 elements and at least D (BASTION_ERR_SIZE otherwise); pools
  * 16-byte aligned.

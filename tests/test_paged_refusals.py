@@ -64,7 +64,7 @@ def _call(b, which, cache=None, **over):
 CACHE_REFUSALS = [
     (dict(k_pool=None), NULL), (dict(v_pool=None), NULL), (dict(page_table=None), NULL),
     (dict(dtype=0), DTYPE), (dict(dtype=7), DTYPE),
-    (dict(B=0), SIZE), (dict(B=4097), SIZE), (dict(Hkv=0), SIZE), (dict(B=4096, Hkv=17), SIZE),
+    (dict(B=0), SIZE), (dict(B=1025), SIZE), (dict(Hkv=0), SIZE), (dict(B=1024, Hkv=65), SIZE),
     (dict(n_pages=0), SIZE), (dict(n_pages=1 << 31), SIZE), (dict(max_pages=0), SIZE),
     (dict(max_pages=(1 << 24) + 1), SIZE), (dict(D=0), SIZE), (dict(page_size=0), SIZE),
     (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED), (dict(page_size=4), UNSUPPORTED),
@@ -109,13 +109,13 @@ def test_call_refusals(b, which, over, code):
 
 def test_workspace_queries(b):
     assert b.bastion_paged_append_workspace_bytes(4) > 0
-    assert b.bastion_paged_append_workspace_bytes(0) == 0 == b.bastion_paged_append_workspace_bytes(4097)
+    assert b.bastion_paged_append_workspace_bytes(0) == 0 == b.bastion_paged_append_workspace_bytes(1025)
     w = b.bastion_paged_attention_workspace_bytes
     assert 0 < w(4, 32, 8, 128, 4096, False) < w(4, 32, 8, 128, 4096, True)
     assert w(4, 33, 8, 128, 4096, False) == w(4, 32, 8, 96, 4096, False) == w(4, 32, 1, 128, 4096, False) == 0
     assert w(4, 32, 8, 128, (1 << 28) + 1, False) == 0
     assert b.bastion_paged_evict_workspace_bytes(4, 8, 4096) > 0
-    assert b.bastion_paged_evict_workspace_bytes(4096, 17, 4096) == 0
+    assert b.bastion_paged_evict_workspace_bytes(1024, 65, 4096) == 0
 
 
 def _tensors(B=2, Hq=8, Hkv=2, D=128, page=16, pages=6, max_pages=3):
