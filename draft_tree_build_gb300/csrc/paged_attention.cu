@@ -137,16 +137,30 @@ __device__ __forceinline__ constexpr uint32_t idesc(bool a_mn, bool b_mn, int n)
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(id), "r"(accum));
+// The instructions that one thread issues are predicated on `one` rather than
+// branched around: the issuing warps stay converged, so that descriptors and
+// addresses live in uniform registers (a tile's 12 products took 2,100 cycles
+// to issue from a branch of one lane).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x;
 }
 
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void mma(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
+                                    uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"(accum), "r"(one));
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -180,12 +194,13 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                            uint64_t *bar) {
+__device__ __forceinline__ void tma_load_4d(uint32_t one, uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      "{\n .reg .pred q;\n setp.ne.b32 q, %7, 0;\n"
+      " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(one)
       : "memory");
 }
 
@@ -259,8 +274,8 @@ struct Walk {
   bool first;  // the first tile of its segment
   __device__ __forceinline__ void load() {
     const int2 e = list[li];
-    r = e.x;
-    n = e.y;
+    r = __shfl_sync(kFull, e.x, 0);  // warp-uniform, and known to be
+    n = __shfl_sync(kFull, e.y, 0);
     tiles = (n + kTileKeys - 1) / kTileKeys;
   }
   __device__ __forceinline__ void start(const int2 *l, int index, int off, int count) {
@@ -316,9 +331,9 @@ __device__ __forceinline__ float pick(const float (&x)[N], int h) {
   return y;
 }
 
-// Sums of N values over the warp; lane l gets that of value l / (32 / N).
-template <int N>
-__device__ __forceinline__ float warp_sums(const float (&x)[N], int lane) {
+// Sums or maxima of N values over the warp; lane l gets that of value l / (32 / N).
+template <int N, bool kMax>
+__device__ __forceinline__ float warp_all(const float (&x)[N], int lane) {
   float v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = x[i];
@@ -329,11 +344,15 @@ __device__ __forceinline__ float warp_sums(const float (&x)[N], int lane) {
 #pragma unroll
     for (int i = 0; i < m; ++i) {
       const float give = up ? v[i] : v[i + m], keep = up ? v[i + m] : v[i];
-      v[i] = keep + __shfl_xor_sync(kFull, give, o);
+      const float got = __shfl_xor_sync(kFull, give, o);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
 #pragma unroll
-  for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kFull, v[0], o);
+  for (; o > 0; o >>= 1) {
+    const float got = __shfl_xor_sync(kFull, v[0], o);
+    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+  }
   return v[0];
 }
 
@@ -464,18 +483,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int f0 = ms.f0;
   Walk w;
-  w.start(list, ms.li0, ms.off0, busy ? ms.f1 - f0 : 0);
+  w.start(list, ms.li0, __shfl_sync(kFull, ms.off0, 0), __shfl_sync(kFull, busy ? ms.f1 - f0 : 0, 0));
 
   if (warp < 2) {
     // ------------------------------------------------------------ TMA: warp 0 keys, warp 1 values
     const CUtensorMap *map = warp == 0 ? &tm_k : &tm_v;
     uint64_t *full = warp == 0 ? ms.k_full : ms.v_full, *empty = warp == 0 ? ms.k_empty : ms.v_empty;
     unsigned char *ring = smem + (warp == 0 ? Lay::kOffK : Lay::kOffV);
-    const int pages_tile = kTileKeys >> c.shift, blk = lane & (kBlocks - 1), pg = lane / kBlocks;
-    // table entry of this lane's box of a tile; -1: the tile has no such page
+    const uint32_t one = elect_one();
+    const int pages_tile = kTileKeys >> c.shift;
+    // lane p: table entry of a tile's page p
     auto entry_of = [&](const Walk &x) {
-      const int j = x.t * kTileKeys + (pg << c.shift);
-      return x.left > 0 && pg < pages_tile && j < x.n ? c.table[(size_t)x.r * c.max_pages + (j >> c.shift)] : -1;
+      const int j = x.t * kTileKeys + (lane << c.shift);
+      return x.left > 0 && lane < pages_tile && j < x.n ? c.table[(size_t)x.r * c.max_pages + (j >> c.shift)] : 0;
     };
     // entries are read kAhead tiles before their use: the reads' latency never holds up the copies
     constexpr int kAhead = 3;
@@ -486,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       entry[x] = entry_of(ahead);
       if (ahead.left > 0) ahead.step(c.Hkv);
     }
+    const uint32_t ring32 = smem_u32(ring), full32 = smem_u32(full);
     int slot = 0, phase = 0, issued = 0;
     bool ok = true;
     while (ok && w.left > 0) {
@@ -495,21 +516,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         int page = entry[x];
         entry[x] = entry_of(ahead);
         if (ahead.left > 0) ahead.step(c.Hkv);
+        if (page < 0 || page >= c.n_pages) {
+          atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
+          page = 0;
+        }
         ok = __all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]));
         if (!ok) break;
-        const int keys = w.n - w.t * kTileKeys;
-        if (lane == 0) {
-          const int np = (min(kTileKeys, keys) + c.page - 1) >> c.shift;
-          mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
-        }
-        __syncwarp();
-        if (pg < pages_tile && (pg << c.shift) < keys) {
-          if (page < 0 || page >= c.n_pages) {
-            atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
-            page = 0;
-          }
-          tma_load_4d(ring + slot * Lay::kTile + blk * Lay::kBlock + (pg << c.shift) * 128, map, blk * 64,
-                      a.swap ? w.g : 0, a.swap ? 0 : w.g, page, &full[slot]);
+        const int np = (min(kTileKeys, w.n - w.t * kTileKeys) + c.page - 1) >> c.shift;
+        if (one) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+        uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
+        const int c1 = a.swap ? w.g : 0, c2 = a.swap ? 0 : w.g;
+        for (int p = 0; p < np; ++p) {
+          const int id = __shfl_sync(kFull, page, p);
+#pragma unroll
+          for (int blk = 0; blk < kBlocks; ++blk)
+            tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot);
+          dst += (uint32_t)(128 << c.shift);
         }
         if (++slot == kStages) {
           slot = 0;
@@ -526,63 +548,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc<kHalf>(false, false, 16), id_o = idesc<kHalf>(true, true, kNP);
-      const uint32_t sk0 = smem_u32(smem + Lay::kOffK), sv0 = smem_u32(smem + Lay::kOffV);
-      const uint32_t sq0 = smem_u32(smem + Lay::kOffQ), sp0 = smem_u32(smem + Lay::kOffP);
-      const uint32_t o_col = tmem + 32u;
-      bool ok = true, prev_first = false;
-      int i = 0, seg = 0, ks = 0, kph = 0, vs = 0, vph = 0;
-      // O += V^T P^T over the 128 keys of tile j
-      auto pv = [&](int j, bool fresh, int r) {
-        const int s = j & 1;
-        if (!wait_bar(&ms.p_full[s], (uint32_t)(j >> 1) & 1u, abort, &a.status[r])) return false;
-        if (!wait_bar(&ms.v_full[vs], (uint32_t)vph, abort, &a.status[r])) return false;
-        tc_fence_after();
-        const uint32_t sv = sv0 + (uint32_t)vs * Lay::kTile, sp = sp0 + (uint32_t)s * Lay::kP;
+    constexpr uint32_t id_s = idesc<kHalf>(false, false, 16), id_o = idesc<kHalf>(true, true, kNP);
+    const uint32_t one = elect_one();
+    // descriptors of the rings' and buffers' first bytes; addresses are added in units of 16 bytes
+    const uint64_t dk = desc(smem_u32(smem + Lay::kOffK), 16, 1024, 2), dq = desc(smem_u32(smem + Lay::kOffQ), 16, 1024, 2);
+    const uint64_t dv = desc(smem_u32(smem + Lay::kOffV), Lay::kBlock, 1024, 2);
+    const uint64_t dp = desc(smem_u32(smem + Lay::kOffP), 128, kTileKeys * 16, 0);
+    const uint32_t o_col = tmem + 32u;
+    bool ok = true, prev_first = false;
+    int i = 0, seg = 0, ks = 0, kph = 0, vs = 0, vph = 0, prev_r = 0;
+    // O += V^T P^T over the 128 keys of tile j
+    auto pv = [&](int j, bool fresh, int r) {
+      const int s = j & 1;
+      if (!__all_sync(kFull, wait_bar(&ms.p_full[s], (uint32_t)(j >> 1) & 1u, abort, &a.status[r]) &&
+                                 wait_bar(&ms.v_full[vs], (uint32_t)vph, abort, &a.status[r])))
+        return false;
+      tc_fence_after();
+      const uint64_t dv_t = dv + (uint32_t)vs * (Lay::kTile >> 4), dp_t = dp + (uint32_t)s * (Lay::kP >> 4);
 #pragma unroll
-        for (int x = 0; x < kTileKeys / 16; ++x)
-          mma(o_col, desc(sv + 2048u * x, Lay::kBlock, 1024, 2), desc(sp + 256u * x, 128, kTileKeys * 16, 0), id_o,
-              !(fresh && x == 0));
-        mma_commit(&ms.v_empty[vs]);
-        mma_commit(&ms.pv_done[s]);
-        if (++vs == kStages) {
-          vs = 0;
-          vph ^= 1;
-        }
-        return true;
-      };
-      int prev_r = 0;
-      for (; ok && w.left > 0; w.step(c.Hkv), ++i) {
-        if (w.first) ok = wait_bar(&ms.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u, abort, &a.status[w.r]);
-        ok = ok && wait_bar(&ms.s_free[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, &a.status[w.r]);
-        ok = ok && wait_bar(&ms.k_full[ks], (uint32_t)kph, abort, &a.status[w.r]);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sk = sk0 + (uint32_t)ks * Lay::kTile, sq = sq0 + (uint32_t)(seg & 1) * Lay::kQ;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          mma(tmem + 16u * (uint32_t)(i & 1), desc(sk + (x >> 2) * Lay::kBlock + (x & 3) * 32u, 16, 1024, 2),
-              desc(sq + (x >> 2) * 2048u + (x & 3) * 32u, 16, 1024, 2), id_s, x > 0);
-        mma_commit(&ms.s_full[i & 1]);
-        mma_commit(&ms.k_empty[ks]);
-        if (++ks == kStages) {
-          ks = 0;
-          kph ^= 1;
-        }
-        if (w.last()) {
-          mma_commit(&ms.q_empty[seg & 1]);
-          ++seg;
-        }
-        if (i > 0) ok = pv(i - 1, prev_first, prev_r);
-        prev_first = w.first;
-        prev_r = w.r;
+      for (int x = 0; x < kTileKeys / 16; ++x)
+        mma(one, o_col, dv_t + 128u * x, dp_t + 16u * x, id_o, x > 0 ? 1u : fresh ? 0u : 1u);
+      mma_commit(one, &ms.pv_done[s]);
+      mma_commit(one, &ms.v_empty[vs]);
+      if (++vs == kStages) {
+        vs = 0;
+        vph ^= 1;
       }
-      if (ok && i > 0) pv(i - 1, prev_first, prev_r);
-      // every product that this thread issued has completed (bounded) before the CTA may free its TMEM
-      mma_commit(&ms.mma_done);
-      mbar_wait_bounded(&ms.mma_done, 0);
+      return true;
+    };
+    for (; ok && w.left > 0; w.step(c.Hkv), ++i) {
+      ok = __all_sync(kFull, (!w.first || wait_bar(&ms.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u, abort, &a.status[w.r])) &&
+                                 wait_bar(&ms.s_free[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, &a.status[w.r]) &&
+                                 wait_bar(&ms.k_full[ks], (uint32_t)kph, abort, &a.status[w.r]));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t dk_t = dk + (uint32_t)ks * (Lay::kTile >> 4), dq_t = dq + (uint32_t)(seg & 1) * (Lay::kQ >> 4);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+        mma(one, tmem + 16u * (uint32_t)(i & 1), dk_t + (x >> 2) * (Lay::kBlock >> 4) + (x & 3) * 2u,
+            dq_t + (x >> 2) * 128u + (x & 3) * 2u, id_s, x > 0);
+      mma_commit(one, &ms.s_full[i & 1]);
+      mma_commit(one, &ms.k_empty[ks]);
+      if (++ks == kStages) {
+        ks = 0;
+        kph ^= 1;
+      }
+      if (w.last()) {
+        mma_commit(one, &ms.q_empty[seg & 1]);
+        ++seg;
+      }
+      if (i > 0) ok = pv(i - 1, prev_first, prev_r);
+      prev_first = w.first;
+      prev_r = w.r;
     }
+    if (ok && i > 0) pv(i - 1, prev_first, prev_r);
+    // every product issued has completed (bounded) before the CTA may free its TMEM
+    mma_commit(one, &ms.mma_done);
+    mbar_wait_bounded(&ms.mma_done, 0);
   } else if (warp == 3) {
     // ------------------------------------------------------------ queries of each segment; empty requests
     int seg = 0;
@@ -658,14 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a segment's first tile always sets the references
       if (w.first || vote128(over || !ok)) {
         // the tile's maximum of each head; the references that it exceeds move to it
-        float mine_x = 0.f;
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          float m;
-          asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v[h]));
-          if (lane == h) mine_x = m;
-        }
-        if (lane < GP) ms.xm[quad][lane] = mine_x;
+        const float top_h = warp_all<GP, true>(v, lane);
+        if ((lane & (32 / GP - 1)) == 0) ms.xm[quad][lane / (32 / GP)] = top_h;
         if (vote128(!ok)) {
           ok = false;
           break;  // all 128 threads
@@ -741,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.last()) continue;
 
       // ---------------------------------------------------------- the segment's end
-      const float part_l = warp_sums<GP>(l, lane);
+      const float part_l = warp_all<GP, false>(l, lane);
       if ((lane & (32 / GP - 1)) == 0) ms.xl[quad][lane / (32 / GP)] = part_l;
       ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)(i >> 1) & 1u, abort, st));
       if (vote128(!ok)) {
