@@ -58,6 +58,7 @@ constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their refere
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
 constexpr int kMinShare = 2;      // tiles
+constexpr int kBatch = 4;         // tiles whose table entries are read together
 constexpr float kGrow = 8.0f;     // a score may exceed its head's reference by 2^8
 
 struct AttendArgs {
@@ -81,7 +82,7 @@ struct AttendArgs {
 
 // --------------------------------------------------------------------------- shared memory
 
-// D elements a head, GP head columns (8 or 16).  The value ring comes first:
+// D elements a head, GP >= G head columns (4, 8 or 16).  The value ring comes first:
 // with D = 64 the transposed value operand has 64 rows, and the M = 128
 // instruction's other 64 rows read the memory one tile further on; those rows
 // of O are never used.
@@ -89,10 +90,11 @@ template <int D, int GP>
 struct Layout {
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kNP = 2 * GP;                              // high and low columns of P
+  static constexpr int kN = kNP < 16 ? 16 : kNP;                  // of the instruction: the rest are zeros
   static constexpr uint32_t kTile = kTileKeys * D * 2;
   static constexpr uint32_t kBlock = kTileKeys * 128;             // 64-element column block of a tile
   static constexpr uint32_t kQ = (D / 64) * 16 * 128;
-  static constexpr uint32_t kP = (kNP / 8) * kTileKeys * 16;
+  static constexpr uint32_t kP = (kN / 8) * kTileKeys * 16;
   static constexpr uint32_t kOffV = 0;
   static constexpr uint32_t kOffK = kStages * kTile;
   static constexpr uint32_t kOffQ = 2 * kStages * kTile;
@@ -171,8 +173,12 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
   uint32_t x[N];
+  if (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(taddr));
 #pragma unroll
-  for (int i = 0; i < N; i += 8)
+  for (int i = 0; i + 8 <= N; i += 8)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]),
                    "=r"(x[i + 6]), "=r"(x[i + 7])
@@ -222,9 +228,9 @@ __device__ __forceinline__ bool vote128(bool x) {
 }
 __device__ __forceinline__ void bar128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Bounded wait that also honours the CTA's abort flag.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait that also honours the CTA's abort flag.  The loop is kept out of
+// line: the roles' loops compete for the instruction cache.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
   const uint64_t t0 = global_ns();
   uint32_t spins = 0;
   while (!mbar_try_wait(bar, parity)) {
@@ -238,6 +244,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     }
   }
   return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, status);
 }
 
 // p as two 16-bit terms: hi = round(p), lo = round(p - hi), two heads a word.
@@ -268,14 +277,16 @@ __device__ __forceinline__ int clamped_len(const Paged &c, const AttendArgs &a, 
 }
 
 // A CTA's tiles, one after the other: tile t of the unit (request r, KV head g).
+// kUniform: all lanes of a warp walk together, and the compiler is told so.
+template <bool kUniform>
 struct Walk {
   const int2 *list;  // the requests that have tiles: number and length
   int li, r, n, tiles, g, t, left;
   bool first;  // the first tile of its segment
   __device__ __forceinline__ void load() {
     const int2 e = list[li];
-    r = __shfl_sync(kFull, e.x, 0);  // warp-uniform, and known to be
-    n = __shfl_sync(kFull, e.y, 0);
+    r = kUniform ? __shfl_sync(kFull, e.x, 0) : e.x;
+    n = kUniform ? __shfl_sync(kFull, e.y, 0) : e.y;
     tiles = (n + kTileKeys - 1) / kTileKeys;
   }
   __device__ __forceinline__ void start(const int2 *l, int index, int off, int count) {
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Paged c,
                            AttendArgs a) {
   using Lay = Layout<D, GP>;
-  constexpr int kStages = Lay::kStages, kNP = Lay::kNP, kBlocks = D / 64;
+  constexpr int kStages = Lay::kStages, kNP = Lay::kNP, kN = Lay::kN, kBlocks = D / 64;
   constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem =
@@ -408,19 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   // ------------------------------------------------------------ this CTA's share
-  // prefix sums over the requests of (requests with tiles, tiles); four requests a thread
-  constexpr int kMine = kMaxB / kThreads;
-  int n_req[kMine], cnt = 0, til = 0;
-#pragma unroll
-  for (int x = 0; x < kMine; ++x) {
-    const int b = tid * kMine + x;
-    n_req[x] = b < c.B ? a.seq_len[b] : 0;
-    if (n_req[x] < 0 || n_req[x] > c.cap) {
-      if (blockIdx.x == 0) atomicOr(&a.status[b], BASTION_STATUS_KV_OVERFLOW);
-      n_req[x] = n_req[x] < 0 ? 0 : c.cap;
-    }
-    cnt += n_req[x] > 0;
-    til += (n_req[x] + kTileKeys - 1) / kTileKeys;
+  // prefix sums over the requests of (requests with tiles, tiles); a thread has consecutive requests
+  const int chunk = (c.B + kThreads - 1) / kThreads, r0 = tid * chunk, r1 = min(c.B, r0 + chunk);
+  int cnt = 0, til = 0;
+#pragma unroll 1
+  for (int b = r0; b < r1; ++b) {
+    const int n = a.seq_len[b];
+    if ((n < 0 || n > c.cap) && blockIdx.x == 0) atomicOr(&a.status[b], BASTION_STATUS_KV_OVERFLOW);
+    const int m = min(max(n, 0), c.cap);
+    cnt += m > 0;
+    til += (m + kTileKeys - 1) / kTileKeys;
   }
   int cnt_i = cnt, til_i = til;
 #pragma unroll
@@ -457,12 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool busy = (int)blockIdx.x < sh.n;
   if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
   if (busy) {
-#pragma unroll
-    for (int x = 0; x < kMine; ++x) {
-      if (n_req[x] == 0) continue;
-      const int t = (n_req[x] + kTileKeys - 1) / kTileKeys, end = at + t * c.Hkv;
-      list[rank] = make_int2(tid * kMine + x, n_req[x]);
-#pragma unroll
+#pragma unroll 1
+    for (int b = r0; b < r1; ++b) {
+      const int n = clamped_len(c, a, b), t = (n + kTileKeys - 1) / kTileKeys, end = at + t * c.Hkv;
+      if (n == 0) continue;
+      list[rank] = make_int2(b, n);
+#pragma unroll 1
       for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int f0 = ms.f0;
-  Walk w;
+  Walk<true> w;
   w.start(list, ms.li0, __shfl_sync(kFull, ms.off0, 0), __shfl_sync(kFull, busy ? ms.f1 - f0 : 0, 0));
 
   if (warp < 2) {
@@ -491,55 +499,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = warp == 0 ? ms.k_full : ms.v_full, *empty = warp == 0 ? ms.k_empty : ms.v_empty;
     unsigned char *ring = smem + (warp == 0 ? Lay::kOffK : Lay::kOffV);
     const uint32_t one = elect_one();
-    const int pages_tile = kTileKeys >> c.shift;
-    // lane p: table entry of a tile's page p
-    auto entry_of = [&](const Walk &x) {
-      const int j = x.t * kTileKeys + (lane << c.shift);
-      return x.left > 0 && lane < pages_tile && j < x.n ? c.table[(size_t)x.r * c.max_pages + (j >> c.shift)] : 0;
+    // Table entries are read in batches of kBatch tiles, a batch ahead of their use, so that the
+    // reads' latency never holds up the copies.  Lane: page lane % ppt of the batch's tile lane / ppt.
+    const int psh = 7 - c.shift, ppt = 1 << psh, batch = min(kBatch, 32 >> psh);
+    Walk<false> lw;  // this lane's tile
+    lw.start(list, ms.li0, ms.off0, w.left);
+    int lead = lane >> psh;
+    auto next_entry = [&]() {  // walks on by `lead` tiles and reads there
+#pragma unroll 1
+      for (int x = 0; x < lead && lw.left > 0; ++x) lw.step(c.Hkv);
+      lead = batch;
+      const int pg = (lw.t << psh) + (lane & (ppt - 1));
+      const bool on = (lane >> psh) < batch && lw.left > 0 && (pg << c.shift) < lw.n;
+      const int e = on ? c.table[(size_t)lw.r * c.max_pages + pg] : 0;
+      __syncwarp();
+      return e;
     };
-    // entries are read kAhead tiles before their use: the reads' latency never holds up the copies
-    constexpr int kAhead = 3;
-    int entry[kAhead];
-    Walk ahead = w;
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      entry[x] = entry_of(ahead);
-      if (ahead.left > 0) ahead.step(c.Hkv);
-    }
+    int entry = next_entry(), entry_n = next_entry(), in_batch = 0;
     const uint32_t ring32 = smem_u32(ring), full32 = smem_u32(full);
     int slot = 0, phase = 0, issued = 0;
-    bool ok = true;
-    while (ok && w.left > 0) {
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        if (w.left <= 0) break;
-        int page = entry[x];
-        entry[x] = entry_of(ahead);
-        if (ahead.left > 0) ahead.step(c.Hkv);
-        if (page < 0 || page >= c.n_pages) {
-          atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
-          page = 0;
-        }
-        ok = __all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]));
-        if (!ok) break;
-        const int np = (min(kTileKeys, w.n - w.t * kTileKeys) + c.page - 1) >> c.shift;
-        if (one) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
-        uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
-        const int c1 = a.swap ? w.g : 0, c2 = a.swap ? 0 : w.g;
-        for (int p = 0; p < np; ++p) {
-          const int id = __shfl_sync(kFull, page, p);
-#pragma unroll
-          for (int blk = 0; blk < kBlocks; ++blk)
-            tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot);
-          dst += (uint32_t)(128 << c.shift);
-        }
-        if (++slot == kStages) {
-          slot = 0;
-          phase ^= 1;
-        }
-        ++issued;
-        w.step(c.Hkv);
+#pragma unroll 1
+    for (; w.left > 0; w.step(c.Hkv)) {
+      if (in_batch == batch) {
+        entry = entry_n;
+        entry_n = next_entry();
+        in_batch = 0;
       }
+      if (!__all_sync(kFull, wait_bar(&empty[slot], phase ^ 1, abort, &a.status[w.r]))) break;
+      const int np = (min(kTileKeys, w.n - w.t * kTileKeys) + c.page - 1) >> c.shift;
+      if (one) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+      uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
+      const int c1 = a.swap ? w.g : 0, c2 = a.swap ? 0 : w.g;
+#pragma unroll 1
+      for (int p = 0; p < np; ++p) {
+        int id = __shfl_sync(kFull, entry, (in_batch << psh) + p);
+        if (id < 0 || id >= c.n_pages) {
+          atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
+          id = 0;
+        }
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+          tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot);
+        dst += (uint32_t)(128 << c.shift);
+      }
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
+      ++issued;
+      ++in_batch;
     }
     // our last copies have landed (bounded) before the CTA may exit
     if (lane == 0) {
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ products
-    constexpr uint32_t id_s = idesc<kHalf>(false, false, 16), id_o = idesc<kHalf>(true, true, kNP);
+    constexpr uint32_t id_s = idesc<kHalf>(false, false, 16), id_o = idesc<kHalf>(true, true, kN);
     const uint32_t one = elect_one();
     // descriptors of the rings' and buffers' first bytes; addresses are added in units of 16 bytes
     const uint64_t dk = desc(smem_u32(smem + Lay::kOffK), 16, 1024, 2), dq = desc(smem_u32(smem + Lay::kOffQ), 16, 1024, 2);
@@ -642,6 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp - 4, kt = quad * 32 + lane;  // key of the tile = TMEM lane = element of O
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     float ref[GP], l[GP];
+    if (kN > kNP) {  // the columns of P that no head uses
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        *reinterpret_cast<uint4 *>(smem + Lay::kOffP + x * Lay::kP + kTileKeys * 16 + kt * 16) = make_uint4(0, 0, 0, 0);
+    }
     bool ok = true;
     int i = 0, t_first = 0, vs = 0, vph = 0;
     for (; w.left > 0; w.step(c.Hkv), ++i) {
@@ -691,16 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
           const float m = fmaxf(fmaxf(ms.xm[0][h], ms.xm[1][h]), fmaxf(ms.xm[2][h], ms.xm[3][h]));
-          alpha[h] = 1.0f;
-          if (m > ref[h] + (kBias + kGrow)) {
-            const float to = m - kBias;
-            if (ref[h] != -INFINITY) {
-              alpha[h] = ex2f(ref[h] - to);
-              moved = true;
-            }
-            ref[h] = to;
-            l[h] *= alpha[h];
-          }
+          const bool grow = m > ref[h] + (kBias + kGrow);
+          const float to = grow ? m - kBias : ref[h];
+          alpha[h] = grow ? ex2f(ref[h] - to) : 1.0f;  // 0 for a head that had no finite score: its l and O are 0
+          moved |= grow && !w.first;
+          ref[h] = to;
+          l[h] *= alpha[h];
         }
         if (moved) {  // the same for all 128 threads; not in a segment's first tile
           ok = __all_sync(kFull, wait_bar(&ms.pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort, st));
@@ -727,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= 2) ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)((i - 2) >> 1) & 1u, abort, st));
       if (ok) {
         unsigned char *pb = smem + Lay::kOffP + s * Lay::kP + kt * 16;
+        if (GP == 4) *reinterpret_cast<uint4 *>(pb) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
 #pragma unroll
         for (int x = 0; x < GP / 8; ++x) {
           *reinterpret_cast<uint4 *>(pb + x * (kTileKeys * 16)) =
@@ -791,24 +801,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h < a.G && kt < D) part[h * D + kt] = o[h];
           if (kt < GP) reinterpret_cast<float2 *>(part + 2048)[kt] = make_float2(pick<GP>(ref, kt), pick<GP>(l, kt));
         };
-        // whether this CTA is the last of `count` to add its part
-        auto arrive = [&](uint32_t *counter, int count) {
+        const int x = (int)blockIdx.x - c0, groups = (np + kGroup - 1) / kGroup;
+        int first = x / kGroup * kGroup, step = 1, count = min(kGroup, np - first), slot = slot_of(x);
+        uint32_t *counter = &a.arrived[slot_of(first)];
+#pragma unroll 1
+        for (;;) {
+          put(slot);
           bar128();
           if (kt == 0) {
-            const bool last = arrive_gpu(counter) == (uint32_t)(count - 1);
-            if (last) *counter = 0;
-            ms.last = last;
+            const bool is_last = arrive_gpu(counter) == (uint32_t)(count - 1);
+            if (is_last) *counter = 0;
+            ms.last = is_last;
           }
           bar128();
-          return ms.last != 0;
-        };
-        // o, l, ref = parts first, first + step, ... joined
-        auto merge = [&](int first, int step, int count) {
-          constexpr int kLoads = GP == 8 ? 4 : 2, kRows = 128 / GP;  // parts whose loads are in flight together
+          if (!ms.last) break;
+          // o, l, ref = parts first, first + step, ... joined
+          constexpr int kLoads = 32 / GP, kRows = 128 / GP;  // parts whose loads are in flight together
           const int fh = kt & (GP - 1), fy = kt / GP;
           // the parts' references and sums, then their factors; in the P buffers, which no product reads now
           float2(*jml)[GP] = reinterpret_cast<float2(*)[GP]>(smem + Lay::kOffP);
-          static_assert(kGroup * GP * 8 <= 2 * Lay::kP, "the factors fit the P buffers");
+          static_assert(kGroup * GP * 8 <= kTileKeys * 16, "the factors fit the P buffers");
           float in[kLoads][GP];
           auto fetch = [&](int y0) {
 #pragma unroll
@@ -819,9 +831,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (h < a.G && kt < D) in[y][h] = __ldcg(part + h * D);
             }
           };
-          float2 ml[kGroup / kRows];
+          constexpr int kMl = (kGroup + kRows - 1) / kRows;
+          float2 ml[kMl];
 #pragma unroll
-          for (int k = 0; k < kGroup / kRows; ++k) {
+          for (int k = 0; k < kMl; ++k) {
             const int y = fy + k * kRows;
             ml[k] = y < count ? __ldcg(reinterpret_cast<const float2 *>(
                                            a.parts + (size_t)slot_of(first + y * step) * kPartFloats + 2048) + fh)
@@ -829,16 +842,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fetch(0);
 #pragma unroll
-          for (int k = 0; k < kGroup / kRows; ++k) jml[fy + k * kRows][fh] = ml[k];
+          for (int k = 0; k < kMl; ++k)
+            if (fy + k * kRows < kGroup) jml[fy + k * kRows][fh] = ml[k];
           bar128();
           float top = -INFINITY;
 #pragma unroll
           for (int y = 0; y < kGroup; ++y) top = fmaxf(top, jml[y][fh].x);
           bar128();
 #pragma unroll
-          for (int k = 0; k < kGroup / kRows; ++k) {
+          for (int k = 0; k < kMl; ++k) {
             const float f = ml[k].x == -INFINITY ? 0.f : ex2f(ml[k].x - top);
-            jml[fy + k * kRows][fh] = make_float2(f, f * ml[k].y);
+            if (fy + k * kRows < kGroup) jml[fy + k * kRows][fh] = make_float2(f, f * ml[k].y);
           }
           if (fy == 0) ms.xm[0][fh] = top;
           bar128();
@@ -860,21 +874,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (y0 + kLoads < count) fetch(y0 + kLoads);
           }
-          bar128();  // jml and xm are read: the next merge or tile may write them
-        };
-        const int x = (int)blockIdx.x - c0, group = x / kGroup, groups = (np + kGroup - 1) / kGroup;
-        put(slot_of(x));
-        const int members = min(kGroup, np - group * kGroup);
-        if (arrive(&a.arrived[slot_of(group * kGroup)], members)) {
-          merge(group * kGroup, 1, members);
-          write = groups == 1;
-          if (!write) {
-            put(slot_of(group * kGroup));
-            if (arrive(&a.arrived[2 * kMaxGrid + w.r * c.Hkv + w.g], groups)) {
-              merge(0, kGroup, groups);
-              write = true;
-            }
+          bar128();  // jml and xm are read: the next round or tile may write them
+          if (step > 1 || groups == 1) {
+            write = true;
+            break;
           }
+          slot = slot_of(first);  // the group's result takes its first part's place
+          first = 0;
+          step = kGroup;
+          count = groups;
+          counter = &a.arrived[2 * kMaxGrid + w.r * c.Hkv + w.g];
         }
       }
       if (write) {
@@ -967,10 +976,12 @@ template <bool kHalf>
 cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int grid, const Paged &c, const AttendArgs &a,
                         cudaStream_t stream) {
   if (c.D == 128)
-    return a.G <= 8 ? launch_one<kHalf, 128, 8>(mk, mv, grid, c, a, stream)
-                    : launch_one<kHalf, 128, 16>(mk, mv, grid, c, a, stream);
-  return a.G <= 8 ? launch_one<kHalf, 64, 8>(mk, mv, grid, c, a, stream)
-                  : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
+    return a.G <= 4   ? launch_one<kHalf, 128, 4>(mk, mv, grid, c, a, stream)
+           : a.G <= 8 ? launch_one<kHalf, 128, 8>(mk, mv, grid, c, a, stream)
+                      : launch_one<kHalf, 128, 16>(mk, mv, grid, c, a, stream);
+  return a.G <= 4   ? launch_one<kHalf, 64, 4>(mk, mv, grid, c, a, stream)
+         : a.G <= 8 ? launch_one<kHalf, 64, 8>(mk, mv, grid, c, a, stream)
+                    : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
 }
 
 constexpr size_t kArrivedBytes = (2 * kMaxGrid + kMaxUnits) * sizeof(uint32_t);
