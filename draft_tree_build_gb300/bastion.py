@@ -359,48 +359,50 @@ def bastion_verify_greedy_noalloc(target_logits, b, n_nodes, parent, token, argm
 
 # --------------------------------------------------------------------------- paged cache
 
+# These calls take a few microseconds on the GPU, so that what the host spends on one counts: the checks below
+# compare integers and shapes without building new objects.
+
 _CACHE_DTYPES = {torch.bfloat16: BASTION_BF16, torch.float16: BASTION_F16}
 
 
 def _need(name, t, dtype, shape):
     """A contiguous tensor of that type and shape (the library reads its bytes as such)."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise BastionError(f"paged cache: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
                            f"{list(t.shape)}, strides {t.stride()}")
 
 
 def _on_device(workspace, *tensors):
-    """All on the current CUDA device: the launches go there."""
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    """All on the current CUDA device, where the launches go."""
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace)")
-    dev = workspace.device
-    if dev.type != "cuda":
+    dev = workspace.get_device()
+    if dev < 0:
         raise BastionError("tensor must live on a CUDA device")
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise BastionError(f"paged cache: tensors on {t.device} and {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise BastionError(f"paged cache: the tensors are on {dev}, the current device is "
+        if t is not None and t.get_device() != dev:
+            raise BastionError(f"paged cache: tensors on {t.device} and {workspace.device}")
+    if dev != torch.cuda.current_device():
+        raise BastionError(f"paged cache: the tensors are on {workspace.device}, the current device is "
                            f"cuda:{torch.cuda.current_device()}")
 
 
 def _cache(k_pool, v_pool, page_table):
     """The cache's struct; pools [n_pages, page_size, Hkv, D] of any strides (a head-major pool is a
     transposed view), page_table [B, max_pages] int32."""
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
+    shape, st = k_pool.shape, k_pool.stride()
+    if len(shape) != 4 or shape != v_pool.shape or k_pool.dtype is not v_pool.dtype:
         raise BastionError("paged cache: the pools must be [n_pages, page_size, Hkv, D], of one shape and dtype")
     dt = _CACHE_DTYPES.get(k_pool.dtype)
     if dt is None:
         raise BastionError(f"paged cache: the pools must be bfloat16 or float16, got {k_pool.dtype}")
-    shape, st = k_pool.shape, k_pool.stride()
     if st[3] != 1 or st != v_pool.stride():
         raise BastionError("paged cache: the pools must have equal strides and a contiguous last dimension")
-    if page_table.dim() != 2:
-        raise BastionError("paged cache: page_table must be [B, max_pages]")
-    _need("page_table", page_table, torch.int32, tuple(page_table.shape))
+    table = page_table.shape
+    if len(table) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
+        raise BastionError("paged cache: page_table must be contiguous int32 [B, max_pages]")
     return _PagedCacheStruct(k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2],
-                             page_table.data_ptr(), dt, page_table.shape[0], shape[2], shape[3], shape[1],
-                             page_table.shape[1])
+                             page_table.data_ptr(), dt, table[0], shape[2], shape[3], shape[1], table[1])
 
 
 def _ptr(t):

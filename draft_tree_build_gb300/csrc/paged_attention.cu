@@ -57,7 +57,6 @@ constexpr int kGroup = 16;        // parts joined at a time
 constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their references and sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
-constexpr int kMinShare = 2;      // tiles
 constexpr int kBatch = 4;         // tiles whose table entries are read together
 constexpr float kGrow = 8.0f;     // a score may exceed its head's reference by 2^8
 
@@ -317,20 +316,27 @@ struct Walk {
 };
 
 // The batch's tiles in equal shares: `big` CTAs of quot + 1 tiles, then shares
-// of quot; a boundary that lies within `snap` tiles of a unit's begin or end
-// moves there (a part that short costs more in the join than it saves).
+// of quot.  A boundary moves to a unit's begin or end where cutting the unit
+// costs more in the join (1.4 us) than it saves: from anywhere in a unit of at
+// most kWhole tiles to the nearer end, and from within kSnap tiles of the ends
+// of a longer one.  Shares may become empty.  (8 units of 3 tiles: 6.6 us whole,
+// 9.9 us cut; 8 of 8 tiles: 8.0 us cut.)
+constexpr int kWhole = 4, kSnap = 1;
 struct Shares {
-  int n, quot, big, snap;
+  int n, quot, big;
   __device__ __forceinline__ int begin(int cta) const { return cta * quot + min(cta, big); }
   __device__ __forceinline__ int owner(int f) const {  // the share of tile f, before boundaries move
     const int edge = big * (quot + 1);
     return f < edge ? f / (quot + 1) : big + (f - edge) / quot;
   }
-  // The first and last CTA of a unit of tiles [u0, u1).
-  __device__ __forceinline__ int first_cta(int u0, int u1) const { return owner(min(u0 + snap, u1 - 1)); }
-  __device__ __forceinline__ int last_cta(int u0, int u1) const {
-    return max(first_cta(u0, u1), owner(max(u1 - snap - 1, u0)));
+  // Where boundary f moves to; unit of t tiles, off = f - its begin.
+  static __device__ __forceinline__ int moved(int f, int off, int t) {
+    if (t <= kWhole) return 2 * off <= t ? f - off : f - off + t;
+    return off <= kSnap ? f - off : t - off <= kSnap ? f - off + t : f;
   }
+  // The first and last CTA of a cut unit of tiles [u0, u1).
+  __device__ __forceinline__ int first_cta(int u0) const { return owner(u0 + kSnap); }
+  __device__ __forceinline__ int last_cta(int u1) const { return owner(u1 - kSnap - 1); }
 };
 
 // Value h of a small array by a thread's own index, without local memory.
@@ -457,10 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   total *= c.Hkv;
   at *= c.Hkv;
   Shares sh;
-  sh.n = min((int)gridDim.x, (total + kMinShare - 1) / kMinShare);
+  sh.n = min((int)gridDim.x, total);
   sh.quot = sh.n > 0 ? total / sh.n : 0;
   sh.big = total - sh.quot * sh.n;
-  sh.snap = sh.quot >= 3 ? 1 : 0;
   const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
   const bool busy = (int)blockIdx.x < sh.n;
   if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
@@ -474,8 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
-        const int off = (f - at) % t;
-        const int to = off <= sh.snap ? f - off : t - off <= sh.snap ? f - off + t : f;
+        // (f - at) % t: the quotient is below Hkv <= 2^16, so that its estimate is off by one at most
+        int off = f - at - (int)(__fdividef((float)(f - at), (float)t)) * t;
+        off += off < 0 ? t : off >= t ? -t : 0;
+        const int to = Shares::moved(f, off, t);
         if (k) {
           ms.f1 = to;
         } else {
@@ -515,13 +522,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       return e;
     };
-    int entry = next_entry(), entry_n = next_entry(), in_batch = 0;
+    int entry = 0, entry_n = next_entry(), in_batch = batch;
     const uint32_t ring32 = smem_u32(ring), full32 = smem_u32(full);
     int slot = 0, phase = 0, issued = 0;
 #pragma unroll 1
     for (; w.left > 0; w.step(c.Hkv)) {
       if (in_batch == batch) {
         entry = entry_n;
+        if (entry < 0 || entry >= c.n_pages) {  // no page of the pool: page 0 stands in
+          atomicOr(&a.status[lw.r], BASTION_STATUS_BAD_PAGE);
+          entry = 0;
+        }
         entry_n = next_entry();
         in_batch = 0;
       }
@@ -530,13 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (one) mbar_arrive_expect_tx(&full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
       uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
       const int c1 = a.swap ? w.g : 0, c2 = a.swap ? 0 : w.g;
-#pragma unroll 1
+#pragma unroll 4
       for (int p = 0; p < np; ++p) {
-        int id = __shfl_sync(kFull, entry, (in_batch << psh) + p);
-        if (id < 0 || id >= c.n_pages) {
-          atomicOr(&a.status[w.r], BASTION_STATUS_BAD_PAGE);
-          id = 0;
-        }
+        const int id = __shfl_sync(kFull, entry, (in_batch << psh) + p);
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
           tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot);
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // last, in the parts' order.  A CTA's first segment has slot 2 * cta, a later one the
         // next; only a unit's first CTA can have begun another unit before.
         const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
-        const int c0 = sh.first_cta(u0, u1), np = sh.last_cta(u0, u1) - c0 + 1;
+        const int c0 = sh.first_cta(u0), np = sh.last_cta(u1) - c0 + 1;
         auto slot_of = [&](int x) { return x == 0 ? 2 * c0 + 1 : 2 * (c0 + x); };  // of part x
         auto put = [&](int slot) {
           float *part = a.parts + (size_t)slot * kPartFloats;
