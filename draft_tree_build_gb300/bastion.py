@@ -372,8 +372,15 @@ def _need(name, t, dtype, shape):
                            f"{list(t.shape)}, strides {t.stride()}")
 
 
-def _on_device(workspace, *tensors):
-    """All on the current CUDA device, where the launches go."""
+def _need_all(names, tensors, dtype, shape):
+    """_need for several tensors (None: left out) of one type and shape; names: a text, split when one fails."""
+    for i, t in enumerate(tensors):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            _need(names.split()[i], t, dtype, shape)
+
+
+def _on_device(stream, workspace, *tensors):
+    """All on the current CUDA device, where the launches go; the handle of the stream to launch on."""
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace)")
     dev = workspace.get_device()
@@ -385,6 +392,8 @@ def _on_device(workspace, *tensors):
     if dev != torch.cuda.current_device():
         raise BastionError(f"paged cache: the tensors are on {workspace.device}, the current device is "
                            f"cuda:{torch.cuda.current_device()}")
+    # the current stream's handle without a Stream object, which costs 3 us to make
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _cache(k_pool, v_pool, page_table):
@@ -420,32 +429,30 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     seq_len_out may be seq_len, n_seen_out n_seen."""
     c = _cache(k_pool, v_pool, page_table)
     B, cap = c.B, c.max_pages * c.page_size
-    if k_new.dim() != 4 or k_new.shape != v_new.shape or tuple(k_new.shape[::2]) != (B, c.Hkv) \
-            or k_new.shape[3] != c.D or k_new.dtype != k_pool.dtype or v_new.dtype != k_pool.dtype:
+    new, st = k_new.shape, k_new.stride()
+    if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != c.Hkv or new[3] != c.D \
+            or k_new.dtype is not k_pool.dtype or v_new.dtype is not k_pool.dtype:
         raise BastionError("paged append: k_new and v_new must be [B, n_rows, Hkv, D] of the pools' dtype")
-    st = k_new.stride()
     if st[3] != 1 or st != v_new.stride():
         raise BastionError("paged append: k_new and v_new must have equal strides and a contiguous last dimension")
-    n_rows = k_new.shape[1]
-    m = n_rows
+    m = n_rows = new[1]
     if rows is not None:
         if rows.dim() != 2:
             raise BastionError("paged append: rows must be [B, m]")
         m = rows.shape[1]
         _need("rows", rows, torch.int32, (B, m))
-    for name, t in (("seq_len", seq_len), ("seq_len_out", seq_len_out), ("status", status), ("n_new", n_new),
-                    ("n_seen", n_seen), ("n_seen_out", n_seen_out)):
-        if t is not None:
-            _need(name, t, torch.int32, (B,))
-    for name, t, dt in (("acc", acc, torch.float32), ("pos", pos, torch.int32)):
-        if t is not None:
-            _need(name, t, dt, (B, c.Hkv, cap))
-    _on_device(workspace, k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, status, rows, n_new, acc,
-               pos, n_seen, n_seen_out)
+    _need_all("seq_len seq_len_out status n_new n_seen n_seen_out",
+              (seq_len, seq_len_out, status, n_new, n_seen, n_seen_out), torch.int32, (B,))
+    if acc is not None:
+        _need("acc", acc, torch.float32, (B, c.Hkv, cap))
+    if pos is not None:
+        _need("pos", pos, torch.int32, (B, c.Hkv, cap))
+    st_cuda = _on_device(stream, workspace, k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, status, rows,
+                         n_new, acc, pos, n_seen, n_seen_out)
     rc = lib().bastion_paged_append(ctypes.byref(c), k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
                                     _ptr(rows), m, _ptr(n_new), seq_len.data_ptr(), seq_len_out.data_ptr(),
                                     _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos), workspace.data_ptr(),
-                                    workspace.numel(), status.data_ptr(), _s(stream))
+                                    workspace.numel(), status.data_ptr(), st_cuda)
     _check(rc, "bastion_paged_append")
 
 
@@ -459,23 +466,22 @@ def bastion_paged_attention(q, k_pool, v_pool, page_table, seq_len, scale, out, 
     """q [B, Hq, D] (heads contiguous, any stride between requests), out [B, Hq, D] contiguous, lse [B, Hq]
     float32 or None; acc/acc_out [B, Hkv, max_pages * page_size] float32 or None (acc_out may be acc)."""
     c = _cache(k_pool, v_pool, page_table)
-    if q.dim() != 3 or q.dtype != k_pool.dtype or q.shape[0] != c.B or q.shape[2] != c.D:
+    qs, st = q.shape, q.stride()
+    if len(qs) != 3 or q.dtype is not k_pool.dtype or qs[0] != c.B or qs[2] != c.D:
         raise BastionError("paged attention: q must be [B, Hq, D] of the pools' dtype")
-    Hq, st = q.shape[1], q.stride()
+    Hq = qs[1]
     if st[2] != 1 or (Hq > 1 and st[1] != c.D):
         raise BastionError("paged attention: the heads of q must be contiguous")
-    _need("out", out, q.dtype, tuple(q.shape))
-    _need("seq_len", seq_len, torch.int32, (c.B,))
-    _need("status", status, torch.int32, (c.B,))
+    _need("out", out, q.dtype, qs)
+    _need_all("seq_len status", (seq_len, status), torch.int32, (c.B,))
     if lse is not None:
         _need("lse", lse, torch.float32, (c.B, Hq))
-    for name, t in (("acc", acc), ("acc_out", acc_out)):
-        if t is not None:
-            _need(name, t, torch.float32, (c.B, c.Hkv, c.max_pages * c.page_size))
-    _on_device(workspace, q, k_pool, v_pool, page_table, seq_len, out, status, lse, acc, acc_out)
+    if acc is not None or acc_out is not None:
+        _need_all("acc acc_out", (acc, acc_out), torch.float32, (c.B, c.Hkv, c.max_pages * c.page_size))
+    st_cuda = _on_device(stream, workspace, q, k_pool, v_pool, page_table, seq_len, out, status, lse, acc, acc_out)
     rc = lib().bastion_paged_attention(ctypes.byref(c), q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale,
                                        out.data_ptr(), _ptr(lse), _ptr(acc), _ptr(acc_out), workspace.data_ptr(),
-                                       workspace.numel(), status.data_ptr(), _s(stream))
+                                       workspace.numel(), status.data_ptr(), st_cuda)
     _check(rc, "bastion_paged_attention")
 
 
@@ -488,18 +494,16 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
     """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
     largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
     c = _cache(k_pool, v_pool, page_table)
-    for name, t in (("seq_len", seq_len), ("n_seen", n_seen), ("seq_len_out", seq_len_out), ("status", status)):
-        _need(name, t, torch.int32, (c.B,))
+    _need_all("seq_len n_seen seq_len_out status", (seq_len, n_seen, seq_len_out, status), torch.int32, (c.B,))
     shape = (c.B, c.Hkv, c.max_pages * c.page_size)
-    for name, t, dt in (("acc", acc, torch.float32), ("acc_out", acc_out, torch.float32),
-                        ("pos", pos, torch.int32), ("pos_out", pos_out, torch.int32)):
-        _need(name, t, dt, shape)
-    _on_device(workspace, k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, seq_len_out, acc_out, pos_out,
-               status)
+    _need_all("acc acc_out", (acc, acc_out), torch.float32, shape)
+    _need_all("pos pos_out", (pos, pos_out), torch.int32, shape)
+    st_cuda = _on_device(stream, workspace, k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, seq_len_out,
+                         acc_out, pos_out, status)
     rc = lib().bastion_paged_evict(ctypes.byref(c), seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(),
                                    pos.data_ptr(), budget, n_sink, n_recent, seq_len_out.data_ptr(),
                                    acc_out.data_ptr(), pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   status.data_ptr(), _s(stream))
+                                   status.data_ptr(), st_cuda)
     _check(rc, "bastion_paged_evict")
 
 
