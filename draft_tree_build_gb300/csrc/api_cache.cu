@@ -140,7 +140,8 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
   if (Hq / cache->Hkv > 16) return BASTION_ERR_UNSUPPORTED;
   if (!tiles_ok(cache)) return BASTION_ERR_SIZE;
   if (!stride_ok(cache->B, q_stride_b, 0)) return BASTION_ERR_SIZE;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return BASTION_ERR_ALIGN;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(acc, 16) || !aligned(acc_out, 16))
+    return BASTION_ERR_ALIGN;
   if (acc && !same_or_apart(acc, acc_out, slots_bytes(cache))) return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_attention_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D,
                                                                 (int64_t)cache->max_pages * cache->page_size,
@@ -166,7 +167,9 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
   const int rc = check_cache(cache);
   if (rc != BASTION_OK) return rc;
   if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget) return BASTION_ERR_SIZE;
-  if (!aligned(workspace, 256)) return BASTION_ERR_ALIGN;
+  if (!aligned(workspace, 256) || !aligned(acc, 16) || !aligned(pos, 16) || !aligned(acc_out, 16) ||
+      !aligned(pos_out, 16))
+    return BASTION_ERR_ALIGN;
   if (!same_or_apart(seq_len, seq_len_out, (size_t)cache->B * 4) ||
       !same_or_apart(acc, acc_out, slots_bytes(cache)) || !same_or_apart(pos, pos_out, slots_bytes(cache)))
     return BASTION_ERR_UNSUPPORTED;

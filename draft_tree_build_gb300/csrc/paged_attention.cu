@@ -200,12 +200,12 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t one, uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                            int c3, uint32_t bar) {
+                                            int c3, uint32_t bar, uint64_t policy) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %7, 0;\n"
-      " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(one)
+      " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6], %8;\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(one), "l"(policy)
       : "memory");
 }
 
@@ -523,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return e;
     };
     int entry = 0, entry_n = next_entry(), in_batch = batch;
+    const uint64_t policy = l2_evict_first_policy();  // read once: not at the scores' and parts' expense
     const uint32_t ring32 = smem_u32(ring), full32 = smem_u32(full);
     int slot = 0, phase = 0, issued = 0;
 #pragma unroll 1
@@ -546,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id = __shfl_sync(kFull, entry, (in_batch << psh) + p);
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
-          tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot);
+          tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot,
+                      policy);
         dst += (uint32_t)(128 << c.shift);
       }
       if (++slot == kStages) {
@@ -915,24 +917,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// acc_out = acc + sum over the group's heads of exp2(s - lse2), in head order.
-__global__ void __launch_bounds__(256) paged_weights_kernel(Paged c, AttendArgs a) {
+// acc_out = acc + sum over the group's heads of exp2(s - lse2), in head order;
+// four keys a thread, 16 bytes of every row that it touches, with the heads'
+// loads in flight together and none of them waiting for the length (the score
+// rows span the whole capacity).
+constexpr int kWeightsThreads = 128;
+__global__ void __launch_bounds__(kWeightsThreads) paged_weights_kernel(Paged c, AttendArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int unit = blockIdx.y, r = unit / c.Hkv, g = unit % c.Hkv;
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  int n = a.seq_len[r];
-  n = min(max(n, 0), c.cap);
-  if (j >= n) return;
+  const int j = 4 * (blockIdx.x * kWeightsThreads + threadIdx.x);
+  if (j >= c.cap) return;
   const float *s = a.scores + ((size_t)unit * a.tiles_cap + j / kTileKeys) * a.G * kTileKeys + j % kTileKeys;
   const float *lse2 = a.lse2 + (size_t)r * a.Hq + g * a.G;
-  float w = 0.f;
-  for (int h = 0; h < a.G; ++h) {
-    const float x = lse2[h];
-    if (x != -INFINITY) w += exp2f(s[h * kTileKeys] - x);
-  }
   const size_t at = (size_t)unit * c.cap + j;
-  a.acc_out[at] = a.acc[at] + w;
+  const int n = clamped_len(c, a, r);
+  const float4 was = *reinterpret_cast<const float4 *>(a.acc + at);
+  float w[4] = {};
+  for (int h0 = 0; h0 < a.G; h0 += 4) {
+    float4 x[4];
+    float y[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const bool on = h0 + h < a.G;
+      y[h] = on ? lse2[h0 + h] : -INFINITY;
+      if (on) x[h] = *reinterpret_cast<const float4 *>(s + (h0 + h) * kTileKeys);
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if (y[h] == -INFINITY) continue;  // no such head, or one that sees nothing
+      w[0] += exp2f(x[h].x - y[h]);
+      w[1] += exp2f(x[h].y - y[h]);
+      w[2] += exp2f(x[h].z - y[h]);
+      w[3] += exp2f(x[h].w - y[h]);
+    }
+  }
+  if (j + 4 <= n) {
+    *reinterpret_cast<float4 *>(a.acc_out + at) = make_float4(was.x + w[0], was.y + w[1], was.z + w[2], was.w + w[3]);
+  } else {
+    if (j < n) a.acc_out[at] = was.x + w[0];
+    if (j + 1 < n) a.acc_out[at + 1] = was.y + w[1];
+    if (j + 2 < n) a.acc_out[at + 2] = was.z + w[2];
+  }
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1040,8 +1066,9 @@ int launch_paged_attention(const Paged &c, bool half, const void *q, int Hq, int
   const int sm_grid = sms < kMaxGrid ? sms : kMaxGrid, grid = most < sm_grid ? (int)most : sm_grid;
   cudaError_t e = half ? launch_half<true>(mk, mv, grid, c, a, stream) : launch_half<false>(mk, mv, grid, c, a, stream);
   if (e == cudaSuccess && acc)
-    e = launch_pdl(paged_weights_kernel, dim3((unsigned)((c.cap + 255) / 256), (unsigned)(c.B * c.Hkv)), dim3(256), 0,
-                   stream, c, a);
+    e = launch_pdl(paged_weights_kernel,
+                   dim3((unsigned)((c.cap + 4 * kWeightsThreads - 1) / (4 * kWeightsThreads)), (unsigned)(c.B * c.Hkv)),
+                   dim3(kWeightsThreads), 0, stream, c, a);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? BASTION_OK : BASTION_ERR_LAUNCH;
 }
 

@@ -102,8 +102,8 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
  * out      [B, Hq, D] contiguous, the cache's dtype (rounded once to nearest
  *          even), 16-byte aligned.
  * lse      [B, Hq] float or NULL.
- * acc, acc_out  [B, Hkv, max_pages * page_size] float, both or neither NULL;
- *          the same array or disjoint ones.  Slots at or past seq_len[r] of
+ * acc, acc_out  [B, Hkv, max_pages * page_size] float, 16-byte aligned, both or
+ *          neither NULL; the same array or disjoint ones.  Slots at or past seq_len[r] of
  *          acc_out are left as they are.
  * scale    finite and > 0, else BASTION_ERR_SIZE.
  * NaN in a used key or query gives NaN in the heads that see it.
@@ -135,8 +135,9 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
  * evicts few tokens moves few.  Slot order is therefore not token order: pos
  * names each slot's token.  Attention does not depend on the order.
  *
- * acc, pos      [B, Hkv, max_pages * page_size]: weights and positions.  A NaN
- *               weight sets BASTION_STATUS_NONFINITE and counts as +inf.
+ * acc, pos      [B, Hkv, max_pages * page_size]: weights and positions, 16-byte
+ *               aligned (as acc_out and pos_out).  A NaN weight sets
+ *               BASTION_STATUS_NONFINITE and counts as +inf.
  * seq_len_out   [B]: min(seq_len, budget).
  * acc_out, pos_out: slots below min(seq_len, budget) are written, the others
  *               left as they are.
@@ -144,7 +145,7 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
  * Limits: 1 <= budget, n_sink, n_recent >= 0, n_sink + n_recent <= budget
  * (BASTION_ERR_SIZE).
  * Workspace: bastion_paged_evict_workspace_bytes(B, Hkv,
- * max_pages * page_size) bytes.  Two launches.
+ * max_pages * page_size) bytes.  One launch.
  */
 size_t bastion_paged_evict_workspace_bytes(int B, int Hkv, int64_t cap);
 int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len,
