@@ -2,20 +2,22 @@
 //
 // One launch; a cluster of 1 to 8 CTAs per (request, KV head).  Slot j's key is
 // its weight as an order-preserving 32-bit integer, the protected slots' above
-// all weights.  A radix select (13 + 10 + 9 bits, histograms in shared memory,
-// summed over the cluster) finds the budget-th largest key t and how many of
-// the slots that tie with it stay.  One count in slot order then gives both
-// lists of the moves: the i-th hole (a slot below budget that is not kept)
-// takes the i-th kept slot at or past budget, with
+// all weights.  A histogram of the keys' top 13 bits, summed over the cluster,
+// gives the bin that holds the budget-th largest key; that bin's keys are
+// gathered and ranked against one another (or, when they are many, split by two
+// more histograms of 10 and 9 bits), which gives the budget-th largest key t
+// and how many of the slots that tie with it stay.  One count in slot order
+// then gives both lists of the moves: the i-th hole (a slot below budget that
+// is not kept) takes the i-th kept slot at or past budget, with
 //   K(s) = kept slots before s = #(key > t before s) + min(#(key == t before s), ties that stay)
 //   hole index of s < budget: s - K(s);   source index of s >= budget: K(s) - K(budget).
 // Sources lie at or past budget and targets below it, so that no move reads
 // what another writes.  Weights and positions are read once (the keys stay in
 // shared memory) and only the holes' rows move.
 //
-// 13 bits in the first pass because weights crowd into few octaves: 16 bins an
-// octave keep the lanes of a warp out of one another's way, 4 (11 bits) made
-// the histogram the longest step.
+// Latency-bound when few tokens leave, HBM-bound when prompts are cut.  13 bits
+// in the first pass because weights crowd into few octaves: 16 bins an octave
+// keep the lanes of a warp out of one another's way.
 #include "paged.cuh"
 
 namespace bastion {
@@ -26,6 +28,9 @@ constexpr uint32_t kSafe = 0xffffffffu;  // key of a protected slot
 constexpr int kBits0 = 13, kBits1 = 10, kBits2 = 9;
 constexpr int kBins0 = 1 << kBits0, kBins1 = 1 << kBits1, kBins2 = 1 << kBits2;
 constexpr int kHist = kBins0 + kBins1 + kBins2;
+constexpr int kCand = 256;       // keys of one bin that are ranked directly
+constexpr int kNearMoves = 512;
+constexpr int kMaxCluster = 8;
 constexpr int kKeysMax = 45056;  // keys a CTA keeps in shared memory
 constexpr int kMovesWarp = 8;    // moves a warp has in flight
 constexpr int kMaxRequests = 1024;
@@ -55,10 +60,11 @@ __device__ __forceinline__ uint32_t slot_key(float w, int pos, int sink, int64_t
 }
 
 struct Misc {
-  uint32_t warp_sum[32];
+  uint32_t warp_sum[3][32];             // entries of each warp's run of bins, of each pass (others may still read one)
   uint32_t warp_gt[32], warp_eq[32];
-  uint32_t count[4];  // this CTA's keys above t, equal to t, and of these below budget
-  uint32_t bin, above;
+  alignas(16) uint32_t count[4];        // this CTA's keys above t, equal to t, and of these below budget
+  uint32_t bin, above, in_bin;
+  uint32_t n_cand;
 };
 
 __device__ __forceinline__ uint4 dsmem_ld_v4(uint32_t addr) {
@@ -70,48 +76,93 @@ __device__ __forceinline__ uint4 dsmem_ld_v4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 // kKeys: the keys of the CTA's segment stay in shared memory (else they are formed anew for each pass).
 template <bool kKeys>
 __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a, int cs) {
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t *hist = smem, *keys = smem + kHist;
   __shared__ Misc ms;
+  __shared__ __align__(16) uint32_t cand[kCand];  // the bin's keys: this CTA's, then the cluster's
+  __shared__ int2 near_moves[kNearMoves];         // the list of moves where it is short and one CTA's
   griddep_wait();
   griddep_launch_dependents();
   const int unit = blockIdx.x / cs, part = blockIdx.x % cs, r = unit / c.Hkv, g = unit % c.Hkv;
   const int tid = threadIdx.x, T = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = T >> 5;
-  const int n = paged_len(c, a.seq_len, r, a.status);
-  const int64_t recent = (int64_t)a.n_seen[r] - a.n_recent;
   const size_t base = (size_t)unit * c.cap;
   const float *acc = a.acc + base;
   const int32_t *pos = a.pos + base;
   float *acc_out = a.acc_out + base;
   int32_t *pos_out = a.pos_out + base;
-
-  // The lengths may be updated in place: the request's last CTA to have read them writes.
-  auto leave = [&]() {
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      if (atomicAdd(&a.arrived[r], 1u) == (uint32_t)(c.Hkv * cs - 1)) {
-        a.arrived[r] = 0;
-        const int raw = a.seq_len[r];
-        a.seq_len_out[r] = raw > a.budget ? a.budget : raw;
+  // A row of acc and pos is whole vectors of 4 (pages have 8 slots at least).  A lone CTA's first
+  // vectors do not depend on the length: they are under way before it is known.
+  float4 w[2];
+  int4 p[2];
+  auto fetch = [&](int v0, int end) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int s = v0 + 4 * (u * T + tid);
+      if (s < end) {
+        w[u] = *reinterpret_cast<const float4 *>(acc + s);
+        p[u] = *reinterpret_cast<const int4 *>(pos + s);
       }
     }
   };
-  if (n <= a.budget) {  // the whole cluster
+  if (kKeys && cs == 1) fetch(0, c.cap);
+  const int n = paged_len(c, a.seq_len, r, a.status);
+  const int64_t recent = (int64_t)a.n_seen[r] - a.n_recent;
+  for (int i = tid; i < kHist / 4; i += T) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) ms.n_cand = 0;
+  if (tid < 4) ms.count[tid] = 0;
+
+  // The lengths may be updated in place: the last of the request's CTAs to have
+  // read them (after a barrier) writes.
+  auto length_read = [&]() {
+    if (tid != 0) return;
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(&a.arrived[r]) : "memory");
+    if (old == (uint32_t)(c.Hkv * cs - 1)) {
+      a.arrived[r] = 0;
+      const int raw = a.seq_len[r];
+      a.seq_len_out[r] = raw > a.budget ? a.budget : raw;
+    }
+  };
+  // this CTA's segment of the slots, in whole vectors of 4
+  const int seg = ((n + cs - 1) / cs + 3) & ~3, s0 = min(n, part * seg), s1 = min(n, s0 + seg), count = s1 - s0;
+  const int keep_end = min(a.budget, s1);  // slots below it go to acc_out and pos_out where those are other arrays
+  // vector s of the segment to the outputs; the holes among its slots are written over by the moves
+  auto copy4 = [&](int s, const float4 &x, const int4 &y) {
+    if (s + 4 <= keep_end) {
+      if (a.acc_out != a.acc) *reinterpret_cast<float4 *>(acc_out + s) = x;
+      if (a.pos_out != a.pos) *reinterpret_cast<int4 *>(pos_out + s) = y;
+    } else {
+      const float *xf = reinterpret_cast<const float *>(&x);
+      const int *yf = reinterpret_cast<const int *>(&y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s + k < keep_end) {
+          acc_out[s + k] = xf[k];
+          pos_out[s + k] = yf[k];
+        }
+    }
+  };
+  if (n <= a.budget) {  // the whole cluster: nothing leaves
     if (a.copy)
-      for (int s = part * T + tid; s < n; s += cs * T) {
-        acc_out[s] = acc[s];
-        pos_out[s] = pos[s];
-      }
-    leave();
+      for (int s = s0 + 4 * tid; s < s1; s += 4 * T)
+        copy4(s, *reinterpret_cast<const float4 *>(acc + s), *reinterpret_cast<const int4 *>(pos + s));
+    __syncthreads();
+    length_read();
     return;
   }
 
-  // this CTA's segment of the slots, in whole vectors of 4
-  const int seg = ((n + cs - 1) / cs + 3) & ~3, s0 = min(n, part * seg), s1 = min(n, s0 + seg), count = s1 - s0;
   auto cluster_sync = [&]() {
     if (cs > 1) {
       cluster_arrive();
@@ -120,144 +171,200 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
       __syncthreads();
     }
   };
-  bool nan = false;
-  for (int i = tid; i < kHist / 4; i += T) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  auto key_at = [&](int i) {
-    return kKeys ? keys[i] : slot_key(acc[s0 + i], pos[s0 + i], a.n_sink, recent, nan);
-  };
+  bool nan = false;
   auto enter = [&](uint32_t k, bool on) {
     // many protected slots lie side by side: one addition for a warp's
     const uint32_t safe = __ballot_sync(kFull, on && k == kSafe);
     if (on && k != kSafe) atomicAdd(&hist[k >> (32 - kBits0)], 1u);
     if (safe && lane == 0) atomicAdd(&hist[kBins0 - 1], (uint32_t)__popc(safe));
   };
-  if (kKeys) {
-    const int vecs = (count + 3) / 4;  // acc and pos rows are padded to whole vectors by the page size
-    for (int v0 = 0; v0 < vecs; v0 += 2 * T) {
-      float4 w[2];
-      int4 p[2];
+  for (int v0 = s0; v0 < s1; v0 += 8 * T) {
+    if (!(kKeys && cs == 1 && v0 == 0)) fetch(v0, s1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int v = v0 + u * T + tid;
-        if (v < vecs) {
-          w[u] = *reinterpret_cast<const float4 *>(acc + s0 + 4 * v);
-          p[u] = *reinterpret_cast<const int4 *>(pos + s0 + 4 * v);
-        }
+    for (int u = 0; u < 2; ++u) {
+      if (v0 + 4 * (u * T + 32 * warp) >= s1) continue;  // the whole warp
+      const int s = v0 + 4 * (u * T + tid);
+      const float *wf = reinterpret_cast<const float *>(&w[u]);
+      const int *pf = reinterpret_cast<const int *>(&p[u]);
+      uint32_t k[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool on = s + x < s1;
+        k[x] = on ? slot_key(wf[x], pf[x], a.n_sink, recent, nan) : 0u;
+        enter(k[x], on);
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int v = v0 + u * T + tid;
-        const float *wf = reinterpret_cast<const float *>(&w[u]);
-        const int *pf = reinterpret_cast<const int *>(&p[u]);
-        uint32_t k[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const bool on = v < vecs && 4 * v + x < count;
-          k[x] = on ? slot_key(wf[x], pf[x], a.n_sink, recent, nan) : 0u;
-          enter(k[x], on);
-        }
-        if (v < vecs) *reinterpret_cast<uint4 *>(keys + 4 * v) = make_uint4(k[0], k[1], k[2], k[3]);
+      if (s < s1) {
+        if (kKeys) *reinterpret_cast<uint4 *>(keys + s - s0) = make_uint4(k[0], k[1], k[2], k[3]);
+        if (a.copy) copy4(s, w[u], p[u]);
       }
     }
-  } else {
-    for (int i0 = 0; i0 < count; i0 += T) enter(i0 + tid < count ? key_at(i0 + tid) : 0u, i0 + tid < count);
   }
   if (nan) atomicOr(&a.status[r], BASTION_STATUS_NONFINITE);
-
-  uint32_t t = 0, need = (uint32_t)a.budget;
+  length_read();
+  // keys i .. i + 3 of the segment, i a multiple of 4; 0 past its end
+  auto keys4 = [&](int i, uint32_t (&k)[4]) {
+    if (kKeys) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(keys + i);
+      k[0] = x.x;
+      k[1] = x.y;
+      k[2] = x.z;
+      k[3] = x.w;
+    } else {
+      const float4 wf = *reinterpret_cast<const float4 *>(acc + s0 + i);
+      const int4 pf = *reinterpret_cast<const int4 *>(pos + s0 + i);
+      const float *ww = reinterpret_cast<const float *>(&wf);
+      const int *pp = reinterpret_cast<const int *>(&pf);
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
+      for (int x = 0; x < 4; ++x) k[x] = i + x < count ? slot_key(ww[x], pp[x], a.n_sink, recent, nan) : 0u;
+    }
+  };
+
+  // t: the bits found of the budget-th largest key, `shift` more are open; `need` of the keys that
+  // begin with t are kept
+  uint32_t t = 0, need = (uint32_t)a.budget;
+  int shift = 32;
+#pragma unroll 1
+  for (int pass = 0; pass < 3 && shift > 0; ++pass) {
     const int bits = pass == 0 ? kBits0 : pass == 1 ? kBits1 : kBits2, bins = 1 << bits;
     uint32_t *h = hist + (pass == 0 ? 0 : pass == 1 ? kBins0 : kBins0 + kBins1);
+    shift -= bits;
     if (pass > 0) {
-      const int shift = pass == 1 ? kBits2 : 0;
-      for (int i = tid; i < count; i += T) {
-        const uint32_t k = key_at(i);
-        if ((k >> (shift + bits)) == t) atomicAdd(&h[(k >> shift) & (uint32_t)(bins - 1)], 1u);
+#pragma unroll 2
+      for (int i = 4 * tid; i < count; i += 4 * T) {
+        uint32_t k[4];
+        keys4(i, k);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (i + x < count && (k[x] >> (shift + bits)) == t) atomicAdd(&h[(k[x] >> shift) & (uint32_t)(bins - 1)], 1u);
       }
     }
-    cluster_sync();
-    // the cluster's sums of bins b .. b + 3
-    auto bins4 = [&](int b) {
-      uint4 x = *reinterpret_cast<const uint4 *>(h + b);
-      for (int o = 1; o < cs; ++o) {
-        const uint4 y = dsmem_ld_v4(dsmem_addr(h + b, (uint32_t)((part + o) % cs)));
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-      }
-      return x;
-    };
-    // each warp sums its run of bins, the first warp the topmost
-    const int run = max(bins / warps, 128), top = bins - warp * run;
-    uint32_t sum = 0;
-    for (int b = top - 4 * lane - 4; b >= top - run && b >= 0; b -= 128) {
-      const uint4 x = bins4(b);
-      sum += x.x + x.y + x.z + x.w;
-    }
-    sum = __reduce_add_sync(kFull, sum);
-    if (lane == 0) ms.warp_sum[warp] = sum;
     __syncthreads();
-    uint32_t before = lane < warps ? ms.warp_sum[lane] : 0u;
+    // each warp's run of bins, the first warp's topmost: this CTA's entries
+    const int run = max(bins / warps, 128), runs = bins / run;
+    uint32_t sum = 0;
+    if (warp < runs)
+      for (int b = bins - warp * run - 4 * lane - 4; b >= bins - (warp + 1) * run; b -= 128) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(h + b);
+        sum += x.x + x.y + x.z + x.w;
+      }
+    sum = __reduce_add_sync(kFull, sum);
+    if (lane == 0) ms.warp_sum[pass][warp] = sum;
+    cluster_sync();
+    if (warp == 0) {
+      // the run, then the bin, over all CTAs of the cluster
+      uint32_t own = lane < runs ? ms.warp_sum[pass][lane] : 0u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(kFull, before, o);
-      if (lane >= o) before += y;
-    }
-    before = __shfl_sync(kFull, before, warp) - sum;  // entries above this warp's run
-    if (before < need && before + sum >= need) {      // one warp: the bin is in its run
-      for (int b0 = top;; b0 -= 128) {
+      for (int o = 1; o < kMaxCluster; ++o)
+        if (o < cs && lane < runs) own += dsmem_ld_u32(dsmem_addr(&ms.warp_sum[pass][lane], (uint32_t)((part + o) & (cs - 1))));
+      uint32_t incl = warp_scan(own, lane);
+      const int in_run = __ffs(__ballot_sync(kFull, incl >= need)) - 1;  // need <= all entries
+      uint32_t before = __shfl_sync(kFull, incl - own, in_run);
+      for (int b0 = bins - in_run * run; b0 > 0; b0 -= 128) {
         const int b = b0 - 4 * lane - 4;
-        const uint4 x = b >= 0 ? bins4(b) : make_uint4(0, 0, 0, 0);
-        uint32_t incl = x.x + x.y + x.z + x.w;
-        const uint32_t own = incl;
+        uint4 x = *reinterpret_cast<const uint4 *>(h + b);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(kFull, incl, o);
-          if (lane >= o) incl += y;
+        for (int o = 1; o < kMaxCluster; ++o) {
+          const uint4 y = o < cs ? dsmem_ld_v4(dsmem_addr(h + b, (uint32_t)((part + o) & (cs - 1)))) : make_uint4(0, 0, 0, 0);
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
         }
+        own = x.x + x.y + x.z + x.w;
+        incl = warp_scan(own, lane);
         uint32_t above = before + incl - own;
-        if (above < need && above + own >= need) {
+        if (above < need && above + own >= need) {  // one lane
           const uint32_t y[4] = {x.w, x.z, x.y, x.x};
-          int at = b + 3;
+          int at = 0;
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            if (at == b + 3 - q && above + y[q] < need) {
+            if (at == q && above + y[q] < need) {
               above += y[q];
-              --at;
+              ++at;
             }
-          ms.bin = (uint32_t)at;
+          ms.bin = (uint32_t)(b + 3 - at);
           ms.above = above;
+          ms.in_bin = at == 0 ? y[0] : at == 1 ? y[1] : at == 2 ? y[2] : y[3];
         }
         before += __shfl_sync(kFull, incl, 31);
-        if (before >= need || b0 <= 128) break;
+        if (before >= need) break;
       }
     }
     __syncthreads();
     need -= ms.above;
     t = (t << bits) | ms.bin;
+    const uint32_t in_bin = ms.in_bin;
+    if (shift > 0 && in_bin <= (uint32_t)kCand) {
+      // few keys begin with t: gather them and rank each against all
+#pragma unroll 2
+      for (int i = 4 * tid; i < count; i += 4 * T) {
+        uint32_t k[4];
+        keys4(i, k);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (i + x < count && (k[x] >> shift) == t) cand[atomicAdd(&ms.n_cand, 1u)] = k[x];
+      }
+      cluster_sync();
+      const int own = (int)ms.n_cand;
+      int m = own;
+      if (cs > 1) {
+        // the other CTAs' keys behind this CTA's own, a warp a CTA; each CTA only ever reads the
+        // first n_cand of another, which do not change any more
+        const uint32_t peer = (uint32_t)((part + lane) & (cs - 1));
+        const uint32_t theirs = lane < cs ? dsmem_ld_u32(dsmem_addr(&ms.n_cand, peer)) : 0u;
+        const uint32_t end = warp_scan(theirs, lane);
+        m = (int)__shfl_sync(kFull, end, 31);
+        if (warp > 0 && warp < cs) {
+          const int k = (int)__shfl_sync(kFull, theirs, warp), at = (int)__shfl_sync(kFull, end, warp) - k;
+          for (int i = lane; i < k; i += 32)
+            cand[at + i] = dsmem_ld_u32(dsmem_addr(cand + i, (uint32_t)((part + warp) & (cs - 1))));
+        }
+        __syncthreads();
+      }
+      for (int i = tid; i < m; i += T) {
+        const uint32_t k = cand[i];
+        uint32_t gt = 0, eq = 0;
+#pragma unroll 2
+        for (int j = 0; j < m; j += 4) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(cand + j);
+          gt += (x.x > k) + (j + 1 < m && x.y > k) + (j + 2 < m && x.z > k) + (j + 3 < m && x.w > k);
+          eq += (x.x == k) + (j + 1 < m && x.y == k) + (j + 2 < m && x.z == k) + (j + 3 < m && x.w == k);
+        }
+        if (gt < need && gt + eq >= need) {  // every thread that holds t writes the same
+          ms.bin = k;
+          ms.above = gt;
+        }
+      }
+      __syncthreads();
+      need -= ms.above;
+      t = ms.bin;
+      shift = 0;
+    }
   }
 
   // t is the budget-th largest key; `need` of the slots that equal it stay.  Each
-  // warp counts its own run of the segment, in whole groups of 32.
-  const int run = (count + T - 1) / T * 32, w0 = min(count, warp * run), w1 = min(count, w0 + run);
+  // warp counts its own run of the segment, 128 slots at a time, 4 a lane.
+  const int run = (count + 4 * T - 1) / (4 * T) * 128, w0 = min(count, warp * run), w1 = min(count, w0 + run);
   const int below = a.budget - s0;  // the segment's slots below it are below budget
   uint32_t gt = 0, eq = 0, gt_b = 0, eq_b = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key_at(i);
-    gt += k > t;
-    eq += k == t;
-    gt_b += i < below && k > t;
-    eq_b += i < below && k == t;
+#pragma unroll 2
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    uint32_t k[4];
+    keys4(i, k);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool on = i + x < w1, low = i + x < below;
+      gt += on && k[x] > t;
+      eq += on && k[x] == t;
+      gt_b += on && low && k[x] > t;
+      eq_b += on && low && k[x] == t;
+    }
   }
   gt = __reduce_add_sync(kFull, gt);
   eq = __reduce_add_sync(kFull, eq);
   gt_b = __reduce_add_sync(kFull, gt_b);
   eq_b = __reduce_add_sync(kFull, eq_b);
-  if (tid < 4) ms.count[tid] = 0;
-  __syncthreads();
   if (lane == 0) {
     ms.warp_gt[warp] = gt;
     ms.warp_eq[warp] = eq;
@@ -267,76 +374,93 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     atomicAdd(&ms.count[3], eq_b);
   }
   __syncthreads();
-  cluster_sync();
+  if (cs > 1) cluster_sync();
   uint32_t g0 = __reduce_add_sync(kFull, lane < warp ? ms.warp_gt[lane] : 0u);
   uint32_t e0 = __reduce_add_sync(kFull, lane < warp ? ms.warp_eq[lane] : 0u);
   uint32_t gb = ms.count[2], eb = ms.count[3];
-  for (int o = 0; o < cs; ++o) {
-    if (o == part) continue;
-    const uint32_t at = dsmem_addr(ms.count, (uint32_t)o);
-    if (o < part) {
-      g0 += dsmem_ld_u32(at);
-      e0 += dsmem_ld_u32(at + 4);
+  if (cs > 1) {
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; ++o) {
+      const int rank = (part + o) & (cs - 1);
+      const uint4 x = o < cs ? dsmem_ld_v4(dsmem_addr(ms.count, (uint32_t)rank)) : make_uint4(0, 0, 0, 0);
+      if (rank < part) {
+        g0 += x.x;
+        e0 += x.y;
+      }
+      gb += x.z;
+      eb += x.w;
     }
-    gb += dsmem_ld_u32(at + 8);
-    eb += dsmem_ld_u32(at + 12);
   }
   const uint32_t kb = gb + min(eb, need);  // kept slots below budget
-  int2 *moves = a.moves + (size_t)unit * a.max_moves;
-  const uint32_t lt = (1u << lane) - 1u;
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const bool on = i < w1;
-    const uint32_t k = on ? key_at(i) : 0u;
-    const uint32_t mg = __ballot_sync(kFull, on && k > t), me = __ballot_sync(kFull, on && k == t);
-    const uint32_t ge = g0 + __popc(mg & lt), ee = e0 + __popc(me & lt);
-    const bool keep = on && (k > t || (k == t && ee < need));
-    const uint32_t before = ge + min(ee, need);
-    const int s = s0 + i;
-    if (on && i < below) {
-      if (!keep) {
-        moves[s - (int)before].y = s;
-      } else if (a.copy) {
-        acc_out[s] = acc[s];
-        pos_out[s] = pos[s];
+  const int n_moves = a.budget - (int)kb;
+  const bool near = cs == 1 && n_moves <= kNearMoves;
+  int2 *moves = near ? near_moves : a.moves + (size_t)unit * a.max_moves;
+  for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
+    uint32_t k[4] = {0, 0, 0, 0};
+    if (i < w1) keys4(i, k);
+    uint32_t both = 0;  // keys above t, and equal ones in the high half
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x < w1) both += k[x] > t ? 1u : k[x] == t ? 0x10000u : 0u;
+    const uint32_t incl = warp_scan(both, lane), excl = incl - both, all = __shfl_sync(kFull, incl, 31);
+    uint32_t ge = g0 + (excl & 0xffffu), ee = e0 + (excl >> 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (i + x >= w1) break;
+      const int s = s0 + i + x;
+      const bool tie = k[x] == t, keep = k[x] > t || (tie && ee < need);
+      const uint32_t before = ge + min(ee, need);
+      if (i + x < below) {
+        if (!keep) moves[s - (int)before].y = s;
+      } else if (keep) {
+        moves[before - kb].x = s;
       }
-    } else if (keep) {
-      moves[before - kb].x = s;
+      ge += k[x] > t;
+      ee += tie;
     }
-    g0 += __popc(mg);
-    e0 += __popc(me);
+    g0 += all & 0xffffu;
+    e0 += all >> 16;
   }
   cluster_sync();  // the list is whole; no CTA reads another's shared memory any more
 
-  // the moves: a warp has the rows of kMovesWarp of them in flight, lanes 0-15
-  // on keys and 16-31 on values (16 bytes each; with D = 64 half of them)
-  const int n_moves = a.budget - (int)kb, half = lane >> 4, sub = lane & 15;
+  // The moves, T of them at a time.  First a thread a move: its pages, its
+  // weight and position; then a warp has the rows of kMovesWarp of them in
+  // flight, lanes 0-15 on keys and 16-31 on values (16 bytes each; with D = 64
+  // half of them).  The resolved rows take the keys' and bins' place.
+  longlong2 *rows = reinterpret_cast<longlong2 *>(smem);
+  const int half = lane >> 4, sub = lane & 15;
   const bool row_on = sub < c.D / 8;
   uint16_t *pool = half ? c.v : c.k;
-  for (int m0 = (part * warps + warp) * kMovesWarp; m0 < n_moves; m0 += cs * warps * kMovesWarp) {
-    int64_t src = -1, dst = -1;
-    if (lane < kMovesWarp && m0 + lane < n_moves) {
-      const int2 mv = __ldcg(&moves[m0 + lane]);
+#pragma unroll 1
+  for (int m0 = part * T; m0 < n_moves; m0 += cs * T) {
+    const int left = min(T, n_moves - m0);
+    if (tid < left) {
+      const int2 mv = near ? near_moves[m0 + tid] : __ldcg(&moves[m0 + tid]);
+      const float x = acc[mv.x];
+      const int y = pos[mv.x];
       const int ps = paged_page(c, r, mv.x, a.status), pd = paged_page(c, r, mv.y, a.status);
-      if (ps >= 0 && pd >= 0) {
-        src = paged_row(c, ps, mv.x, g);
-        dst = paged_row(c, pd, mv.y, g);
+      rows[tid] = ps >= 0 && pd >= 0 ? make_longlong2(paged_row(c, ps, mv.x, g), paged_row(c, pd, mv.y, g))
+                                     : make_longlong2(-1, -1);
+      acc_out[mv.y] = x;
+      pos_out[mv.y] = y;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = warp * kMovesWarp; i < left; i += warps * kMovesWarp) {
+      uint4 v[kMovesWarp];
+#pragma unroll
+      for (int x = 0; x < kMovesWarp; ++x) {
+        const int64_t src = i + x < left ? rows[i + x].x : -1;
+        if (src >= 0 && row_on) v[x] = *reinterpret_cast<const uint4 *>(pool + src + sub * 8);
       }
-      acc_out[mv.y] = acc[mv.x];
-      pos_out[mv.y] = pos[mv.x];
-    }
-    uint4 v[kMovesWarp];
-    int64_t to[kMovesWarp];
 #pragma unroll
-    for (int x = 0; x < kMovesWarp; ++x) {
-      const int64_t from = __shfl_sync(kFull, src, x);
-      to[x] = __shfl_sync(kFull, dst, x);
-      if (to[x] >= 0 && row_on) v[x] = *reinterpret_cast<const uint4 *>(pool + from + sub * 8);
+      for (int x = 0; x < kMovesWarp; ++x) {
+        const int64_t dst = i + x < left ? rows[i + x].y : -1;
+        if (dst >= 0 && row_on) *reinterpret_cast<uint4 *>(pool + dst + sub * 8) = v[x];
+      }
     }
-#pragma unroll
-    for (int x = 0; x < kMovesWarp; ++x)
-      if (to[x] >= 0 && row_on) *reinterpret_cast<uint4 *>(pool + to[x] + sub * 8) = v[x];
+    __syncthreads();
   }
-  leave();
 }
 
 }  // namespace
@@ -376,7 +500,7 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
   while (cs < 8 && ((units * cs * 2 <= sms && c.cap >= 4096 * cs) || c.cap > cs * kKeysMax)) cs *= 2;
   const int seg = ((c.cap + cs - 1) / cs + 3) & ~3;
   const bool in_smem = seg <= kKeysMax;
-  const int T = seg <= 4096 ? 256 : seg <= 8192 ? 512 : 1024;
+  const int T = seg <= 4096 ? 512 : 1024;
   const size_t smem = (size_t)kHist * 4 + (in_smem ? (size_t)seg * 4 : 0);
   auto kernel = in_smem ? paged_evict_kernel<true> : paged_evict_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kHist + kKeysMax) * 4));
