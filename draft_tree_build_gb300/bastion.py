@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -53,13 +54,9 @@ class BastionError(RuntimeError):
     pass
 
 
-class _PagedCacheStruct(ctypes.Structure):
-    """bastion_paged_cache of include/bastion_cache.h."""
-    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
-                ("stride_page", ctypes.c_int64), ("stride_slot", ctypes.c_int64), ("stride_head", ctypes.c_int64),
-                ("page_table", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("B", ctypes.c_int32),
-                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("max_pages", ctypes.c_int32)]
+# bastion_paged_cache of include/bastion_cache.h: k_pool, v_pool, n_pages, stride_page, stride_slot, stride_head,
+# page_table, dtype, B, Hkv, D, page_size, max_pages
+_PAGED_CACHE = struct.Struct("@PPqqqqPiiiiii")
 
 
 _lib = None
@@ -119,20 +116,19 @@ def lib(build_if_missing: bool = True):
     L.bastion_verify_greedy_noalloc.restype = i32
     L.bastion_verify_greedy_noalloc.argtypes = [vp, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp, vp,
                                                 vp, vp, vp, vp]
-    pc = ctypes.POINTER(_PagedCacheStruct)
     L.bastion_paged_append_workspace_bytes.restype = sz
     L.bastion_paged_append_workspace_bytes.argtypes = [i32]
     L.bastion_paged_append.restype = i32
-    L.bastion_paged_append.argtypes = [pc, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp,
+    L.bastion_paged_append.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                        vp, sz, vp, vp]
     L.bastion_paged_attention_workspace_bytes.restype = sz
     L.bastion_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i32]
     L.bastion_paged_attention.restype = i32
-    L.bastion_paged_attention.argtypes = [pc, vp, i32, i64, vp, f32, vp, vp, vp, vp, vp, sz, vp, vp]
+    L.bastion_paged_attention.argtypes = [vp, vp, i32, i64, vp, f32, vp, vp, vp, vp, vp, sz, vp, vp]
     L.bastion_paged_evict_workspace_bytes.restype = sz
     L.bastion_paged_evict_workspace_bytes.argtypes = [i32, i32, i64]
     L.bastion_paged_evict.restype = i32
-    L.bastion_paged_evict.argtypes = [pc, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
+    L.bastion_paged_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
     _lib = L
     return L
 
@@ -410,8 +406,11 @@ def _cache(k_pool, v_pool, page_table):
     table = page_table.shape
     if len(table) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
         raise BastionError("paged cache: page_table must be contiguous int32 [B, max_pages]")
-    return _PagedCacheStruct(k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2],
-                             page_table.data_ptr(), dt, table[0], shape[2], shape[3], shape[1], table[1])
+    # (B, Hkv, D, slots of a request, the struct's bytes, which ctypes passes by address)
+    B, max_pages, page, Hkv, D = table[0], table[1], shape[1], shape[2], shape[3]
+    return B, Hkv, D, max_pages * page, _PAGED_CACHE.pack(
+        k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2], page_table.data_ptr(), dt, B, Hkv, D, page,
+        max_pages)
 
 
 def _ptr(t):
@@ -427,10 +426,9 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     """k_new/v_new [B, n_rows, Hkv, D] (equal strides, last dim contiguous) enter the cache's next slots: the
     rows listed in rows [B, m] (a negative entry ends a list; Verify.accept_nodes fits), or the first n_new [B].
     seq_len_out may be seq_len, n_seen_out n_seen."""
-    c = _cache(k_pool, v_pool, page_table)
-    B, cap = c.B, c.max_pages * c.page_size
+    B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
     new, st = k_new.shape, k_new.stride()
-    if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != c.Hkv or new[3] != c.D \
+    if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != Hkv or new[3] != D \
             or k_new.dtype is not k_pool.dtype or v_new.dtype is not k_pool.dtype:
         raise BastionError("paged append: k_new and v_new must be [B, n_rows, Hkv, D] of the pools' dtype")
     if st[3] != 1 or st != v_new.stride():
@@ -444,12 +442,12 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     _need_all("seq_len seq_len_out status n_new n_seen n_seen_out",
               (seq_len, seq_len_out, status, n_new, n_seen, n_seen_out), torch.int32, (B,))
     if acc is not None:
-        _need("acc", acc, torch.float32, (B, c.Hkv, cap))
+        _need("acc", acc, torch.float32, (B, Hkv, cap))
     if pos is not None:
-        _need("pos", pos, torch.int32, (B, c.Hkv, cap))
+        _need("pos", pos, torch.int32, (B, Hkv, cap))
     st_cuda = _on_device(stream, workspace, k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, status, rows,
                          n_new, acc, pos, n_seen, n_seen_out)
-    rc = lib().bastion_paged_append(ctypes.byref(c), k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
+    rc = lib().bastion_paged_append(cache, k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
                                     _ptr(rows), m, _ptr(n_new), seq_len.data_ptr(), seq_len_out.data_ptr(),
                                     _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos), workspace.data_ptr(),
                                     workspace.numel(), status.data_ptr(), st_cuda)
@@ -465,21 +463,21 @@ def bastion_paged_attention(q, k_pool, v_pool, page_table, seq_len, scale, out, 
                             acc=None, acc_out=None, stream=None):
     """q [B, Hq, D] (heads contiguous, any stride between requests), out [B, Hq, D] contiguous, lse [B, Hq]
     float32 or None; acc/acc_out [B, Hkv, max_pages * page_size] float32 or None (acc_out may be acc)."""
-    c = _cache(k_pool, v_pool, page_table)
+    B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
     qs, st = q.shape, q.stride()
-    if len(qs) != 3 or q.dtype is not k_pool.dtype or qs[0] != c.B or qs[2] != c.D:
+    if len(qs) != 3 or q.dtype is not k_pool.dtype or qs[0] != B or qs[2] != D:
         raise BastionError("paged attention: q must be [B, Hq, D] of the pools' dtype")
     Hq = qs[1]
-    if st[2] != 1 or (Hq > 1 and st[1] != c.D):
+    if st[2] != 1 or (Hq > 1 and st[1] != D):
         raise BastionError("paged attention: the heads of q must be contiguous")
     _need("out", out, q.dtype, qs)
-    _need_all("seq_len status", (seq_len, status), torch.int32, (c.B,))
+    _need_all("seq_len status", (seq_len, status), torch.int32, (B,))
     if lse is not None:
-        _need("lse", lse, torch.float32, (c.B, Hq))
+        _need("lse", lse, torch.float32, (B, Hq))
     if acc is not None or acc_out is not None:
-        _need_all("acc acc_out", (acc, acc_out), torch.float32, (c.B, c.Hkv, c.max_pages * c.page_size))
+        _need_all("acc acc_out", (acc, acc_out), torch.float32, (B, Hkv, cap))
     st_cuda = _on_device(stream, workspace, q, k_pool, v_pool, page_table, seq_len, out, status, lse, acc, acc_out)
-    rc = lib().bastion_paged_attention(ctypes.byref(c), q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale,
+    rc = lib().bastion_paged_attention(cache, q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale,
                                        out.data_ptr(), _ptr(lse), _ptr(acc), _ptr(acc_out), workspace.data_ptr(),
                                        workspace.numel(), status.data_ptr(), st_cuda)
     _check(rc, "bastion_paged_attention")
@@ -493,14 +491,14 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
                         seq_len_out, acc_out, pos_out, workspace, status, stream=None):
     """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
     largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
-    c = _cache(k_pool, v_pool, page_table)
-    _need_all("seq_len n_seen seq_len_out status", (seq_len, n_seen, seq_len_out, status), torch.int32, (c.B,))
-    shape = (c.B, c.Hkv, c.max_pages * c.page_size)
+    B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
+    _need_all("seq_len n_seen seq_len_out status", (seq_len, n_seen, seq_len_out, status), torch.int32, (B,))
+    shape = (B, Hkv, cap)
     _need_all("acc acc_out", (acc, acc_out), torch.float32, shape)
     _need_all("pos pos_out", (pos, pos_out), torch.int32, shape)
     st_cuda = _on_device(stream, workspace, k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, seq_len_out,
                          acc_out, pos_out, status)
-    rc = lib().bastion_paged_evict(ctypes.byref(c), seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(),
+    rc = lib().bastion_paged_evict(cache, seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(),
                                    pos.data_ptr(), budget, n_sink, n_recent, seq_len_out.data_ptr(),
                                    acc_out.data_ptr(), pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                    status.data_ptr(), st_cuda)

@@ -497,10 +497,10 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
   // CTAs of a unit: as many as the device has room for at one CTA per SM, with 2,048 slots each at least; more
   // where their keys would not fit
   int cs = 1;
-  while (cs < 8 && ((units * cs * 2 <= sms && c.cap >= 4096 * cs) || c.cap > cs * kKeysMax)) cs *= 2;
+  while (cs < 8 && ((units * cs <= sms && c.cap >= 4096 * cs) || c.cap > cs * kKeysMax)) cs *= 2;
   const int seg = ((c.cap + cs - 1) / cs + 3) & ~3;
   const bool in_smem = seg <= kKeysMax;
-  const int T = seg <= 4096 ? 512 : 1024;
+  const int T = seg <= 8192 ? 512 : 1024;
   const size_t smem = (size_t)kHist * 4 + (in_smem ? (size_t)seg * 4 : 0);
   auto kernel = in_smem ? paged_evict_kernel<true> : paged_evict_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kHist + kKeysMax) * 4));

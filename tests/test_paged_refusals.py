@@ -34,11 +34,35 @@ def test_header_and_binding_agree(b):
         assert b.bastion_status_string(code) != "unknown code"
 
 
+class _Struct(ctypes.Structure):
+    """bastion_paged_cache, as the header declares it."""
+    _fields_ = [("k_pool", vp), ("v_pool", vp), ("n_pages", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+                ("stride_slot", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("page_table", vp)] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "B", "Hkv", "D", "page_size", "max_pages")]
+
+
+def test_struct_layout(b):
+    """The binding packs the struct's bytes itself: the same size and members as a C struct of that declaration."""
+    src = open(os.path.join(ROOT, "include", "bastion_cache.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    body = re.search(r"typedef struct \{(.*?)\} bastion_paged_cache;", src, flags=re.S).group(1)
+    names = [n.strip(" *") for line in body.split(";") if line.strip() for n in line.strip().split(None, 1)[1].split(",")]
+    assert [n.split()[-1].strip("*") for n in names] == [n for n, _ in _Struct._fields_]
+    assert b._PAGED_CACHE.size == ctypes.sizeof(_Struct)
+    t = _tensors()
+    B, Hkv, D, cap, raw = b._cache(t["k"], t["v"], t["table"])
+    s = _Struct.from_buffer_copy(raw)
+    assert (B, Hkv, D, cap) == (2, 2, 128, 48)
+    assert (s.k_pool, s.v_pool, s.page_table) == tuple(t[n].data_ptr() for n in ("k", "v", "table"))
+    assert (s.n_pages, s.stride_page, s.stride_slot, s.stride_head) == (6, 16 * 2 * 128, 2 * 128, 128)
+    assert (s.dtype, s.B, s.Hkv, s.D, s.page_size, s.max_pages) == (1, 2, 2, 128, 16, 3)
+
+
 def _struct(b, **over):
     v = dict(k_pool=0x100000, v_pool=0x200000, n_pages=100, stride_page=16 * 8 * 128, stride_slot=8 * 128,
              stride_head=128, page_table=0x300000, dtype=1, B=4, Hkv=8, D=128, page_size=16, max_pages=20)
     v.update(over)
-    return ctypes.byref(b._PagedCacheStruct(*(v[n] for n, _ in b._PagedCacheStruct._fields_)))
+    return ctypes.byref(_Struct(*(v[n] for n, _ in _Struct._fields_)))
 
 
 APPEND = dict(k_new=vp(0x400000), v_new=vp(0x500000), n_rows=16, sb=16 * 1024, sr=1024, sh=128, rows=None, m=16,
