@@ -492,6 +492,8 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
     """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
     largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
     B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
+    if max(budget, n_sink, n_recent) >= 1 << 31:  # ctypes would cut it to 32 bits
+        raise BastionError("paged evict: budget, n_sink and n_recent must fit 32 bits")
     _need_all("seq_len n_seen seq_len_out status", (seq_len, n_seen, seq_len_out, status), torch.int32, (B,))
     shape = (B, Hkv, cap)
     _need_all("acc acc_out", (acc, acc_out), torch.float32, shape)

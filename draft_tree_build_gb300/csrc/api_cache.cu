@@ -46,7 +46,7 @@ Paged paged_args(const bastion_paged_cache &c) {
 namespace {
 
 constexpr int64_t kMaxCap = 1LL << 28;
-constexpr int kMaxB = 1024, kMaxUnits = 65536;
+constexpr int kMaxB = 1024, kMaxUnits = 65535;  // units: a grid's y
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 

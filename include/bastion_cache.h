@@ -22,13 +22,15 @@
  * [B, L_cap, Hkv, D] whose L_cap is a multiple of page_size is such a pool
  * with page_table[r][i] = r * L_cap / page_size + i: the same memory serves
  * bastion_tree_attention.
+ * A workspace that a call with BASTION_STATUS_TIMEOUT has used is cleared
+ * before its next use.
  * Page table entries past a request's last used page are not read.  Slots at
  * or past seq_len[r] never affect a result (they may hold NaN) and are left as
  * they are by every call except for the slots that append fills.
  *
  * Limits of every call: dtype BASTION_BF16 or BASTION_F16, D = 64 or 128,
  * page_size a power of two in [8, 128] (BASTION_ERR_UNSUPPORTED otherwise);
- * 1 <= B <= 1024, 1 <= Hkv, B * Hkv <= 65536, n_pages < 2^31,
+ * 1 <= B <= 1024, 1 <= Hkv, B * Hkv <= 65535, n_pages < 2^31,
  * max_pages * page_size <= 2^28; strides of dimensions longer than 1 are
  * multiples of 8 elements and at least D (BASTION_ERR_SIZE otherwise); pools
  * 16-byte aligned.

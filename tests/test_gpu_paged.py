@@ -195,6 +195,24 @@ def test_attention_strided_queries_and_shared_pool(cuda_lib):
     c.run().check()
 
 
+def test_attention_pools_in_any_order_of_dimensions(cuda_lib):
+    """Pages nearer to one another than a page's slots; heads outermost."""
+    for order in ((1, 0, 2, 3), (2, 0, 1, 3), (2, 1, 0, 3)):
+        c = Case([300, 17, 129], 8, 2, 128, 16, weights=True, seed=30, poison=float("nan"))
+        back = [order.index(i) for i in range(4)]
+        c.k, c.v = (x.permute(order).contiguous().permute(back) for x in (c.k, c.v))
+        assert not c.k.is_contiguous()
+        c.run().check()
+
+
+def test_attention_repeated_pages(cuda_lib):
+    """Requests that share pages, and one that lists a page twice."""
+    c = Case([300, 300, 64], 8, 2, 128, 16, weights=True, seed=31)
+    c.table[1] = c.table[0]
+    c.table[2, 1:4] = c.table[2, 0]
+    c.run().check()
+
+
 def test_attention_offsets_past_32_bits(cuda_lib):
     """Pools of more than 2^31 elements; the requests' pages lie at both ends."""
     from draft_tree_build_gb300 import bastion
@@ -444,6 +462,27 @@ def test_evict_long(cuda_lib, D, page, layout, dtype):
     c = Cache([9000, 5000, 2049], 9216 // page, Hkv=2, D=D, page=page, layout=layout, dtype=dtype, seed=page)
     _positions(c)
     c.evict(2048, 4, 256)
+    c.same()
+
+
+def test_evict_more_slots_than_a_cluster_holds(cuda_lib):
+    """380,000 slots: the keys of a head do not fit the shared memory of eight CTAs."""
+    c = Cache([380000, 379999], 2970, Hkv=1, D=64, page=128, seed=26)
+    _positions(c)
+    c.evict(379000, 4, 1000)
+    c.same()
+    c.evict(100, 4, 10, False)
+    c.same()
+
+
+def test_evict_no_spread_in_the_weights(cuda_lib):
+    """Long runs of equal and nearly equal weights: the deciding bin holds almost every slot."""
+    c = Cache([20000, 20000, 9000], 1250, Hkv=2, D=64, page=16, seed=27)
+    c.acc[0] = 0.0
+    c.acc[1] = 1.0 + torch.randint(0, 3000, c.acc[1].shape, generator=c.gen) * 2.0 ** -23
+    c.acc[2, :, ::2] = 0.5
+    _positions(c)
+    c.evict(4000, 4, 100)
     c.same()
 
 

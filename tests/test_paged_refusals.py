@@ -88,7 +88,7 @@ def _call(b, which, cache=None, **over):
 CACHE_REFUSALS = [
     (dict(k_pool=None), NULL), (dict(v_pool=None), NULL), (dict(page_table=None), NULL),
     (dict(dtype=0), DTYPE), (dict(dtype=7), DTYPE),
-    (dict(B=0), SIZE), (dict(B=1025), SIZE), (dict(Hkv=0), SIZE), (dict(B=1024, Hkv=65), SIZE),
+    (dict(B=0), SIZE), (dict(B=1025), SIZE), (dict(Hkv=0), SIZE), (dict(B=1024, Hkv=64), SIZE),
     (dict(n_pages=0), SIZE), (dict(n_pages=1 << 31), SIZE), (dict(max_pages=0), SIZE),
     (dict(max_pages=(1 << 24) + 1), SIZE), (dict(D=0), SIZE), (dict(page_size=0), SIZE),
     (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED), (dict(page_size=4), UNSUPPORTED),
@@ -140,7 +140,7 @@ def test_workspace_queries(b):
     assert w(4, 33, 8, 128, 4096, False) == w(4, 32, 8, 96, 4096, False) == w(4, 32, 1, 128, 4096, False) == 0
     assert w(4, 32, 8, 128, (1 << 28) + 1, False) == 0
     assert b.bastion_paged_evict_workspace_bytes(4, 8, 4096) > 0
-    assert b.bastion_paged_evict_workspace_bytes(1024, 65, 4096) == 0
+    assert b.bastion_paged_evict_workspace_bytes(1024, 64, 4096) == 0
 
 
 def _tensors(B=2, Hq=8, Hkv=2, D=128, page=16, pages=6, max_pages=3):
@@ -207,15 +207,17 @@ def test_binding_refuses_other_arguments(b):
         append()
 
     def evict(**kw):
-        a = dict(seq_len=t["lens"], n_seen=t["lens"], acc=t["acc"], pos=t["pos"])
+        a = dict(seq_len=t["lens"], n_seen=t["lens"], acc=t["acc"], pos=t["pos"], budget=8)
         a.update(kw)
-        b.bastion_paged_evict(t["k"], t["v"], t["table"], a["seq_len"], a["n_seen"], a["acc"], a["pos"], 8, 0, 0,
+        b.bastion_paged_evict(t["k"], t["v"], t["table"], a["seq_len"], a["n_seen"], a["acc"], a["pos"], a["budget"], 0, 0,
                               t["lens"], t["acc"], t["pos"], t["ws"], t["st"])
 
     with pytest.raises(b.BastionError, match="n_seen"):
         evict(n_seen=t["lens"].long())
     with pytest.raises(b.BastionError, match="acc"):
         evict(acc=t["acc"].double())
+    with pytest.raises(b.BastionError, match="32 bits"):
+        evict(budget=(1 << 32) + 8)
     with pytest.raises(b.BastionError, match="CUDA device"):
         evict()
     with pytest.raises(b.BastionError, match="n_pages"):
