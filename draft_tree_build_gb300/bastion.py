@@ -361,41 +361,38 @@ def bastion_verify_greedy_noalloc(target_logits, b, n_nodes, parent, token, argm
 _CACHE_DTYPES = {torch.bfloat16: BASTION_BF16, torch.float16: BASTION_F16}
 
 
-def _need(name, t, dtype, shape):
-    """A contiguous tensor of that type and shape (the library reads its bytes as such)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise BastionError(f"paged cache: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
-                           f"{list(t.shape)}, strides {t.stride()}")
-
-
-def _need_all(names, tensors, dtype, shape):
-    """_need for several tensors (None: left out) of one type and shape; names: a text, split when one fails."""
+def _need(names, dev, dtype, shape, *tensors):
+    """Contiguous tensors (None: left out) of one type and shape on device dev: the library reads their bytes as
+    such.  names: a text, split when one fails."""
     for i, t in enumerate(tensors):
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
-            _need(names.split()[i], t, dtype, shape)
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                              or not t.is_contiguous()):
+            name = names.split()[i]
+            if t.get_device() != dev:
+                raise BastionError(f"paged cache: {name} is on {t.device}, the page table on another device")
+            raise BastionError(f"paged cache: {name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
+                               f"{list(t.shape)}, strides {t.stride()}")
 
 
-def _on_device(stream, workspace, *tensors):
-    """All on the current CUDA device, where the launches go; the handle of the stream to launch on."""
-    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace)")
-    dev = workspace.get_device()
+def _launch_on(dev, stream, workspace):
+    """Checks the workspace and that dev is the current CUDA device, where the launches go; the stream's handle."""
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace) on the tensors' "
+                           "device")
     if dev < 0:
         raise BastionError("tensor must live on a CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise BastionError(f"paged cache: tensors on {t.device} and {workspace.device}")
     if dev != torch.cuda.current_device():
-        raise BastionError(f"paged cache: the tensors are on {workspace.device}, the current device is "
+        raise BastionError(f"paged cache: the tensors are on cuda:{dev}, the current device is "
                            f"cuda:{torch.cuda.current_device()}")
     # the current stream's handle without a Stream object, which costs 3 us to make
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _cache(k_pool, v_pool, page_table):
-    """The cache's struct; pools [n_pages, page_size, Hkv, D] of any strides (a head-major pool is a
-    transposed view), page_table [B, max_pages] int32."""
-    shape, st = k_pool.shape, k_pool.stride()
+    """Checks the cache; (device, B, Hkv, D, slots of a request, the struct's bytes, which ctypes passes by address).
+    Pools [n_pages, page_size, Hkv, D] of any strides (a head-major pool is a transposed view), page_table
+    [B, max_pages] int32."""
+    shape, st, dev = k_pool.shape, k_pool.stride(), page_table.get_device()
     if len(shape) != 4 or shape != v_pool.shape or k_pool.dtype is not v_pool.dtype:
         raise BastionError("paged cache: the pools must be [n_pages, page_size, Hkv, D], of one shape and dtype")
     dt = _CACHE_DTYPES.get(k_pool.dtype)
@@ -406,10 +403,13 @@ def _cache(k_pool, v_pool, page_table):
     table = page_table.shape
     if len(table) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
         raise BastionError("paged cache: page_table must be contiguous int32 [B, max_pages]")
-    # (B, Hkv, D, slots of a request, the struct's bytes, which ctypes passes by address)
-    B, max_pages, page, Hkv, D = table[0], table[1], shape[1], shape[2], shape[3]
-    return B, Hkv, D, max_pages * page, _PAGED_CACHE.pack(
-        k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2], page_table.data_ptr(), dt, B, Hkv, D, page,
+    if k_pool.get_device() != dev or v_pool.get_device() != dev:
+        raise BastionError(f"paged cache: pools on {k_pool.device} and {v_pool.device}, page_table on "
+                           f"{page_table.device}")
+    n_pages, page, Hkv, D = shape
+    B, max_pages = table
+    return dev, B, Hkv, D, max_pages * page, _PAGED_CACHE.pack(
+        k_pool.data_ptr(), v_pool.data_ptr(), n_pages, st[0], st[1], st[2], page_table.data_ptr(), dt, B, Hkv, D, page,
         max_pages)
 
 
@@ -426,27 +426,27 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     """k_new/v_new [B, n_rows, Hkv, D] (equal strides, last dim contiguous) enter the cache's next slots: the
     rows listed in rows [B, m] (a negative entry ends a list; Verify.accept_nodes fits), or the first n_new [B].
     seq_len_out may be seq_len, n_seen_out n_seen."""
-    B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
-    new, st = k_new.shape, k_new.stride()
+    dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
+    new, st, dtype = k_new.shape, k_new.stride(), k_pool.dtype
     if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != Hkv or new[3] != D \
-            or k_new.dtype is not k_pool.dtype or v_new.dtype is not k_pool.dtype:
+            or k_new.dtype is not dtype or v_new.dtype is not dtype:
         raise BastionError("paged append: k_new and v_new must be [B, n_rows, Hkv, D] of the pools' dtype")
     if st[3] != 1 or st != v_new.stride():
         raise BastionError("paged append: k_new and v_new must have equal strides and a contiguous last dimension")
+    if k_new.get_device() != dev or v_new.get_device() != dev:
+        raise BastionError("paged append: k_new and v_new must be on the pools' device")
     m = n_rows = new[1]
     if rows is not None:
         if rows.dim() != 2:
             raise BastionError("paged append: rows must be [B, m]")
         m = rows.shape[1]
-        _need("rows", rows, torch.int32, (B, m))
-    _need_all("seq_len seq_len_out status n_new n_seen n_seen_out",
-              (seq_len, seq_len_out, status, n_new, n_seen, n_seen_out), torch.int32, (B,))
-    if acc is not None:
-        _need("acc", acc, torch.float32, (B, Hkv, cap))
-    if pos is not None:
-        _need("pos", pos, torch.int32, (B, Hkv, cap))
-    st_cuda = _on_device(stream, workspace, k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, status, rows,
-                         n_new, acc, pos, n_seen, n_seen_out)
+        _need("rows", dev, torch.int32, (B, m), rows)
+    _need("seq_len seq_len_out status n_new n_seen n_seen_out", dev, torch.int32, (B,), seq_len, seq_len_out, status,
+          n_new, n_seen, n_seen_out)
+    if acc is not None or pos is not None:
+        _need("acc", dev, torch.float32, (B, Hkv, cap), acc)
+        _need("pos", dev, torch.int32, (B, Hkv, cap), pos)
+    st_cuda = _launch_on(dev, stream, workspace)
     rc = lib().bastion_paged_append(cache, k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
                                     _ptr(rows), m, _ptr(n_new), seq_len.data_ptr(), seq_len_out.data_ptr(),
                                     _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos), workspace.data_ptr(),
@@ -463,23 +463,25 @@ def bastion_paged_attention(q, k_pool, v_pool, page_table, seq_len, scale, out, 
                             acc=None, acc_out=None, stream=None):
     """q [B, Hq, D] (heads contiguous, any stride between requests), out [B, Hq, D] contiguous, lse [B, Hq]
     float32 or None; acc/acc_out [B, Hkv, max_pages * page_size] float32 or None (acc_out may be acc)."""
-    B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
-    qs, st = q.shape, q.stride()
-    if len(qs) != 3 or q.dtype is not k_pool.dtype or qs[0] != B or qs[2] != D:
+    dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
+    qs, st, dtype = q.shape, q.stride(), q.dtype
+    if len(qs) != 3 or dtype is not k_pool.dtype or qs[0] != B or qs[2] != D:
         raise BastionError("paged attention: q must be [B, Hq, D] of the pools' dtype")
     Hq = qs[1]
     if st[2] != 1 or (Hq > 1 and st[1] != D):
         raise BastionError("paged attention: the heads of q must be contiguous")
-    _need("out", out, q.dtype, qs)
-    _need_all("seq_len status", (seq_len, status), torch.int32, (B,))
+    if q.get_device() != dev:
+        raise BastionError("paged attention: q must be on the pools' device")
+    _need("out", dev, dtype, qs, out)
+    _need("seq_len status", dev, torch.int32, (B,), seq_len, status)
     if lse is not None:
-        _need("lse", lse, torch.float32, (B, Hq))
+        _need("lse", dev, torch.float32, (B, Hq), lse)
     if acc is not None or acc_out is not None:
-        _need_all("acc acc_out", (acc, acc_out), torch.float32, (B, Hkv, cap))
-    st_cuda = _on_device(stream, workspace, q, k_pool, v_pool, page_table, seq_len, out, status, lse, acc, acc_out)
-    rc = lib().bastion_paged_attention(cache, q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale,
-                                       out.data_ptr(), _ptr(lse), _ptr(acc), _ptr(acc_out), workspace.data_ptr(),
-                                       workspace.numel(), status.data_ptr(), st_cuda)
+        _need("acc acc_out", dev, torch.float32, (B, Hkv, cap), acc, acc_out)
+    st_cuda = _launch_on(dev, stream, workspace)
+    rc = lib().bastion_paged_attention(cache, q.data_ptr(), Hq, st[0], seq_len.data_ptr(), scale, out.data_ptr(),
+                                       _ptr(lse), _ptr(acc), _ptr(acc_out), workspace.data_ptr(), workspace.numel(),
+                                       status.data_ptr(), st_cuda)
     _check(rc, "bastion_paged_attention")
 
 
@@ -491,19 +493,17 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
                         seq_len_out, acc_out, pos_out, workspace, status, stream=None):
     """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
     largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
-    B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
+    dev, B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
     if max(budget, n_sink, n_recent) >= 1 << 31:  # ctypes would cut it to 32 bits
         raise BastionError("paged evict: budget, n_sink and n_recent must fit 32 bits")
-    _need_all("seq_len n_seen seq_len_out status", (seq_len, n_seen, seq_len_out, status), torch.int32, (B,))
-    shape = (B, Hkv, cap)
-    _need_all("acc acc_out", (acc, acc_out), torch.float32, shape)
-    _need_all("pos pos_out", (pos, pos_out), torch.int32, shape)
-    st_cuda = _on_device(stream, workspace, k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, seq_len_out,
-                         acc_out, pos_out, status)
-    rc = lib().bastion_paged_evict(cache, seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(),
-                                   pos.data_ptr(), budget, n_sink, n_recent, seq_len_out.data_ptr(),
-                                   acc_out.data_ptr(), pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   status.data_ptr(), st_cuda)
+    _need("seq_len n_seen seq_len_out status", dev, torch.int32, (B,), seq_len, n_seen, seq_len_out, status)
+    _need("acc acc_out", dev, torch.float32, (B, Hkv, cap), acc, acc_out)
+    _need("pos pos_out", dev, torch.int32, (B, Hkv, cap), pos, pos_out)
+    st_cuda = _launch_on(dev, stream, workspace)
+    rc = lib().bastion_paged_evict(cache, seq_len.data_ptr(), n_seen.data_ptr(), acc.data_ptr(), pos.data_ptr(),
+                                   budget, n_sink, n_recent, seq_len_out.data_ptr(), acc_out.data_ptr(),
+                                   pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr(),
+                                   st_cuda)
     _check(rc, "bastion_paged_evict")
 
 

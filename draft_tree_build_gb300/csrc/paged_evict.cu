@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     }
     __syncthreads();
     // each warp's run of bins, the first warp's topmost: this CTA's entries
-    const int run = max(bins / warps, 128), runs = bins / run;
+    const int run = (bins + 128 * warps - 1) / (128 * warps) * 128, runs = (bins + run - 1) / run;
     uint32_t sum = 0;
     if (warp < runs)
-      for (int b = bins - warp * run - 4 * lane - 4; b >= bins - (warp + 1) * run; b -= 128) {
+      for (int b = bins - warp * run - 4 * lane - 4; b >= max(bins - (warp + 1) * run, 0); b -= 128) {
         const uint4 x = *reinterpret_cast<const uint4 *>(h + b);
         sum += x.x + x.y + x.z + x.w;
       }
@@ -494,8 +494,8 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return BASTION_ERR_LAUNCH;
-  // CTAs of a unit: as many as the device has room for at one CTA per SM, with 2,048 slots each at least; more
-  // where their keys would not fit
+  // CTAs of a unit: up to two an SM over all units, each with 2,048 slots at least (32 units of 8,200 slots: 12.3 us
+  // so, 14.7 with half as many slots a CTA, 13.9 with twice as many); more where their keys would not fit
   int cs = 1;
   while (cs < 8 && ((units * cs <= sms && c.cap >= 4096 * cs) || c.cap > cs * kKeysMax)) cs *= 2;
   const int seg = ((c.cap + cs - 1) / cs + 3) & ~3;

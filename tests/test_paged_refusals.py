@@ -50,9 +50,9 @@ def test_struct_layout(b):
     assert [n.split()[-1].strip("*") for n in names] == [n for n, _ in _Struct._fields_]
     assert b._PAGED_CACHE.size == ctypes.sizeof(_Struct)
     t = _tensors()
-    B, Hkv, D, cap, raw = b._cache(t["k"], t["v"], t["table"])
+    dev, B, Hkv, D, cap, raw = b._cache(t["k"], t["v"], t["table"])
     s = _Struct.from_buffer_copy(raw)
-    assert (B, Hkv, D, cap) == (2, 2, 128, 48)
+    assert (dev, B, Hkv, D, cap) == (-1, 2, 2, 128, 48)
     assert (s.k_pool, s.v_pool, s.page_table) == tuple(t[n].data_ptr() for n in ("k", "v", "table"))
     assert (s.n_pages, s.stride_page, s.stride_slot, s.stride_head) == (6, 16 * 2 * 128, 2 * 128, 128)
     assert (s.dtype, s.B, s.Hkv, s.D, s.page_size, s.max_pages) == (1, 2, 2, 128, 16, 3)
