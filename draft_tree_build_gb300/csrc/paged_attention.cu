@@ -755,11 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (w.n - w.t * kTileKeys < kTileKeys) {  // the rows past the end: zeros, whatever the page holds there
         ok = __all_sync(kFull, ok && wait_bar(&ms.v_full[vs], (uint32_t)vph, abort, st));
-        if (ok && !live) {
-          unsigned char *row = smem + Lay::kOffV + vs * Lay::kTile + kt * 128;
+        if (ok) {  // consecutive threads on consecutive 16 bytes: a row a thread would hit one bank 32 times over
+          unsigned char *tile = smem + Lay::kOffV + vs * Lay::kTile;
+#pragma unroll 1
+          for (int x = (w.n - w.t * kTileKeys) * 128 + kt * 16; x < kTileKeys * 128; x += 128 * 16)
 #pragma unroll
-          for (int x = 0; x < kBlocks * 8; ++x)
-            *reinterpret_cast<uint4 *>(row + (x >> 3) * Lay::kBlock + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int blk = 0; blk < kBlocks; ++blk)
+              *reinterpret_cast<uint4 *>(tile + blk * Lay::kBlock + x) = make_uint4(0, 0, 0, 0);
         }
       }
       if (++vs == kStages) {
