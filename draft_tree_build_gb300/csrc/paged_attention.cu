@@ -105,7 +105,9 @@ struct Layout {
 struct Misc {
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_empty[2], mma_done;
+  uint2 warp_sum[8];
   float xm[4][16], xl[4][16];
+  int li0, off0, f0, f1;
   uint32_t last;
   uint32_t tmem;
   int abort;
@@ -419,20 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 64;" ::"r"(smem_u32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  tc_fence_before();
-  __syncthreads();  // the barriers and TMEM are ready
-  tc_fence_after();
-  const uint32_t tmem = ms.tmem;
   griddep_wait();
   griddep_launch_dependents();
 
   // ------------------------------------------------------------ this CTA's share
-  // Every warp works it out for itself, so that none waits for another; a lane has consecutive
-  // requests.  Prefix sums of (requests with tiles, tiles), then the requests' list, which all
-  // warps write alike, and the lanes that hold the share's begin and end.
-  const int chunk = (c.B + 31) / 32, r0 = lane * chunk, r1 = min(c.B, r0 + chunk);
+  // prefix sums over the requests of (requests with tiles, tiles); a thread has consecutive requests
+  const int chunk = (c.B + kThreads - 1) / kThreads, r0 = tid * chunk, r1 = min(c.B, r0 + chunk);
   int cnt = 0, til = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int b = r0; b < r1; ++b) {
     const int n = a.seq_len[b];
     if ((n < 0 || n > c.cap) && blockIdx.x == 0) atomicOr(&a.status[b], BASTION_STATUS_KV_OVERFLOW);
@@ -440,35 +436,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     cnt += m > 0;
     til += (m + kTileKeys - 1) / kTileKeys;
   }
-  int rank = cnt, at = til;
+  int cnt_i = cnt, til_i = til;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, rank, o), y = __shfl_up_sync(kFull, at, o);
+    const int x = __shfl_up_sync(kFull, cnt_i, o), y = __shfl_up_sync(kFull, til_i, o);
     if (lane >= o) {
-      rank += x;
-      at += y;
+      cnt_i += x;
+      til_i += y;
     }
   }
-  const int total = __shfl_sync(kFull, at, 31) * c.Hkv;
-  rank -= cnt;
-  at = (at - til) * c.Hkv;
+  if (lane == 31) ms.warp_sum[warp] = make_uint2((unsigned)cnt_i, (unsigned)til_i);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  int rank = cnt_i - cnt, at = til_i - til, total = 0;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const uint2 y = ms.warp_sum[x];
+    if (x < warp) {
+      rank += (int)y.x;
+      at += (int)y.y;
+    }
+    total += (int)y.y;
+  }
+  total *= c.Hkv;
+  at *= c.Hkv;
   Shares sh;
   sh.n = min((int)gridDim.x, total);
   sh.quot = sh.n > 0 ? total / sh.n : 0;
   sh.big = total - sh.quot * sh.n;
+  const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
   const bool busy = (int)blockIdx.x < sh.n;
-  int f0 = 0, share = 0, li0 = 0, off0 = 0;
+  if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
   if (busy) {
-    const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
-    int f1 = total;
-    bool has0 = false, has1 = false;
 #pragma unroll 1
     for (int b = r0; b < r1; ++b) {
       const int n = clamped_len(c, a, b), t = (n + kTileKeys - 1) / kTileKeys, end = at + t * c.Hkv;
       if (n == 0) continue;
       list[rank] = make_int2(b, n);
 #pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
         // (f - at) % t: the quotient is below Hkv <= 2^16, so that its estimate is off by one at most
@@ -476,28 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         off += off < 0 ? t : off >= t ? -t : 0;
         const int to = Shares::moved(f, off, t);
         if (k) {
-          has1 = true;
-          f1 = to;
+          ms.f1 = to;
         } else {
-          has0 = true;
-          f0 = to;
-          li0 = to == end ? rank + 1 : rank;  // the next request's begin
-          off0 = to == end ? 0 : to - at;
+          ms.f0 = to;
+          ms.li0 = to == end ? rank + 1 : rank;  // the next request's begin
+          ms.off0 = to == end ? 0 : to - at;
         }
       }
       ++rank;
       at = end;
     }
-    const int l0 = __ffs(__ballot_sync(kFull, has0)) - 1, l1 = __ffs(__ballot_sync(kFull, has1)) - 1;
-    f0 = __shfl_sync(kFull, f0, l0);  // b0 < total: some lane has it
-    li0 = __shfl_sync(kFull, li0, l0);
-    off0 = __shfl_sync(kFull, off0, l0);
-    if (l1 >= 0) f1 = __shfl_sync(kFull, f1, l1);  // else the share ends with the batch
-    share = f1 - f0;
-    __syncwarp();
   }
+  __syncthreads();
+  const int f0 = ms.f0;
   Walk<true> w;
-  w.start(list, li0, off0, share);
+  w.start(list, ms.li0, __shfl_sync(kFull, ms.off0, 0), __shfl_sync(kFull, busy ? ms.f1 - f0 : 0, 0));
 
   if (warp < 2) {
     // ------------------------------------------------------------ TMA: warp 0 keys, warp 1 values
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // reads' latency never holds up the copies.  Lane: page lane % ppt of the batch's tile lane / ppt.
     const int psh = 7 - c.shift, ppt = 1 << psh, batch = min(kBatch, 32 >> psh);
     Walk<false> lw;  // this lane's tile
-    lw.start(list, li0, off0, share);
+    lw.start(list, ms.li0, ms.off0, w.left);
     int lead = lane >> psh;
     auto next_entry = [&]() {  // walks on by `lead` tiles and reads there
 #pragma unroll 1
@@ -777,9 +778,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.last()) continue;
 
       // ---------------------------------------------------------- the segment's end
-      const bool whole = t_first == 0 && w.t == w.tiles - 1;
-      const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
-      const int c0 = whole ? 0 : sh.first_cta(u0), np = whole ? 1 : sh.last_cta(u1) - c0 + 1;  // its unit's CTAs
       const float part_l = warp_all<GP, false>(l, lane);
       if ((lane & (32 / GP - 1)) == 0) ms.xl[quad][lane / (32 / GP)] = part_l;
       ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)(i >> 1) & 1u, abort, st));
@@ -798,12 +796,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // the next segment's products overwrite O after this thread's next p_full arrival
 #pragma unroll
       for (int h = 0; h < GP; ++h) l[h] = (ms.xl[0][h] + ms.xl[1][h]) + (ms.xl[2][h] + ms.xl[3][h]);
-      bool write = whole;
+      bool write = t_first == 0 && w.t == w.tiles - 1;
       if (!write) {
         // One of several parts of the unit.  Parts are joined in groups of kGroup consecutive
         // CTAs, the groups' results then as parts of their own; each time by whoever arrives
         // last, in the parts' order.  A CTA's first segment has slot 2 * cta, a later one the
         // next; only a unit's first CTA can have begun another unit before.
+        const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
+        const int c0 = sh.first_cta(u0), np = sh.last_cta(u1) - c0 + 1;
         auto slot_of = [&](int x) { return x == 0 ? 2 * c0 + 1 : 2 * (c0 + x); };  // of part x
         auto put = [&](int slot) {
           float *part = a.parts + (size_t)slot * kPartFloats;
