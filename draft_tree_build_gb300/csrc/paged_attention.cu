@@ -778,6 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.last()) continue;
 
       // ---------------------------------------------------------- the segment's end
+      const bool whole = t_first == 0 && w.t == w.tiles - 1;
+      const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
+      const int c0 = whole ? 0 : sh.first_cta(u0), np = whole ? 1 : sh.last_cta(u1) - c0 + 1;  // its unit's CTAs
       const float part_l = warp_all<GP, false>(l, lane);
       if ((lane & (32 / GP - 1)) == 0) ms.xl[quad][lane / (32 / GP)] = part_l;
       ok = __all_sync(kFull, ok && wait_bar(&ms.pv_done[s], (uint32_t)(i >> 1) & 1u, abort, st));
@@ -796,14 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // the next segment's products overwrite O after this thread's next p_full arrival
 #pragma unroll
       for (int h = 0; h < GP; ++h) l[h] = (ms.xl[0][h] + ms.xl[1][h]) + (ms.xl[2][h] + ms.xl[3][h]);
-      bool write = t_first == 0 && w.t == w.tiles - 1;
+      bool write = whole;
       if (!write) {
         // One of several parts of the unit.  Parts are joined in groups of kGroup consecutive
         // CTAs, the groups' results then as parts of their own; each time by whoever arrives
         // last, in the parts' order.  A CTA's first segment has slot 2 * cta, a later one the
         // next; only a unit's first CTA can have begun another unit before.
-        const int u0 = f0 + i - w.t, u1 = u0 + w.tiles;
-        const int c0 = sh.first_cta(u0), np = sh.last_cta(u1) - c0 + 1;
         auto slot_of = [&](int x) { return x == 0 ? 2 * c0 + 1 : 2 * (c0 + x); };  // of part x
         auto put = [&](int slot) {
           float *part = a.parts + (size_t)slot * kPartFloats;
