@@ -36,6 +36,15 @@
 // With weights, the scores (in base 2) are kept and a second kernel adds
 // sum_h exp2(s - lse_h) to each slot's accumulated weight.
 //
+// Measured, cold caches, 32 query heads on 8 KV heads, D = 128: 64 requests of up to 16,384
+// tokens (2.4 GB) 368 us, 98% of the copy bandwidth; 8 of 4,096 (134 MB) 28.4 us, 70%; one of
+// 131,072 (537 MB) 89 us, 89%; one of 300 (1.2 MB) 6.8 us.  What is left of the small ones is
+// latency: a launch (2.2 us), the dependent reads of lengths and page table before the first copy
+// (1.5 us), the last tile's chain of products and softmax (1 us) and, where a unit is shared, the
+// join (1.4 us).  The accumulated weights add 5 us to 32 requests of 2,065 tokens (53 us) and 12 us to 8 of
+// up to 32,768 (70 us): the scores, stored once and read back from L2, and the second launch.
+// With D = 64 the tile's 12 products and the softmax have half the time: 98% all the same (2.6 GB).
+//
 // Every wait is bounded (~1 s); after one ran out the CTA flags the request,
 // waits for its own copies and products (bounded), frees its TMEM and returns.
 #include <cuda.h>
