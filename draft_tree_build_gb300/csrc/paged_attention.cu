@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar128();
           if (!ms.last) break;
           // o, l, ref = parts first, first + step, ... joined
-          constexpr int kLoads = 32 / GP, kRows = 128 / GP;  // parts whose loads are in flight together
+          constexpr int kLoads = GP == 16 ? 4 : 32 / GP, kRows = 128 / GP;  // parts whose loads are in flight together
           const int fh = kt & (GP - 1), fy = kt / GP;
           // the parts' references and sums, then their factors; in the P buffers, which no product reads now
           float2(*jml)[GP] = reinterpret_cast<float2(*)[GP]>(smem + Lay::kOffP);
