@@ -46,21 +46,22 @@ Paged paged_args(const bastion_paged_cache &c) {
 namespace {
 
 constexpr int64_t kMaxCap = 1LL << 28;
-constexpr int kMaxB = 1024, kMaxUnits = 65535;  // units: a grid's y
+constexpr int kMaxB = bastion::kMaxRequests, kMaxHeads = 65535;  // B * Hkv: a grid's y
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 bool stride_ok(int64_t n, int64_t s, int64_t least) { return n == 1 || (s >= least && s % 8 == 0 && s < (1LL << 38)); }
 
 bool sizes_ok(int B, int Hkv, int64_t cap) {
-  return B >= 1 && B <= kMaxB && Hkv >= 1 && (int64_t)B * Hkv <= kMaxUnits && cap >= 1 && cap <= kMaxCap;
+  return B >= 1 && B <= kMaxB && Hkv >= 1 && (int64_t)B * Hkv <= kMaxHeads && cap >= 1 && cap <= kMaxCap;
 }
 
 // Whether an output is its input's array or disjoint from it.
-bool same_or_apart(const void *a, const void *b, size_t bytes) {
+bool apart(const void *a, const void *b, size_t bytes) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x == y || x + bytes <= y || y + bytes <= x;
+  return x + bytes <= y || y + bytes <= x;
 }
+bool same_or_apart(const void *a, const void *b, size_t bytes) { return a == b || apart(a, b, bytes); }
 
 size_t slots_bytes(const bastion_paged_cache *c) {  // of acc and of pos
   return (size_t)c->B * c->Hkv * (size_t)c->max_pages * c->page_size * 4;
@@ -93,7 +94,7 @@ extern "C" {
 
 size_t bastion_paged_append_workspace_bytes(int B) {
   if (B < 1 || B > kMaxB) return 0;
-  return (size_t)kMaxB * sizeof(uint32_t);  // arrival counters, the same for every B: calls of all sizes share it
+  return (size_t)kMaxB * sizeof(uint32_t);  // arrival counters
 }
 
 int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, const void *v_new,
@@ -170,7 +171,8 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
   if (!aligned(workspace, 256) || !aligned(acc, 16) || !aligned(pos, 16) || !aligned(acc_out, 16) ||
       !aligned(pos_out, 16))
     return BASTION_ERR_ALIGN;
-  if (!same_or_apart(seq_len, seq_len_out, (size_t)cache->B * 4) ||
+  const size_t lens = (size_t)cache->B * 4;
+  if (!same_or_apart(seq_len, seq_len_out, lens) || !apart(n_seen, seq_len_out, lens) ||
       !same_or_apart(acc, acc_out, slots_bytes(cache)) || !same_or_apart(pos, pos_out, slots_bytes(cache)))
     return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_evict_workspace_bytes(cache->B, cache->Hkv,

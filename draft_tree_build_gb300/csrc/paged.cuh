@@ -6,6 +6,15 @@
 
 namespace bastion {
 
+// Every call's arrival counters lie in the first bytes of its workspace and
+// nothing else does, so that calls of all sizes, and of all three kinds, can
+// share one: 2 * kMaxParts counters of groups, then one per (request, KV head).
+constexpr int kMaxParts = 192;      // CTAs of an attention launch, at most
+constexpr int kMaxUnits = 65536;    // B * Hkv
+constexpr int kMaxRequests = 1024;  // B
+constexpr size_t kCounterBytes = (2 * kMaxParts + kMaxUnits) * sizeof(uint32_t);
+static_assert(kCounterBytes % 256 == 0 && kCounterBytes >= kMaxRequests * sizeof(uint32_t), "counters");
+
 struct Paged {
   uint16_t *k, *v;
   int64_t n_pages, st_page, st_slot, st_head;

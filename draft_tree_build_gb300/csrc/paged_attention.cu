@@ -59,9 +59,6 @@ namespace bastion {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kMaxUnits = 65536;  // B * Hkv: arrival counters
-constexpr int kMaxB = 1024;
-constexpr int kMaxGrid = 192;     // CTAs that may hold parts
 constexpr int kGroup = 24;        // parts joined at a time, at most
 constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their references and sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -79,8 +76,8 @@ struct AttendArgs {
   float *lse;
   const float *acc;
   float *acc_out;
-  uint32_t *arrived;  // [2 * kMaxGrid + kMaxUnits], zero between calls
-  float *parts;       // [2 * kMaxGrid, kPartFloats]
+  uint32_t *arrived;  // [2 * kMaxParts + kMaxUnits], zero between calls
+  float *parts;       // [2 * kMaxParts, kPartFloats]
   float *lse2;        // [B, Hq] base-2 log of the sum, of the scores in base 2
   float *scores;      // [B, Hkv, tiles, G, 128], in base 2
   int tiles_cap;
@@ -108,7 +105,7 @@ struct Layout {
   static constexpr uint32_t kOffQ = 2 * kStages * kTile;
   static constexpr uint32_t kOffP = kOffQ + 2 * kQ;
   static constexpr uint32_t kOffList = kOffP + 2 * kP;
-  static constexpr uint32_t kOffMisc = kOffList + kMaxB * 8;
+  static constexpr uint32_t kOffMisc = kOffList + kMaxRequests * 8;
 };
 
 struct Misc {
@@ -907,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           first = 0;
           step = size;
           count = groups;
-          counter = &a.arrived[2 * kMaxGrid + w.r * c.Hkv + w.g];
+          counter = &a.arrived[2 * kMaxParts + w.r * c.Hkv + w.g];
         }
       }
       if (write) {
@@ -1032,16 +1029,14 @@ cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int grid, 
                     : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
 }
 
-constexpr size_t kArrivedBytes = (2 * kMaxGrid + kMaxUnits) * sizeof(uint32_t);
-constexpr size_t kPartsBytes = (size_t)2 * kMaxGrid * kPartFloats * sizeof(float);
+constexpr size_t kPartsBytes = (size_t)2 * kMaxParts * kPartFloats * sizeof(float);
 
 }  // namespace
 
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t cap, int weights) {
   (void)Hkv;
   (void)D;
-  // the counters lie at the same place for every size, so that calls of all sizes share a workspace
-  size_t n = kArrivedBytes + up256(kPartsBytes);
+  size_t n = kCounterBytes + up256(kPartsBytes);
   if (weights) {
     n += up256((size_t)B * Hq * sizeof(float));
     n += (size_t)B * Hq * (size_t)((cap + kTileKeys - 1) / kTileKeys) * kTileKeys * sizeof(float);
@@ -1066,7 +1061,7 @@ int launch_paged_attention(const Paged &c, bool half, const void *q, int Hq, int
   a.tiles_cap = (c.cap + kTileKeys - 1) / kTileKeys;
   char *at = static_cast<char *>(ws);
   a.arrived = reinterpret_cast<uint32_t *>(at);
-  a.parts = reinterpret_cast<float *>(at += kArrivedBytes);
+  a.parts = reinterpret_cast<float *>(at += kCounterBytes);
   a.lse2 = reinterpret_cast<float *>(at += up256(kPartsBytes));
   a.scores = acc ? reinterpret_cast<float *>(at + up256((size_t)c.B * Hq * 4)) : nullptr;
   a.swap = c.Hkv > 1 && c.st_head < c.st_slot;
@@ -1078,7 +1073,7 @@ int launch_paged_attention(const Paged &c, bool half, const void *q, int Hq, int
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return BASTION_ERR_LAUNCH;
   const int64_t most = (int64_t)c.B * c.Hkv * a.tiles_cap;  // tiles, at most
-  const int sm_grid = sms < kMaxGrid ? sms : kMaxGrid, grid = most < sm_grid ? (int)most : sm_grid;
+  const int sm_grid = sms < kMaxParts ? sms : kMaxParts, grid = most < sm_grid ? (int)most : sm_grid;
   cudaError_t e = half ? launch_half<true>(mk, mv, grid, c, a, stream) : launch_half<false>(mk, mv, grid, c, a, stream);
   if (e == cudaSuccess && acc)
     e = launch_pdl(paged_weights_kernel,

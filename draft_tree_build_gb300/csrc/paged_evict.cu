@@ -36,7 +36,6 @@ constexpr int kNearMoves = 512;
 constexpr int kMaxCluster = 8;
 constexpr int kKeysMax = 45056;  // keys a CTA keeps in shared memory
 constexpr int kMovesWarp = 8;    // moves a warp has in flight
-constexpr int kMaxRequests = 1024;
 
 struct EvictArgs {
   const int32_t *seq_len, *n_seen;
@@ -469,8 +468,8 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
 }  // namespace
 
 size_t paged_evict_workspace_bytes(int B, int Hkv, int64_t cap) {
-  // counters, at the same place for every size; at most cap / 2 moves: targets lie below budget, sources past it
-  return kMaxRequests * sizeof(uint32_t) + (size_t)B * Hkv * (size_t)(cap / 2) * sizeof(int2);
+  // at most cap / 2 moves: targets lie below budget, sources at or past it
+  return kCounterBytes + (size_t)B * Hkv * (size_t)(cap / 2) * sizeof(int2);
 }
 
 int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_seen, const float *acc,
@@ -490,7 +489,7 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
   a.acc_out = acc_out;
   a.pos_out = pos_out;
   a.arrived = static_cast<uint32_t *>(ws);
-  a.moves = reinterpret_cast<int2 *>(static_cast<char *>(ws) + kMaxRequests * sizeof(uint32_t));
+  a.moves = reinterpret_cast<int2 *>(static_cast<char *>(ws) + kCounterBytes);
   a.copy = acc_out != acc || pos_out != pos;
   a.status = status;
   int dev = 0, sms = 0;

@@ -22,8 +22,9 @@
  * [B, L_cap, Hkv, D] whose L_cap is a multiple of page_size is such a pool
  * with page_table[r][i] = r * L_cap / page_size + i: the same memory serves
  * bastion_tree_attention.
- * A workspace that a call with BASTION_STATUS_TIMEOUT has used is cleared
- * before its next use.
+ * One workspace that is large enough for each may serve all three calls, at
+ * all sizes, one after the other.  A workspace that a call with
+ * BASTION_STATUS_TIMEOUT has used is cleared before its next use.
  * Page table entries past a request's last used page are not read.  Slots at
  * or past seq_len[r] never affect a result (they may hold NaN) and are left as
  * they are by every call except for the slots that append fills.
@@ -143,7 +144,8 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
  * seq_len_out   [B]: min(seq_len, budget).
  * acc_out, pos_out: slots below min(seq_len, budget) are written, the others
  *               left as they are.
- * Each output is its input's array or disjoint from every input.
+ * Each output is its input's array or disjoint from every input
+ * (BASTION_ERR_UNSUPPORTED where seq_len_out overlaps n_seen).
  * Limits: 1 <= budget, n_sink, n_recent >= 0, n_sink + n_recent <= budget
  * (BASTION_ERR_SIZE).
  * Workspace: bastion_paged_evict_workspace_bytes(B, Hkv,

@@ -253,6 +253,24 @@ def test_attention_repeats_bit_for_bit_and_shares_a_workspace(cuda_lib):
         assert torch.equal(a, b)
 
 
+def test_one_workspace_serves_all_calls(cuda_lib):
+    """Attention, eviction and append in turn on one workspace, whatever they leave in it."""
+    from draft_tree_build_gb300 import bastion
+    a = Case([20000, 3, 5000], 32, 8, weights=True, seed=40)
+    c = Cache([900, 700, 300, 40], 130, Hkv=8, D=64, page=8, seed=41)
+    _positions(c)
+    ws = bastion.workspace(max(a.ws.numel(), c.ws.numel()), dev())
+    c.ws = ws
+    for budget in (600, 350, 60):
+        a.run(ws)
+        c.evict(budget, 2, 20)
+        c.append(*c.rows(5))
+        a.run(ws)
+        a.check()
+        c.same()
+    assert int(c.status.sum()) == 0
+
+
 def test_attention_weights_in_place(cuda_lib):
     c = Case([300, 0, 77], 8, 4, weights=True, seed=15).run()
     acc = c.acc.clone()

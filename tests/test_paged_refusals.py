@@ -126,7 +126,7 @@ def test_cache_refusals(b, which, over, code):
     ("evict", dict(sink=40, recent=25), SIZE), ("evict", dict(ws_bytes=64), WORKSPACE),
     ("evict", dict(acc_out=vp(0x10000010)), UNSUPPORTED), ("evict", dict(acc=vp(0x10000004)), ALIGN),
     ("evict", dict(pos_out=vp(0x20000008)), ALIGN), ("attend", dict(acc=vp(0x10000008)), ALIGN), ("evict", dict(pos_out=vp(0x1fffff00)), UNSUPPORTED),
-    ("evict", dict(ws=vp(0xa00080)), ALIGN),
+    ("evict", dict(ws=vp(0xa00080)), ALIGN), ("evict", dict(n_seen=vp(0x400000)), UNSUPPORTED),
 ])
 def test_call_refusals(b, which, over, code):
     assert _call(b, which, **over) == code
