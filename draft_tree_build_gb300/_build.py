@@ -8,6 +8,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libbastion.so")
+MARSHAL = os.path.join(BUILD, "bastion_marshal.so")  # csrc/marshal.c, a CPython extension
 SOURCES = ["api.cu", "topk_marginals.cu", "build_tree.cu", "verify_greedy.cu", "tree_attention.cu",
            "verify_noalloc.cu", "verify_sample.cu", "calibrate.cu",
            "build_tree_mixture.cu", "lm_head_topk.cu",
@@ -34,11 +36,12 @@ def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")]
+    files.append(os.path.join(CSRC, "marshal.c"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -61,8 +64,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def marshal():
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        r = subprocess.run(["gcc", "-O2", "-std=gnu11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I",
+                            sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed for marshal.c:\n{r.stderr[-4000:]}")
+        os.replace(tmp, MARSHAL)
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        m = ex.submit(marshal)
         objs = list(ex.map(one, SOURCES))
+        m.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)

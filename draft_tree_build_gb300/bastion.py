@@ -7,6 +7,8 @@ fallback path: if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 from dataclasses import dataclass
@@ -60,6 +62,18 @@ _PAGED_CACHE = struct.Struct("@PPqqqqPiiiiii")
 
 
 _lib = None
+_marshal = None  # the paged cache's short way past ctypes (csrc/marshal.c), loaded with the library
+
+
+def _load_marshal(L):
+    loader = importlib.machinery.ExtensionFileLoader("bastion_marshal", _build.MARSHAL)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("bastion_marshal", loader))
+    loader.exec_module(m)
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    m.init(torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8, torch._C._cuda_getDevice,
+           torch._C._cuda_getCurrentRawStream, address(L.bastion_paged_append), address(L.bastion_paged_attention),
+           address(L.bastion_paged_evict))
+    return m
 
 
 def library_path() -> str:
@@ -68,7 +82,7 @@ def library_path() -> str:
 
 def lib(build_if_missing: bool = True):
     """Load libbastion.so (building it in-tree first if it is missing or stale)."""
-    global _lib
+    global _lib, _marshal
     if _lib is not None:
         return _lib
     if build_if_missing and not _build.up_to_date():
@@ -129,6 +143,7 @@ def lib(build_if_missing: bool = True):
     L.bastion_paged_evict_workspace_bytes.argtypes = [i32, i32, i64]
     L.bastion_paged_evict.restype = i32
     L.bastion_paged_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
+    _marshal = _load_marshal(L)
     _lib = L
     return L
 
@@ -355,8 +370,9 @@ def bastion_verify_greedy_noalloc(target_logits, b, n_nodes, parent, token, argm
 
 # --------------------------------------------------------------------------- paged cache
 
-# These calls take a few microseconds on the GPU, so that what the host spends on one counts: the checks below
-# compare integers and shapes without building new objects.
+# These calls take a few microseconds on the GPU, so that what the host spends on one counts: a call whose arguments
+# are right goes through csrc/marshal.c, which checks them and calls the library; any other comes back here, where the
+# same checks say what is wrong.
 
 _CACHE_DTYPES = {torch.bfloat16: BASTION_BF16, torch.float16: BASTION_F16}
 
@@ -426,6 +442,11 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     """k_new/v_new [B, n_rows, Hkv, D] (equal strides, last dim contiguous) enter the cache's next slots: the
     rows listed in rows [B, m] (a negative entry ends a list; Verify.accept_nodes fits), or the first n_new [B].
     seq_len_out may be seq_len, n_seen_out n_seen."""
+    if _marshal is not None:
+        rc = _marshal.append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, workspace, status, rows,
+                             n_new, acc, pos, n_seen, n_seen_out, stream)
+        if rc is not None:
+            return _check(rc, "bastion_paged_append")
     dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
     new, st, dtype = k_new.shape, k_new.stride(), k_pool.dtype
     if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != Hkv or new[3] != D \
@@ -463,6 +484,11 @@ def bastion_paged_attention(q, k_pool, v_pool, page_table, seq_len, scale, out, 
                             acc=None, acc_out=None, stream=None):
     """q [B, Hq, D] (heads contiguous, any stride between requests), out [B, Hq, D] contiguous, lse [B, Hq]
     float32 or None; acc/acc_out [B, Hkv, max_pages * page_size] float32 or None (acc_out may be acc)."""
+    if _marshal is not None:
+        rc = _marshal.attention(q, k_pool, v_pool, page_table, seq_len, scale, out, workspace, status, lse, acc, acc_out,
+                                stream)
+        if rc is not None:
+            return _check(rc, "bastion_paged_attention")
     dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
     qs, st, dtype = q.shape, q.stride(), q.dtype
     if len(qs) != 3 or dtype is not k_pool.dtype or qs[0] != B or qs[2] != D:
@@ -493,6 +519,11 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
                         seq_len_out, acc_out, pos_out, workspace, status, stream=None):
     """Every request and KV head keeps budget slots: those of the n_sink first and n_recent last tokens, then the
     largest acc.  acc/pos [B, Hkv, max_pages * page_size]; each output may be its input."""
+    if _marshal is not None:
+        rc = _marshal.evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, budget, n_sink, n_recent, seq_len_out,
+                            acc_out, pos_out, workspace, status, stream)
+        if rc is not None:
+            return _check(rc, "bastion_paged_evict")
     dev, B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
     if max(budget, n_sink, n_recent) >= 1 << 31:  # ctypes would cut it to 32 bits
         raise BastionError("paged evict: budget, n_sink and n_recent must fit 32 bits")

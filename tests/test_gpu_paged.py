@@ -253,6 +253,46 @@ def test_attention_repeats_bit_for_bit_and_shares_a_workspace(cuda_lib):
         assert torch.equal(a, b)
 
 
+def test_both_ways_into_the_library_agree(cuda_lib, monkeypatch):
+    """With and without the compiled short way: the same results, and refusals from the same checks."""
+    from draft_tree_build_gb300 import bastion
+
+    def all_calls():
+        a = Case([700, 0, 90], 8, 2, 128, 16, layout="head", weights=True, seed=50).run(stream=torch.cuda.Stream())
+        c = Cache([90, 64, 30], 20, Hkv=2, D=64, page=8, seed=51)
+        _positions(c)
+        c.evict(60, 2, 8, False)
+        c.append(*c.rows(5), rows=torch.tensor([[0, 2, -1], [4, -1, -1], [1, 1, 1]], dtype=torch.int32))
+        c.same()
+        a.check()
+        return [a.out, a.lse, a.acc_out, c.g_k, c.g_v, c.g_acc, c.g_pos, c.g_lens, c.g_seen]
+
+    assert bastion._marshal is not None
+    calls = []
+    with monkeypatch.context() as mp:
+        spy = type("Spy", (), {n: (lambda *x, f=getattr(bastion._marshal, n): calls.append(f(*x)) or calls[-1])
+                               for n in ("append", "attention", "evict")})
+        mp.setattr(bastion, "_marshal", spy)
+        first = all_calls()
+    assert calls == [0, 0, 0]  # all three were taken
+    monkeypatch.setattr(bastion, "_marshal", None)
+    for x, y in zip(first, all_calls()):
+        assert torch.equal(x, y)
+    c = Case([40], 4, 2, seed=52)
+    for marshal in (None, bastion._load_marshal(bastion.lib())):
+        monkeypatch.setattr(bastion, "_marshal", marshal)
+        lens = c.seq_len
+        c.seq_len = lens.long()
+        with pytest.raises(bastion.BastionError, match="seq_len"):
+            c.run()
+        c.seq_len, scale = lens, c.scale
+        c.scale = -1.0
+        with pytest.raises(bastion.BastionError, match="out of range"):
+            c.run()
+        c.scale = scale
+        c.run().check()
+
+
 def test_one_workspace_serves_all_calls(cuda_lib):
     """Attention, eviction and append in turn on one workspace, whatever they leave in it."""
     from draft_tree_build_gb300 import bastion

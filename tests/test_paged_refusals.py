@@ -179,6 +179,23 @@ def test_binding_refuses_attention_arguments(b, change, match):
         _attend(b, t)
 
 
+def test_marshal_declines_what_the_binding_refuses(b):
+    """The compiled short way takes only calls that are right (CUDA tensors): for anything else it calls nothing,
+    raises nothing and leaves the binding's own checks to speak."""
+    m, t = b._marshal, _tensors()
+    assert m is not None
+    att = [t["q"], t["k"], t["v"], t["table"], t["lens"], 0.1, t["out"], t["ws"], t["st"], None, None, None, None]
+    app = [t["new"], t["new"], t["k"], t["v"], t["table"], t["lens"], t["lens"], t["ws"], t["st"]] + [None] * 7
+    ev = [t["k"], t["v"], t["table"], t["lens"], t["lens"], t["acc"], t["pos"], 8, 0, 0, t["lens"], t["acc"], t["pos"],
+          t["ws"], t["st"], None]
+    for f, args in ((m.attention, att), (m.append, app), (m.evict, ev)):
+        assert f(*args) is None            # CPU tensors
+        assert f() is None and f(*args, None) is None
+        for i in range(len(args)):
+            for bad in (None, 3, "x", 1 << 70, torch.zeros(1, 1, 1, 1, 1), object()):
+                assert f(*args[:i], bad, *args[i + 1:]) is None
+
+
 def test_binding_refuses_other_arguments(b):
     t = _tensors()
     with pytest.raises(b.BastionError, match="lse"):
