@@ -1,6 +1,8 @@
 // What the kernels of the paged cache share: its geometry on the device.
 #pragma once
 
+#include <atomic>
+
 #include "bastion_cache.h"
 #include "common.cuh"
 
@@ -46,5 +48,16 @@ __device__ __forceinline__ int64_t paged_row(const Paged &c, int page, int j, in
 }
 
 Paged paged_args(const bastion_paged_cache &c);
+
+// Lets a kernel have that much dynamic shared memory on device dev, once per
+// device: asking again costs 0.4 us a call.  done: the kernel's own, a bit a device.
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, int bytes, int dev, std::atomic<uint64_t> &done) {
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 }  // namespace bastion

@@ -1007,26 +1007,26 @@ bool make_map(CUtensorMap *m, const uint16_t *base, const Paged &c, bool swap, b
 }
 
 template <bool kHalf, int D, int GP>
-cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, int grid, const Paged &c, const AttendArgs &a,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap &mk, const CUtensorMap &mv, int dev, int grid, const Paged &c,
+                       const AttendArgs &a, cudaStream_t stream) {
   constexpr uint32_t smem = smem_bytes<D, GP>();
-  const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<kHalf, D, GP>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(paged_attention_kernel<kHalf, D, GP>, (int)smem, dev, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_attention_kernel<kHalf, D, GP>, dim3((unsigned)grid), dim3(kThreads), smem, stream, mk, mv,
                     c, a);
 }
 
 template <bool kHalf>
-cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int grid, const Paged &c, const AttendArgs &a,
-                        cudaStream_t stream) {
+cudaError_t launch_half(const CUtensorMap &mk, const CUtensorMap &mv, int dev, int grid, const Paged &c,
+                        const AttendArgs &a, cudaStream_t stream) {
   if (c.D == 128)
-    return a.G <= 4   ? launch_one<kHalf, 128, 4>(mk, mv, grid, c, a, stream)
-           : a.G <= 8 ? launch_one<kHalf, 128, 8>(mk, mv, grid, c, a, stream)
-                      : launch_one<kHalf, 128, 16>(mk, mv, grid, c, a, stream);
-  return a.G <= 4   ? launch_one<kHalf, 64, 4>(mk, mv, grid, c, a, stream)
-         : a.G <= 8 ? launch_one<kHalf, 64, 8>(mk, mv, grid, c, a, stream)
-                    : launch_one<kHalf, 64, 16>(mk, mv, grid, c, a, stream);
+    return a.G <= 4   ? launch_one<kHalf, 128, 4>(mk, mv, dev, grid, c, a, stream)
+           : a.G <= 8 ? launch_one<kHalf, 128, 8>(mk, mv, dev, grid, c, a, stream)
+                      : launch_one<kHalf, 128, 16>(mk, mv, dev, grid, c, a, stream);
+  return a.G <= 4   ? launch_one<kHalf, 64, 4>(mk, mv, dev, grid, c, a, stream)
+         : a.G <= 8 ? launch_one<kHalf, 64, 8>(mk, mv, dev, grid, c, a, stream)
+                    : launch_one<kHalf, 64, 16>(mk, mv, dev, grid, c, a, stream);
 }
 
 constexpr size_t kPartsBytes = (size_t)2 * kMaxParts * kPartFloats * sizeof(float);
@@ -1074,7 +1074,7 @@ int launch_paged_attention(const Paged &c, bool half, const void *q, int Hq, int
     return BASTION_ERR_LAUNCH;
   const int64_t most = (int64_t)c.B * c.Hkv * a.tiles_cap;  // tiles, at most
   const int sm_grid = sms < kMaxParts ? sms : kMaxParts, grid = most < sm_grid ? (int)most : sm_grid;
-  cudaError_t e = half ? launch_half<true>(mk, mv, grid, c, a, stream) : launch_half<false>(mk, mv, grid, c, a, stream);
+  cudaError_t e = half ? launch_half<true>(mk, mv, dev, grid, c, a, stream) : launch_half<false>(mk, mv, dev, grid, c, a, stream);
   if (e == cudaSuccess && acc)
     e = launch_pdl(paged_weights_kernel,
                    dim3((unsigned)((c.cap + 4 * kWeightsThreads - 1) / (4 * kWeightsThreads)), (unsigned)(c.B * c.Hkv)),

@@ -505,7 +505,8 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
   const int T = seg <= 8192 ? 512 : 1024;
   const size_t smem = (size_t)kHist * 4 + (in_smem ? (size_t)seg * 4 : 0);
   auto kernel = in_smem ? paged_evict_kernel<true> : paged_evict_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)((kHist + kKeysMax) * 4));
+  static std::atomic<uint64_t> done[2] = {{0}, {0}};
+  cudaError_t e = allow_smem(kernel, (int)((kHist + kKeysMax) * 4), dev, done[in_smem]);
   if (e == cudaSuccess)
     e = launch_cluster_pdl(kernel, dim3((unsigned)(units * cs)), dim3((unsigned)T), smem, stream, cs, c, a, cs);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? BASTION_OK : BASTION_ERR_LAUNCH;
