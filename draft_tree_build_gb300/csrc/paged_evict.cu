@@ -15,12 +15,14 @@
 // what another writes.  Weights and positions are read once (the keys stay in
 // shared memory) and only the holes' rows move.
 //
-// Few tokens leaving (32 requests x 8 heads, 2,065 slots cut to 2,048): 10.7 us, a chain of some
+// Few tokens leaving (32 requests x 8 heads, 2,065 slots cut to 2,048): 10.2 us, a chain of some
 // ten phases with a barrier each, against 1.9 us of traffic; as two launches it took 14.2 us.
-// Prompts cut (8 x 8 heads, up to 32,768 slots to 4,096): 54 us, of which the moves take two
+// Prompts cut (8 x 8 heads, up to 32,768 slots to 4,096): 55 us, of which the moves take two
 // thirds at 5.5 TB/s (rows of 256 bytes in no order) and the selection the rest; as two
 // launches, one CTA a head selecting, 88 us.  11, 12 or 13 bits in the first histogram are alike
-// within 3% (12 leaves fewer keys in the bin than 11 and clears faster than 13).
+// within 3% (12 leaves fewer keys in the bin than 11 and clears faster than 13).  The loops take a
+// key a lane and little code: every phase runs once or a few times, and its instructions have to
+// be fetched (four keys a lane, unrolled: 5 to 8% slower when few tokens leave, 2% faster on prompts).
 #include "paged.cuh"
 
 namespace bastion {
@@ -51,14 +53,11 @@ struct EvictArgs {
   int32_t *status;
 };
 
-// Key of a slot: larger is kept first.
-__device__ __forceinline__ uint32_t slot_key(float w, int pos, int sink, int64_t recent, bool &nan) {
-  if (pos < sink || pos >= recent) return kSafe;
-  if (w != w) {
-    nan = true;
-    w = INFINITY;
-  }
-  return ord_f32(w);  // at most ord(+inf) = 0xff800000
+// Key of slot s < end: larger is kept first.  (At or past the end: of no meaning, and no NaN is reported.)
+__device__ __forceinline__ uint32_t slot_key(float w, int pos, int sink, int64_t recent, int s, int end, bool &nan) {
+  const bool safe = pos < sink || pos >= recent, bad = w != w;
+  nan |= bad && !safe && s < end;
+  return safe ? kSafe : ord_f32(bad ? INFINITY : w);  // at most ord(+inf) = 0xff800000
 }
 
 struct Misc {
@@ -126,12 +125,15 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
   if (tid < 4) ms.count[tid] = 0;
 
   // The lengths may be updated in place: the last of the request's CTAs to have
-  // read them (after a barrier) writes.
+  // read them writes.  A CTA says so after the barrier behind its threads' reads
+  // (whose values they have used by then) and looks at the answer when it is done.
+  uint32_t readers = 0;
   auto length_read = [&]() {
-    if (tid != 0) return;
-    uint32_t old;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(&a.arrived[r]) : "memory");
-    if (old == (uint32_t)(c.Hkv * cs - 1)) {
+    if (tid == 0)
+      asm volatile("atom.add.relaxed.gpu.global.u32 %0, [%1], 1;" : "=r"(readers) : "l"(&a.arrived[r]) : "memory");
+  };
+  auto write_length = [&]() {
+    if (tid == 0 && readers == (uint32_t)(c.Hkv * cs - 1)) {
       a.arrived[r] = 0;
       const int raw = a.seq_len[r];
       a.seq_len_out[r] = raw > a.budget ? a.budget : raw;
@@ -139,32 +141,6 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
   };
   // this CTA's segment of the slots, in whole vectors of 4
   const int seg = ((n + cs - 1) / cs + 3) & ~3, s0 = min(n, part * seg), s1 = min(n, s0 + seg), count = s1 - s0;
-  const int keep_end = min(a.budget, s1);  // slots below it go to acc_out and pos_out where those are other arrays
-  // vector s of the segment to the outputs; the holes among its slots are written over by the moves
-  auto copy4 = [&](int s, const float4 &x, const int4 &y) {
-    if (s + 4 <= keep_end) {
-      if (a.acc_out != a.acc) *reinterpret_cast<float4 *>(acc_out + s) = x;
-      if (a.pos_out != a.pos) *reinterpret_cast<int4 *>(pos_out + s) = y;
-    } else {
-      const float *xf = reinterpret_cast<const float *>(&x);
-      const int *yf = reinterpret_cast<const int *>(&y);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (s + k < keep_end) {
-          acc_out[s + k] = xf[k];
-          pos_out[s + k] = yf[k];
-        }
-    }
-  };
-  if (n <= a.budget) {  // the whole cluster: nothing leaves
-    if (a.copy)
-      for (int s = s0 + 4 * tid; s < s1; s += 4 * T)
-        copy4(s, *reinterpret_cast<const float4 *>(acc + s), *reinterpret_cast<const int4 *>(pos + s));
-    __syncthreads();
-    length_read();
-    return;
-  }
-
   auto cluster_sync = [&]() {
     if (cs > 1) {
       cluster_arrive();
@@ -173,54 +149,61 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
       __syncthreads();
     }
   };
-  __syncthreads();
+  // Where acc_out and pos_out are other arrays, the slots below budget are copied (the holes among
+  // them are written over by the moves): with the keys, in whole vectors, or here slot by slot.
+  auto copy_slots = [&](int from, int to) {
+#pragma unroll 2
+    for (int s = from + tid; s < to; s += T) {
+      acc_out[s] = acc[s];
+      pos_out[s] = pos[s];
+    }
+  };
+  if (n <= a.budget) {  // the whole cluster: nothing leaves
+    if (a.copy) copy_slots(s0, s1);
+    __syncthreads();
+    length_read();
+    write_length();
+    return;
+  }
+
   bool nan = false;
-  auto enter = [&](uint32_t k, bool on) {
+  if (kKeys) {
+#pragma unroll 1
+    for (int v0 = s0; v0 < s1; v0 += 8 * T) {
+      if (cs > 1 || v0 > 0) fetch(v0, s1);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int s = v0 + 4 * (u * T + tid);
+        if (s >= s1) continue;
+        uint4 k;  // slots past the end are never looked at
+        k.x = slot_key(w[u].x, p[u].x, a.n_sink, recent, s, s1, nan);
+        k.y = slot_key(w[u].y, p[u].y, a.n_sink, recent, s + 1, s1, nan);
+        k.z = slot_key(w[u].z, p[u].z, a.n_sink, recent, s + 2, s1, nan);
+        k.w = slot_key(w[u].w, p[u].w, a.n_sink, recent, s + 3, s1, nan);
+        *reinterpret_cast<uint4 *>(keys + s - s0) = k;
+        if (a.copy && s + 4 <= a.budget) {
+          *reinterpret_cast<float4 *>(acc_out + s) = w[u];
+          *reinterpret_cast<int4 *>(pos_out + s) = p[u];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  auto key_at = [&](int i) {
+    return kKeys ? keys[i] : slot_key(acc[s0 + i], pos[s0 + i], a.n_sink, recent, 0, 1, nan);
+  };
+#pragma unroll 2
+  for (int i0 = 32 * warp; i0 < count; i0 += T) {
+    const int i = i0 + lane;
+    const bool on = i < count;
+    const uint32_t k = on ? key_at(i) : 0u;
     // many protected slots lie side by side: one addition for a warp's
     const uint32_t safe = __ballot_sync(kFull, on && k == kSafe);
     if (on && k != kSafe) atomicAdd(&hist[k >> (32 - kBits0)], 1u);
     if (safe && lane == 0) atomicAdd(&hist[kBins0 - 1], (uint32_t)__popc(safe));
-  };
-  for (int v0 = s0; v0 < s1; v0 += 8 * T) {
-    if (!(kKeys && cs == 1 && v0 == 0)) fetch(v0, s1);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (v0 + 4 * (u * T + 32 * warp) >= s1) continue;  // the whole warp
-      const int s = v0 + 4 * (u * T + tid);
-      const float *wf = reinterpret_cast<const float *>(&w[u]);
-      const int *pf = reinterpret_cast<const int *>(&p[u]);
-      uint32_t k[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool on = s + x < s1;
-        k[x] = on ? slot_key(wf[x], pf[x], a.n_sink, recent, nan) : 0u;
-        enter(k[x], on);
-      }
-      if (s < s1) {
-        if (kKeys) *reinterpret_cast<uint4 *>(keys + s - s0) = make_uint4(k[0], k[1], k[2], k[3]);
-        if (a.copy) copy4(s, w[u], p[u]);
-      }
-    }
   }
   if (nan) atomicOr(&a.status[r], BASTION_STATUS_NONFINITE);
   length_read();
-  // keys i .. i + 3 of the segment, i a multiple of 4; 0 past its end
-  auto keys4 = [&](int i, uint32_t (&k)[4]) {
-    if (kKeys) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(keys + i);
-      k[0] = x.x;
-      k[1] = x.y;
-      k[2] = x.z;
-      k[3] = x.w;
-    } else {
-      const float4 wf = *reinterpret_cast<const float4 *>(acc + s0 + i);
-      const int4 pf = *reinterpret_cast<const int4 *>(pos + s0 + i);
-      const float *ww = reinterpret_cast<const float *>(&wf);
-      const int *pp = reinterpret_cast<const int *>(&pf);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) k[x] = i + x < count ? slot_key(ww[x], pp[x], a.n_sink, recent, nan) : 0u;
-    }
-  };
 
   // t: the bits found of the budget-th largest key, `shift` more are open; `need` of the keys that
   // begin with t are kept
@@ -233,12 +216,9 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     shift -= bits;
     if (pass > 0) {
 #pragma unroll 2
-      for (int i = 4 * tid; i < count; i += 4 * T) {
-        uint32_t k[4];
-        keys4(i, k);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (i + x < count && (k[x] >> (shift + bits)) == t) atomicAdd(&h[(k[x] >> shift) & (uint32_t)(bins - 1)], 1u);
+      for (int i = tid; i < count; i += T) {
+        const uint32_t k = key_at(i);
+        if ((k >> (shift + bits)) == t) atomicAdd(&h[(k >> shift) & (uint32_t)(bins - 1)], 1u);
       }
     }
     __syncthreads();
@@ -256,6 +236,7 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     if (warp == 0) {
       // the run, then the bin, over all CTAs of the cluster
       uint32_t own = lane < runs ? ms.warp_sum[pass][lane] : 0u;
+      if (cs > 1)
 #pragma unroll
       for (int o = 1; o < kMaxCluster; ++o)
         if (o < cs && lane < runs) own += dsmem_ld_u32(dsmem_addr(&ms.warp_sum[pass][lane], (uint32_t)((part + o) & (cs - 1))));
@@ -265,6 +246,7 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
       for (int b0 = bins - in_run * run; b0 > 0; b0 -= 128) {
         const int b = b0 - 4 * lane - 4;
         uint4 x = *reinterpret_cast<const uint4 *>(h + b);
+        if (cs > 1)
 #pragma unroll
         for (int o = 1; o < kMaxCluster; ++o) {
           const uint4 y = o < cs ? dsmem_ld_v4(dsmem_addr(h + b, (uint32_t)((part + o) & (cs - 1)))) : make_uint4(0, 0, 0, 0);
@@ -300,12 +282,9 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     if (shift > 0 && in_bin <= (uint32_t)kCand) {
       // few keys begin with t: gather them and rank each against all
 #pragma unroll 2
-      for (int i = 4 * tid; i < count; i += 4 * T) {
-        uint32_t k[4];
-        keys4(i, k);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (i + x < count && (k[x] >> shift) == t) cand[atomicAdd(&ms.n_cand, 1u)] = k[x];
+      for (int i = tid; i < count; i += T) {
+        const uint32_t k = key_at(i);
+        if ((k >> shift) == t) cand[atomicAdd(&ms.n_cand, 1u)] = k;
       }
       cluster_sync();
       const int own = (int)ms.n_cand;
@@ -346,22 +325,17 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
   }
 
   // t is the budget-th largest key; `need` of the slots that equal it stay.  Each
-  // warp counts its own run of the segment, 128 slots at a time, 4 a lane.
-  const int run = (count + 4 * T - 1) / (4 * T) * 128, w0 = min(count, warp * run), w1 = min(count, w0 + run);
+  // warp counts its own run of the segment, in whole groups of 32.
+  const int run = (count + T - 1) / T * 32, w0 = min(count, warp * run), w1 = min(count, w0 + run);
   const int below = a.budget - s0;  // the segment's slots below it are below budget
   uint32_t gt = 0, eq = 0, gt_b = 0, eq_b = 0;
 #pragma unroll 2
-  for (int i = w0 + 4 * lane; i < w1; i += 128) {
-    uint32_t k[4];
-    keys4(i, k);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const bool on = i + x < w1, low = i + x < below;
-      gt += on && k[x] > t;
-      eq += on && k[x] == t;
-      gt_b += on && low && k[x] > t;
-      eq_b += on && low && k[x] == t;
-    }
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key_at(i);
+    gt += k > t;
+    eq += k == t;
+    gt_b += i < below && k > t;
+    eq_b += i < below && k == t;
   }
   gt = __reduce_add_sync(kFull, gt);
   eq = __reduce_add_sync(kFull, eq);
@@ -397,32 +371,24 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
   const int n_moves = a.budget - (int)kb;
   const bool near = cs == 1 && n_moves <= kNearMoves;
   int2 *moves = near ? near_moves : a.moves + (size_t)unit * a.max_moves;
-  for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
-    uint32_t k[4] = {0, 0, 0, 0};
-    if (i < w1) keys4(i, k);
-    uint32_t both = 0;  // keys above t, and equal ones in the high half
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (i + x < w1) both += k[x] > t ? 1u : k[x] == t ? 0x10000u : 0u;
-    const uint32_t incl = warp_scan(both, lane), excl = incl - both, all = __shfl_sync(kFull, incl, 31);
-    uint32_t ge = g0 + (excl & 0xffffu), ee = e0 + (excl >> 16);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (i + x >= w1) break;
-      const int s = s0 + i + x;
-      const bool tie = k[x] == t, keep = k[x] > t || (tie && ee < need);
-      const uint32_t before = ge + min(ee, need);
-      if (i + x < below) {
-        if (!keep) moves[s - (int)before].y = s;
-      } else if (keep) {
-        moves[before - kb].x = s;
-      }
-      ge += k[x] > t;
-      ee += tie;
+  const uint32_t lt = (1u << lane) - 1u;
+#pragma unroll 1
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const bool on = i < w1;
+    const uint32_t k = on ? key_at(i) : 0u;
+    const uint32_t mg = __ballot_sync(kFull, on && k > t), me = __ballot_sync(kFull, on && k == t);
+    const uint32_t ee = e0 + __popc(me & lt), before = g0 + __popc(mg & lt) + min(ee, need);
+    const bool keep = on && (k > t || (k == t && ee < need));
+    if (on && i < below) {
+      if (!keep) moves[s0 + i - (int)before].y = s0 + i;
+    } else if (keep) {
+      moves[before - kb].x = s0 + i;
     }
-    g0 += all & 0xffffu;
-    e0 += all >> 16;
+    g0 += __popc(mg);
+    e0 += __popc(me);
   }
+  // what the keys' vectors left out
+  if (a.copy) copy_slots(kKeys ? max(s0, a.budget & ~3) : s0, min(a.budget, s1));
   cluster_sync();  // the list is whole; no CTA reads another's shared memory any more
 
   // The moves, T of them at a time.  First a thread a move: its pages, its
@@ -463,6 +429,7 @@ __global__ void __launch_bounds__(1024) paged_evict_kernel(Paged c, EvictArgs a,
     }
     __syncthreads();
   }
+  write_length();
 }
 
 }  // namespace
