@@ -116,6 +116,13 @@ def test_attention_many_requests(cuda_lib):
     Case(lens, 8, 2, 64, 16, weights=True, seed=3).run().check()
 
 
+@pytest.mark.parametrize("B,Hq,Hkv", [(1024, 3, 3), (255, 257, 257)])
+def test_attention_at_the_limits_of_requests_and_heads(cuda_lib, B, Hq, Hkv):
+    """1,024 requests; 65,535 (request, KV head) pairs, one unit each."""
+    lens = torch.randint(0, 12 if Hkv > 3 else 150, (B,), generator=_gen(B)).tolist()
+    Case(lens, Hq, Hkv, 64, 8, weights=True, seed=B).run().check()
+
+
 def test_attention_one_long_among_many_short(cuda_lib):
     lens = [3] * 40 + [30000] + [0, 5] * 20
     Case(lens, 16, 4, 128, 32, weights=True, seed=4).run().check()
