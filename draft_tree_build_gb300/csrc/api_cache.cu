@@ -144,6 +144,10 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(acc, 16) || !aligned(acc_out, 16))
     return BASTION_ERR_ALIGN;
   if (acc && !same_or_apart(acc, acc_out, slots_bytes(cache))) return BASTION_ERR_UNSUPPORTED;
+  // in place: a head's queries are read by all who need them before its output is written, but not another head's
+  const int64_t row = (int64_t)Hq * cache->D, q_st = cache->B > 1 ? q_stride_b : row;
+  const uintptr_t q0 = (uintptr_t)q, q1 = q0 + 2 * (uintptr_t)((cache->B - 1) * q_st + row), o0 = (uintptr_t)out;
+  if (!(q0 == o0 && q_st == row) && o0 < q1 && q0 < o0 + 2 * (uintptr_t)(cache->B * row)) return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_attention_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D,
                                                                 (int64_t)cache->max_pages * cache->page_size,
                                                                 acc != nullptr))

@@ -103,7 +103,8 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
  * seq_len  [B] int32.  A request without slots, or a head whose scores are all
  *          -inf, gives out = 0 and lse = -inf.
  * out      [B, Hq, D] contiguous, the cache's dtype (rounded once to nearest
- *          even), 16-byte aligned.
+ *          even), 16-byte aligned; q itself where q is contiguous, or apart from
+ *          it (BASTION_ERR_UNSUPPORTED otherwise).
  * lse      [B, Hq] float or NULL.
  * acc, acc_out  [B, Hkv, max_pages * page_size] float, 16-byte aligned, both or
  *          neither NULL; the same array or disjoint ones.  Slots at or past seq_len[r] of

@@ -318,6 +318,14 @@ def test_one_workspace_serves_all_calls(cuda_lib):
     assert int(c.status.sum()) == 0
 
 
+def test_attention_output_in_place_of_the_queries(cuda_lib):
+    c = Case([300, 0, 5000, 1], Hq=8, Hkv=2, seed=21).run()
+    q = c.q.clone()
+    c.b.bastion_paged_attention(q, c.k, c.v, c.table, c.seq_len, c.scale, q, c.ws, c.status)
+    c.check()
+    assert torch.equal(q, c.out)
+
+
 def test_attention_weights_in_place(cuda_lib):
     c = Case([300, 0, 77], 8, 4, weights=True, seed=15).run()
     acc = c.acc.clone()

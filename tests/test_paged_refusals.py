@@ -132,6 +132,15 @@ def test_call_refusals(b, which, over, code):
     assert _call(b, which, **over) == code
 
 
+@pytest.mark.parametrize("over", [
+    dict(out=vp(0x400010)), dict(out=vp(0x3ffff0)), dict(q_stride_b=33 * 128, out=vp(0x400000)),
+    dict(q_stride_b=64 * 128, out=vp(0x400000 + 64 * 128 * 2 * 3 + 32 * 128 * 2 - 16)),
+])
+def test_outputs_over_part_of_the_queries(b, over):
+    """out is q's own memory, row for row, or none of it."""
+    assert _call(b, "attend", **over) == UNSUPPORTED
+
+
 def test_workspace_queries(b):
     assert b.bastion_paged_append_workspace_bytes(4) > 0
     assert b.bastion_paged_append_workspace_bytes(0) == 0 == b.bastion_paged_append_workspace_bytes(1025)
