@@ -115,8 +115,14 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
     return BASTION_ERR_SIZE;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(workspace, 256)) return BASTION_ERR_ALIGN;
   const size_t lens = (size_t)cache->B * 4;
-  if (!same_or_apart(seq_len, seq_len_out, lens) || (n_seen && !same_or_apart(n_seen, n_seen_out, lens)))
+  if (!same_or_apart(seq_len, seq_len_out, lens) || (n_new && !same_or_apart(n_new, seq_len_out, lens)))
     return BASTION_ERR_UNSUPPORTED;
+  if (n_seen) {  // where no slot is ever evicted, both counts may be one array
+    if (!same_or_apart(n_seen, n_seen_out, lens) || !same_or_apart(n_seen, seq_len_out, lens) ||
+        !same_or_apart(seq_len, n_seen_out, lens) || (n_new && !same_or_apart(n_new, n_seen_out, lens)) ||
+        !(apart(seq_len_out, n_seen_out, lens) || (seq_len_out == n_seen_out && seq_len == n_seen)))
+      return BASTION_ERR_UNSUPPORTED;
+  }
   if (workspace_bytes < bastion_paged_append_workspace_bytes(cache->B)) return BASTION_ERR_WORKSPACE;
   return bastion::launch_paged_append(bastion::paged_args(*cache), k_new, v_new, n_rows,
                                       cache->B > 1 ? new_stride_b : 0, n_rows > 1 ? new_stride_row : 0,

@@ -75,7 +75,10 @@ typedef struct {
  *               or disjoint ones.
  * n_seen, n_seen_out    [B] int32: tokens ever appended, before and after (the
  *               position of the next token); the same or disjoint.  Needed
- *               with acc and pos, else both may be NULL.
+ *               with acc and pos, else both may be NULL.  Where nothing is ever
+ *               evicted they may be seq_len and seq_len_out.
+ *               No output overlaps part of an input or of the other output
+ *               (BASTION_ERR_UNSUPPORTED).
  * acc, pos      [B, Hkv, max_pages * page_size], both or neither NULL: the new
  *               slots get weight 0 and their token's position.
  * A request whose rows do not fit (seq_len + rows > max_pages * page_size)

@@ -502,6 +502,16 @@ def test_append_strided_rows_and_separate_lengths(cuda_lib):
     assert torch.equal(out.cpu(), new)
 
 
+def test_append_one_array_of_lengths(cuda_lib):
+    """Without evictions a request's tokens are its slots: seq_len serves as n_seen."""
+    c = Cache([5, 0, 61], 12, seed=7)
+    k, v = c.rows(20)
+    c.b.bastion_paged_append(k.to(dev()), v.to(dev()), c.g_k, c.g_v, c.g_table, c.g_lens, c.g_lens, c.ws, c.status,
+                             acc=c.g_acc, pos=c.g_pos, n_seen=c.g_lens, n_seen_out=c.g_lens)
+    c.lens, _ = ref.append(k, v, c.k, c.v, c.table, c.lens, c.seen, c.acc, c.pos)
+    c.same(("k", "v", "lens", "acc", "pos"))
+
+
 def test_append_long_prompts(cuda_lib):
     c = Cache([100, 0], 300, Hkv=4, D=128, page=16, seed=5)
     c.append(*c.rows(4501), n_new=torch.tensor([4501, 1777], dtype=torch.int32))

@@ -133,6 +133,15 @@ def test_call_refusals(b, which, over, code):
 
 
 @pytest.mark.parametrize("over", [
+    dict(seq_len_out=vp(0x700004)), dict(n_seen_out=vp(0x600008)), dict(n_new=vp(0x600004)), dict(n_new=vp(0x6ffffc)),
+    dict(seq_len_out=vp(0xd00000), n_seen_out=vp(0xd00000)), dict(seq_len_out=vp(0xd00000), n_seen_out=vp(0xd00004)),
+])
+def test_lengths_over_part_of_one_another(b, over):
+    """A request's last CTA writes its lengths while others may still read their own requests' entries."""
+    assert _call(b, "append", **over) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("over", [
     dict(out=vp(0x400010)), dict(out=vp(0x3ffff0)), dict(q_stride_b=33 * 128, out=vp(0x400000)),
     dict(q_stride_b=64 * 128, out=vp(0x400000 + 64 * 128 * 2 * 3 + 32 * 128 * 2 - 16)),
 ])
