@@ -404,6 +404,12 @@ def _launch_on(dev, stream, workspace):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _same_strides(a, b):
+    """Of two tensors of one shape: the stride of a dimension of length 1 says nothing."""
+    x, y = a.stride(), b.stride()
+    return x == y or all(n == 1 or i == j for n, i, j in zip(a.shape, x, y))
+
+
 def _cache(k_pool, v_pool, page_table):
     """Checks the cache; (device, B, Hkv, D, slots of a request, the struct's bytes, which ctypes passes by address).
     Pools [n_pages, page_size, Hkv, D] of any strides (a head-major pool is a transposed view), page_table
@@ -414,7 +420,7 @@ def _cache(k_pool, v_pool, page_table):
     dt = _CACHE_DTYPES.get(k_pool.dtype)
     if dt is None:
         raise BastionError(f"paged cache: the pools must be bfloat16 or float16, got {k_pool.dtype}")
-    if st[3] != 1 or st != v_pool.stride():
+    if st[3] != 1 or not _same_strides(k_pool, v_pool):
         raise BastionError("paged cache: the pools must have equal strides and a contiguous last dimension")
     table = page_table.shape
     if len(table) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
@@ -452,7 +458,7 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
     if len(new) != 4 or new != v_new.shape or new[0] != B or new[2] != Hkv or new[3] != D \
             or k_new.dtype is not dtype or v_new.dtype is not dtype:
         raise BastionError("paged append: k_new and v_new must be [B, n_rows, Hkv, D] of the pools' dtype")
-    if st[3] != 1 or st != v_new.stride():
+    if st[3] != 1 or not _same_strides(k_new, v_new):
         raise BastionError("paged append: k_new and v_new must have equal strides and a contiguous last dimension")
     if k_new.get_device() != dev or v_new.get_device() != dev:
         raise BastionError("paged append: k_new and v_new must be on the pools' device")

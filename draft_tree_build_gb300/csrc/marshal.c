@@ -103,7 +103,7 @@ static int cache_of(PyObject *k, PyObject *v, PyObject *table, bastion_paged_cac
   if (tk.dim != 4 || tv.dim != 4 || tt.dim != 2 || tk.dtype != tv.dtype || tk.dev != tt.dev || tv.dev != tt.dev || tt.dev < 0)
     return 0;
   for (int i = 0; i < 4; ++i)
-    if (tk.shape[i] != tv.shape[i] || tk.stride[i] != tv.stride[i]) return 0;
+    if (tk.shape[i] != tv.shape[i] || (tk.shape[i] != 1 && tk.stride[i] != tv.stride[i])) return 0;
   if (tk.stride[3] != 1 || (tk.dtype != dt_bf16 && tk.dtype != dt_f16)) return 0;
   void *at;
   if (!contiguous(table, tt.dev, dt_i32, 2, tt.shape, &at)) return 0;
@@ -183,7 +183,7 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       v.dtype != dtype || k.dev != dev || v.dev != dev || k.stride[3] != 1)
     return declined();
   for (int i = 0; i < 4; ++i)
-    if (k.shape[i] != v.shape[i] || k.stride[i] != v.stride[i]) return declined();
+    if (k.shape[i] != v.shape[i] || (k.shape[i] != 1 && k.stride[i] != v.stride[i])) return declined();
   if (k.shape[0] != c.B || k.shape[2] != c.Hkv || k.shape[3] != c.D || k.shape[1] > INT32_MAX) return declined();
   int64_t m = k.shape[1];
   rows.ptr = NULL;

@@ -502,6 +502,18 @@ def test_append_strided_rows_and_separate_lengths(cuda_lib):
     assert torch.equal(out.cpu(), new)
 
 
+def test_append_one_token_of_any_stride(cuda_lib):
+    """One token's keys as a transposed view (heads before tokens), its values not."""
+    c = Cache([5, 0, 61], 12, Hkv=4, seed=8)
+    k, v = c.rows(1)
+    k_t = k.transpose(1, 2).clone(memory_format=torch.contiguous_format).to(dev()).transpose(1, 2)
+    v_g = v.to(dev())
+    assert k_t.stride() != v_g.stride()
+    c.b.bastion_paged_append(k_t, v_g, c.g_k, c.g_v, c.g_table, c.g_lens, c.g_lens, c.ws, c.status)
+    c.lens, _ = ref.append(k, v, c.k, c.v, c.table, c.lens, c.seen, None, None)
+    c.same(("k", "v", "lens"))
+
+
 def test_append_one_array_of_lengths(cuda_lib):
     """Without evictions a request's tokens are its slots: seq_len serves as n_seen."""
     c = Cache([5, 0, 61], 12, seed=7)

@@ -214,6 +214,21 @@ def test_marshal_declines_what_the_binding_refuses(b):
                 assert f(*args[:i], bad, *args[i + 1:]) is None
 
 
+def test_strides_of_single_entries_do_not_matter(b):
+    """One token's rows [B, 1, Hkv, D], transposed or not: the same memory, whatever the stride of the 1 says."""
+    t = _tensors()
+    one = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16)
+    other = torch.zeros(2, 2, 1, 128, dtype=torch.bfloat16).transpose(1, 2)
+    assert one.stride() != other.stride()
+    with pytest.raises(b.BastionError, match="CUDA device"):  # and nothing else
+        b.bastion_paged_append(one, other, t["k"], t["v"], t["table"], t["lens"], t["lens"], t["ws"], t["st"])
+    k = t["k"][:1]
+    v = torch.as_strided(k, k.shape, (8, *k.stride()[1:]))
+    assert v.stride() != k.stride()
+    with pytest.raises(b.BastionError, match="CUDA device"):
+        b.bastion_paged_append(one, one, k, v, t["table"], t["lens"], t["lens"], t["ws"], t["st"])
+
+
 def test_binding_refuses_other_arguments(b):
     t = _tensors()
     with pytest.raises(b.BastionError, match="lse"):
