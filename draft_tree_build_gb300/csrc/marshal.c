@@ -10,6 +10,10 @@
  *
  * A tensor is looked at through its Python attributes, so that nothing here
  * depends on how torch is built.
+ *
+ * The library runs without the interpreter's lock, as it does through ctypes: a
+ * launch waits where the stream's queue is full, and other threads (a host
+ * callback that the queue waits for among them) must get on meanwhile.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -201,8 +205,12 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       !contiguous_or_none(a[13], dev, dt_i32, 1, B, &seen) || !contiguous_or_none(a[14], dev, dt_i32, 1, B, &seen_out) ||
       !stream_on(a[15], dev, &stream))
     return declined();
-  return PyLong_FromLong(f_append(&c, k.ptr, v.ptr, (int)k.shape[1], k.stride[0], k.stride[1], k.stride[2], rows.ptr,
-                                  (int)m, n_new, len, len_out, seen, seen_out, acc, pos, ws, bytes, st, stream));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_append(&c, k.ptr, v.ptr, (int)k.shape[1], k.stride[0], k.stride[1], k.stride[2], rows.ptr, (int)m, n_new, len,
+                len_out, seen, seen_out, acc, pos, ws, bytes, st, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
 }
 
 /* q, k_pool, v_pool, page_table, seq_len, scale, out, workspace, status, lse, acc, acc_out, stream */
@@ -229,8 +237,12 @@ static PyObject *attention(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       !contiguous_or_none(a[10], dev, dt_f32, 3, slots, &acc) ||
       !contiguous_or_none(a[11], dev, dt_f32, 3, slots, &acc_out) || !stream_on(a[12], dev, &stream))
     return declined();
-  return PyLong_FromLong(f_attention(&c, q.ptr, (int)q.shape[1], q.stride[0], len, (float)scale, out, lse, acc, acc_out,
-                                     ws, bytes, st, stream));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_attention(&c, q.ptr, (int)q.shape[1], q.stride[0], len, (float)scale, out, lse, acc, acc_out, ws, bytes, st,
+                   stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
 }
 
 /* k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, budget, n_sink, n_recent, seq_len_out, acc_out, pos_out,
@@ -253,8 +265,11 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       !contiguous(a[12], dev, dt_i32, 3, slots, &pos_out) || !workspace_of(a[13], dev, &ws, &bytes) ||
       !contiguous(a[14], dev, dt_i32, 1, B, &st) || !stream_on(a[15], dev, &stream))
     return declined();
-  return PyLong_FromLong(f_evict(&c, len, seen, acc, pos, budget, sink, recent, len_out, acc_out, pos_out, ws, bytes, st,
-                                 stream));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_evict(&c, len, seen, acc, pos, budget, sink, recent, len_out, acc_out, pos_out, ws, bytes, st, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
 }
 
 /* bfloat16, float16, float32, int32, uint8, current device, raw stream of a device, and the addresses of the

@@ -229,6 +229,34 @@ def test_strides_of_single_entries_do_not_matter(b):
         b.bastion_paged_append(one, one, k, v, t["table"], t["lens"], t["lens"], t["ws"], t["st"])
 
 
+class _Fake:
+    """What the short way looks at of a tensor; on device 0."""
+
+    def __init__(self, t):
+        self.t, self.dtype, self.shape = t, t.dtype, tuple(t.shape)
+        self.stride, self.is_contiguous, self.data_ptr = t.stride, t.is_contiguous, t.data_ptr
+
+    def get_device(self):
+        return 0
+
+
+def test_marshal_calls_without_the_interpreters_lock(b):
+    """A function that says whether its thread holds the lock, in place of the library's three."""
+    m, t = b._marshal, {n: _Fake(x) for n, x in _tensors().items()}
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, vp).value
+    try:
+        m.init(torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8, lambda: 0, lambda dev: 0, held,
+               held, held)
+        assert m.attention(t["q"], t["k"], t["v"], t["table"], t["lens"], 0.1, t["out"], t["ws"], t["st"], None, None,
+                           None, None) == 0
+        assert m.append(t["new"], t["new"], t["k"], t["v"], t["table"], t["lens"], t["lens"], t["ws"], t["st"],
+                        *[None] * 7) == 0
+        assert m.evict(t["k"], t["v"], t["table"], t["lens"], t["lens"], t["acc"], t["pos"], 8, 0, 0, t["lens"],
+                       t["acc"], t["pos"], t["ws"], t["st"], None) == 0
+    finally:
+        b._marshal = b._load_marshal(b.lib())
+
+
 def test_binding_refuses_other_arguments(b):
     t = _tensors()
     with pytest.raises(b.BastionError, match="lse"):
