@@ -12,8 +12,7 @@
 //  * the rows are cut into M-tiles of 128 and the vocabulary into N-tiles of
 //    192; CTA c owns M-tile c % MT and every CPM-th N-tile from c / MT on, so
 //    the MT CTAs that read the same N-tile of W run side by side and W comes
-//    from HBM about once (the other reads hit L2; optionally the MT CTAs form
-//    a cluster and each loads a slice of the W tile for all of them);
+//    from HBM about once (the other reads hit L2);
 //  * warp 0 streams A (hidden, 128 x 64) and B (W, 192 x 64) tiles through a
 //    4-stage ring with TMA (cp.async.bulk.tensor, 128-byte swizzle, zero fill
 //    past the edges); lane 0 of warp 1 issues tcgen05.mma kind::f16 (bf16 in,
@@ -49,8 +48,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cstdlib>
-
 #include "common.cuh"
 
 namespace bastion {
@@ -73,7 +70,6 @@ constexpr float kCNone = -1.0e30f;                      // c before the first fi
 
 struct LmArgs {
   int rows, H, V, K, b, MT, NT, CPM, KC, J;
-  int CL;  // CTAs of a cluster: M-tiles that share each W tile, loaded once and multicast
   uint64_t *part_keys;  // [rows][CPM][K]
   float4 *part_stat;    // [rows][CPM]: max, c, sum (hi, lo)
   uint64_t *pub;        // [rows][CPS]: each share's J-th (4th) best key so far (0: none yet);
@@ -112,16 +108,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
-}
-
-// Arrives on the same barrier of every CTA in mask once this thread's MMAs
-// so far have completed.
-__device__ __forceinline__ void mma_commit_mc(uint64_t *bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() {
@@ -207,17 +193,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
       "{%2, %3}], [%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// The same box into the same shared-memory offset of every CTA in mask, each
-// CTA's barrier at bar's offset counting the bytes.
-__device__ __forceinline__ void tma_load_2d_mc(void *dst, const CUtensorMap *map, int c0, int c1,
-                                               uint64_t *bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "h"(mask)
       : "memory");
 }
 
@@ -323,7 +298,7 @@ __global__ void __launch_bounds__(kLT, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bs.full[s], 1);
-      mbar_init(&bs.empty[s], (uint32_t)a.CL);  // every CTA of the cluster has read the stage
+      mbar_init(&bs.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bs.acc_full[s], 1);
@@ -346,14 +321,6 @@ __global__ void __launch_bounds__(kLT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bs.tmem;
-  // every CTA of the cluster has set its barriers before any copy or commit
-  // reaches them
-  const uint16_t cmask = (uint16_t)((1u << a.CL) - 1u);
-  const int crank = blockIdx.x % a.CL;
-  if (a.CL > 1) {
-    cluster_arrive_relaxed();
-    cluster_wait();
-  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -367,13 +334,7 @@ __global__ void __launch_bounds__(kLT, 1)
         unsigned char *dst = smem + (uint32_t)s * kStageBytes;
         mbar_arrive_expect_tx(&bs.full[s], kStageBytes);
         tma_load_2d(dst, &tm_h, kc * kBK, mt * kBM, &bs.full[s]);
-        if (a.CL == 1) {
-          tma_load_2d(dst + kABytes, &tm_w, kc * kBK, n * kBN, &bs.full[s]);
-        } else {  // this CTA's slice of the W tile, into every CTA of the cluster
-          const int sr = kBN / a.CL;
-          tma_load_2d_mc(dst + kABytes + (uint32_t)(crank * sr) * 128u, &tm_w, kc * kBK, n * kBN + crank * sr,
-                         &bs.full[s], cmask);
-        }
+        tma_load_2d(dst + kABytes, &tm_w, kc * kBK, n * kBN, &bs.full[s]);
         issued = g + 1;
       }
       // our copies have landed (bounded) before the CTA may exit
@@ -402,9 +363,8 @@ __global__ void __launch_bounds__(kLT, 1)
           for (int ks = 0; ks < kBK / 16; ++ks)
             mma_bf16(d, sw128_desc(sa + (uint32_t)ks * 32u), sw128_desc(sb + (uint32_t)ks * 32u),
                      (kc > 0 || ks > 0) ? 1u : 0u);
-          // the stage frees (in every CTA of the cluster) once these MMAs have read it
-          if (a.CL == 1) mma_commit(&bs.empty[s]);
-          else mma_commit_mc(&bs.empty[s], cmask);
+          // the stage frees once these MMAs have read it
+          mma_commit(&bs.empty[s]);
         }
         if (ok) mma_commit(&bs.acc_full[buf]);
       }
@@ -642,11 +602,6 @@ __global__ void __launch_bounds__(kLT, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  // no copy or commit of another CTA of the cluster targets this one any more
-  if (a.CL > 1) {
-    cluster_arrive();
-    cluster_wait();
-  }
 }
 
 // ---------------------------------------------------------------------------- merge
@@ -813,14 +768,9 @@ bool make_map_2d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uin
 }
 
 struct LmPlan {
-  int MT, NT, CPM, CL, grid;
+  int MT, NT, CPM, grid;
 };
 
-// Clusters of CL CTAs (M-tiles that share each W tile, loaded once and
-// multicast; BASTION_LMHEAD_CLUSTER=2|4 chooses them, the default is none:
-// on the batched workload clusters of 2 and 4 measured 669 and 710 us against
-// 647 us without, the cluster placement leaving SMs idle), as many as can be
-// resident at once.
 LmPlan lm_plan(int rows, int V) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -828,37 +778,7 @@ LmPlan lm_plan(int rows, int V) {
   LmPlan p;
   p.MT = (rows + kBM - 1) / kBM;
   p.NT = (V + kBN - 1) / kBN;
-  const char *env = getenv("BASTION_LMHEAD_CLUSTER");
-  int want = env ? atoi(env) : 1;
-  p.CL = 1;
-  for (int cl = 4; cl >= 2; cl /= 2)
-    if (cl <= want && p.MT % cl == 0) {
-      p.CL = cl;
-      break;
-    }
-  int slots = sms;  // CTAs resident at once (one per SM)
-  if (p.CL > 1) {
-    cudaFuncSetAttribute(lm_head_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.CL * sms));
-    cfg.blockDim = dim3(kLT);
-    cfg.dynamicSmemBytes = kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.CL;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int nc = 0;
-    if (cudaOccupancyMaxActiveClusters(&nc, lm_head_kernel, &cfg) == cudaSuccess && nc > 0) {
-      slots = nc * p.CL;
-    } else {
-      cudaGetLastError();
-      p.CL = 1;
-    }
-  }
-  p.CPM = slots / p.MT;
+  p.CPM = sms / p.MT;  // one CTA per SM
   if (p.CPM < 1) p.CPM = 1;
   if (p.CPM > p.NT) p.CPM = p.NT;
   p.grid = p.MT * p.CPM;
@@ -882,7 +802,7 @@ int launch_lm_head(const void *hidden, const void *weight, int B, int b, int H, 
   const LmPlan p = lm_plan(rows, V);
   CUtensorMap mh, mw;
   if (!make_map_2d(&mh, hidden, (uint64_t)H, (uint64_t)rows, kBM) ||
-      !make_map_2d(&mw, weight, (uint64_t)H, (uint64_t)V, (uint32_t)(kBN / p.CL)))
+      !make_map_2d(&mw, weight, (uint64_t)H, (uint64_t)V, kBN))
     return BASTION_ERR_LAUNCH;
   LmArgs a;
   a.rows = rows;
@@ -893,7 +813,6 @@ int launch_lm_head(const void *hidden, const void *weight, int B, int b, int H, 
   a.MT = p.MT;
   a.NT = p.NT;
   a.CPM = p.CPM;
-  a.CL = p.CL;
   a.KC = H / kBK;
   unsigned char *w = static_cast<unsigned char *>(ws);
   const size_t keys = ((size_t)rows * p.CPM * K * 8 + 255) / 256 * 256;
@@ -906,12 +825,8 @@ int launch_lm_head(const void *hidden, const void *weight, int B, int b, int H, 
   a.J = (K + 3) / 4 <= p.CPM ? 4 : 0;
   a.status = status;
   cudaError_t e = cudaFuncSetAttribute(lm_head_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) {
-    if (p.CL > 1)
-      e = launch_cluster_pdl(lm_head_kernel, dim3((unsigned)p.grid), dim3(kLT), kSmem, stream, p.CL, mh, mw, a);
-    else
-      e = launch_pdl(lm_head_kernel, dim3((unsigned)p.grid), dim3(kLT), kSmem, stream, mh, mw, a);
-  }
+  if (e == cudaSuccess)
+    e = launch_pdl(lm_head_kernel, dim3((unsigned)p.grid), dim3(kLT), kSmem, stream, mh, mw, a);
   if (e != cudaSuccess) return BASTION_ERR_LAUNCH;
   MergeArgs m;
   m.part_keys = a.part_keys;
