@@ -729,7 +729,8 @@ class PagedCache:
 
     page_table None: request r owns pages r * max_pages .. (r + 1) * max_pages - 1, i.e. the pools are a
     contiguous cache [B, max_pages * page_size, Hkv, D], which ``contiguous()`` gives to bastion_tree_attention.
-    weights: keep the accumulated attention weight and the position of every slot, which evict() needs."""
+    weights: keep the accumulated attention weight and the position of every slot, which evict() needs.
+    After STATUS_TIMEOUT in status, zero ws_attend before the next attend()."""
 
     def __init__(self, B, Hq, Hkv, D, page_size, max_pages, device, dtype=torch.bfloat16, page_table=None,
                  n_pages=None, weights=False):

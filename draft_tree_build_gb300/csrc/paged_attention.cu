@@ -45,20 +45,21 @@
 // up to 32,768 (70 us): the scores, stored once and read back from L2, and the second launch.
 // With D = 64 the tile's 12 products and the softmax have half the time: 98% all the same (2.6 GB).
 //
-// Every wait is bounded (~1 s); after one ran out the CTA flags the request,
-// waits for its own copies and products (bounded), frees its TMEM and returns.
+// Every wait is bounded (~1 s); after one ran out the CTA flags every request of
+// which it had tiles left, whose accumulated weights then stay as they were, waits
+// for its own copies and products (bounded), frees its TMEM and returns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
+#include "paged_walk.cuh"
 
 namespace bastion {
 
 namespace {
 
-constexpr int kTileKeys = 128;
 constexpr int kGroup = 24;        // parts joined at a time, at most
 constexpr int kPartFloats = 16 * 128 + 32;  // O of up to 16 heads, their references and sums
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -78,7 +79,7 @@ struct AttendArgs {
   float *acc_out;
   uint32_t *arrived;  // [2 * kMaxParts + kMaxUnits], zero between calls
   float *parts;       // [2 * kMaxParts, kPartFloats]
-  float *lse2;        // [B, Hq] base-2 log of the sum, of the scores in base 2
+  float *lse2;        // [B, Hq] base-2 log of the sum, of the scores in base 2; +inf: given up
   float *scores;      // [B, Hkv, tiles, G, 128], in base 2
   int tiles_cap;
   int swap;           // tensor map dimensions 1 and 2: (head, slot) instead of (slot, head)
@@ -281,70 +282,6 @@ __device__ __forceinline__ int clamped_len(const Paged &c, const AttendArgs &a, 
   return min(max(a.seq_len[r], 0), c.cap);
 }
 
-// A CTA's tiles, one after the other: tile t of the unit (request r, KV head g).
-// kUniform: all lanes of a warp walk together, and the compiler is told so.
-template <bool kUniform>
-struct Walk {
-  const int2 *list;  // the requests that have tiles: number and length
-  int li, r, n, tiles, g, t, left;
-  bool first;  // the first tile of its segment
-  __device__ __forceinline__ void load() {
-    const int2 e = list[li];
-    r = kUniform ? __shfl_sync(kFull, e.x, 0) : e.x;
-    n = kUniform ? __shfl_sync(kFull, e.y, 0) : e.y;
-    tiles = (n + kTileKeys - 1) / kTileKeys;
-  }
-  __device__ __forceinline__ void start(const int2 *l, int index, int off, int count) {
-    list = l;
-    li = index;
-    left = count;
-    first = true;
-    if (left > 0) {
-      load();
-      g = off / tiles;
-      t = off - g * tiles;
-    }
-  }
-  __device__ __forceinline__ void step(int heads) {
-    first = false;
-    --left;
-    if (++t == tiles) {
-      t = 0;
-      first = true;
-      if (++g == heads) {
-        g = 0;
-        ++li;
-        if (left > 0) load();
-      }
-    }
-  }
-  __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == 1; }
-};
-
-// The batch's tiles in equal shares: `big` CTAs of quot + 1 tiles, then shares
-// of quot.  A boundary moves to a unit's begin or end where cutting the unit
-// costs more in the join (1.4 us) than it saves: from anywhere in a unit of at
-// most kWhole tiles to the nearer end, and from within kSnap tiles of the ends
-// of a longer one.  Shares may become empty.  (8 units of 3 tiles: 6.6 us whole,
-// 9.9 us cut; 8 of 8 tiles: 8.0 us cut.)
-constexpr int kWhole = 4, kSnap = 1;
-struct Shares {
-  int n, quot, big;
-  __device__ __forceinline__ int begin(int cta) const { return cta * quot + min(cta, big); }
-  __device__ __forceinline__ int owner(int f) const {  // the share of tile f, before boundaries move
-    const int edge = big * (quot + 1);
-    return f < edge ? f / (quot + 1) : big + (f - edge) / quot;
-  }
-  // Where boundary f moves to; unit of t tiles, off = f - its begin.
-  static __device__ __forceinline__ int moved(int f, int off, int t) {
-    if (t <= kWhole) return 2 * off <= t ? f - off : f - off + t;
-    return off <= kSnap ? f - off : t - off <= kSnap ? f - off + t : f;
-  }
-  // The first and last CTA of a cut unit of tiles [u0, u1).
-  __device__ __forceinline__ int first_cta(int u0) const { return owner(u0 + kSnap); }
-  __device__ __forceinline__ int last_cta(int u1) const { return owner(u1 - kSnap - 1); }
-};
-
 // Value h of a small array by a thread's own index, without local memory.
 template <int N>
 __device__ __forceinline__ float pick(const float (&x)[N], int h) {
@@ -385,6 +322,15 @@ __device__ __forceinline__ uint32_t arrive_gpu(uint32_t *p) {
   uint32_t old;
   asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
   return old;
+}
+
+// Flags the requests of what is left of a share, and marks their rows for the
+// weights pass.  Out of line, like wait_slow.
+__device__ __noinline__ void leave(Walk<true> w, int heads, int32_t *status, float *lse2, int G, int kt) {
+  give_up(w, heads, [&](int r, int g) {
+    if (kt == 0) atomicOr(&status[r], BASTION_STATUS_TIMEOUT);
+    if (lse2 && kt < G) lse2[((size_t)r * heads + g) * G + kt] = INFINITY;
+  });
 }
 
 template <bool kHalf, int D, int GP>
@@ -920,6 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // a wait ran out, of which only one request has been told
+    if (w.left > 0) leave(w, c.Hkv, a.status, a.acc ? a.lse2 : nullptr, a.G, kt);
   }
   tc_fence_before();
   __syncthreads();
@@ -957,7 +905,7 @@ __global__ void __launch_bounds__(kWeightsThreads) paged_weights_kernel(Paged c,
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      if (y[h] == -INFINITY) continue;  // no such head, or one that sees nothing
+      if (isinf(y[h])) continue;  // -inf: no such head, or one that sees nothing; +inf: given up
       w[0] += exp2f(x[h].x - y[h]);
       w[1] += exp2f(x[h].y - y[h]);
       w[2] += exp2f(x[h].z - y[h]);

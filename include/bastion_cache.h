@@ -114,6 +114,8 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
  *          acc_out are left as they are.
  * scale    finite and > 0, else BASTION_ERR_SIZE.
  * NaN in a used key or query gives NaN in the heads that see it.
+ * A request that BASTION_STATUS_TIMEOUT flags may lack the outputs of some or
+ * all of its heads; acc_out is acc where a group's were not finished.
  * Scores, sums and outputs are accumulated in 32 bits.  Results do not depend
  * on the order in which the parts of a split row finish.
  * Limits: Hq a multiple of Hkv (BASTION_ERR_SIZE), Hq / Hkv <= 16
