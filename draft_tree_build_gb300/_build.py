@@ -1,7 +1,10 @@
 """In-tree build of libbastion.so (nvcc, sm_103a only).
 
 Each CUDA translation unit compiles in parallel; the shared library links the
-CUDA runtime statically so it loads without a separate libcudart.
+CUDA runtime statically so it loads without a separate libcudart.  Beside it
+gcc compiles a small CPython extension (csrc/marshal.c), the paged cache's short
+way from Python into the library; where that cannot be built, the library stands
+without it.
 """
 from __future__ import annotations
 
@@ -9,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,20 +40,47 @@ def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")]
-    files.append(os.path.join(CSRC, "marshal.c"))
     return files
 
 
+def _newer(path, inputs) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB, _inputs())
+
+
+def marshal_up_to_date() -> bool:
+    return _newer(MARSHAL, [os.path.join(CSRC, "marshal.c")] +
+                  [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")])
+
+
+def build_marshal() -> None:
+    """The extension, or a warning that says why there is none."""
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    try:
+        r = subprocess.run(["gcc", "-O2", "-std=gnu11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I",
+                            sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise OSError(r.stderr[-2000:])
+        os.replace(tmp, MARSHAL)
+    except OSError as e:
+        warnings.warn(f"csrc/marshal.c could not be built (the paged cache's calls take the way through ctypes): {e}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    if force or not up_to_date():
+        _build_library()
+    if force or not marshal_up_to_date():
+        build_marshal()
+    if verbose:
+        print(f"built {LIB}")
+    return LIB
+
+
+def _build_library() -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
@@ -64,28 +95,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
         return obj
 
-    def marshal():
-        tmp = MARSHAL + f".tmp{os.getpid()}"
-        r = subprocess.run(["gcc", "-O2", "-std=gnu11", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I",
-                            sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp],
-                           capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"gcc failed for marshal.c:\n{r.stderr[-4000:]}")
-        os.replace(tmp, MARSHAL)
-
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        m = ex.submit(marshal)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(one, SOURCES))
-        m.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "--cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB}")
-    return LIB
 
 
 if __name__ == "__main__":

@@ -11,6 +11,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -76,6 +77,18 @@ def _load_marshal(L):
     return m
 
 
+def _short_way(L):
+    """The compiled short way, or None where it is not there or cannot be loaded: the binding's own checks and ctypes
+    do the same then, a few microseconds a call later."""
+    if not _build.marshal_up_to_date():
+        return None
+    try:
+        return _load_marshal(L)
+    except (ImportError, OSError, AttributeError) as e:  # AttributeError: a torch without CUDA has no current stream
+        warnings.warn(f"the paged cache's calls take the way through ctypes: {e}")
+        return None
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -85,7 +98,7 @@ def lib(build_if_missing: bool = True):
     global _lib, _marshal
     if _lib is not None:
         return _lib
-    if build_if_missing and not _build.up_to_date():
+    if build_if_missing:
         _build.build()
     if not os.path.exists(_build.LIB):
         raise BastionError(f"libbastion.so not found at {_build.LIB}; run __graft_entry__.build()")
@@ -143,7 +156,7 @@ def lib(build_if_missing: bool = True):
     L.bastion_paged_evict_workspace_bytes.argtypes = [i32, i32, i64]
     L.bastion_paged_evict.restype = i32
     L.bastion_paged_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
-    _marshal = _load_marshal(L)
+    _marshal = _short_way(L)
     _lib = L
     return L
 
