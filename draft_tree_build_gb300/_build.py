@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libbastion.so")
-MARSHAL = os.path.join(BUILD, "bastion_marshal.so")  # csrc/marshal.c, a CPython extension
+# csrc/marshal.c, a CPython extension; it is built against one interpreter's C API, which its name says
+MARSHAL = os.path.join(BUILD, "bastion_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "topk_marginals.cu", "build_tree.cu", "verify_greedy.cu", "tree_attention.cu",
            "verify_noalloc.cu", "verify_sample.cu", "calibrate.cu",
            "build_tree_mixture.cu", "lm_head_topk.cu",

@@ -78,3 +78,14 @@ def test_an_extension_older_than_its_source_is_not_loaded(fresh, tmp_path):
     assert not _build.marshal_up_to_date()
     L = bastion.lib(build_if_missing=False)
     assert bastion._marshal is None and L is bastion.lib()
+
+
+def test_another_interpreter_has_a_file_of_its_own():
+    """The extension is built against one interpreter's C API: another looks for another file, and builds it."""
+    import importlib.machinery
+    import sys
+    import sysconfig
+    name = os.path.basename(_build.MARSHAL)
+    tag = sysconfig.get_config_var("EXT_SUFFIX")
+    assert name == "bastion_marshal" + tag and tag in importlib.machinery.EXTENSION_SUFFIXES
+    assert f"{sys.version_info[0]}{sys.version_info[1]}" in tag  # such as .cpython-312-aarch64-linux-gnu.so
