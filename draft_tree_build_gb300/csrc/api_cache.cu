@@ -2,6 +2,8 @@
 // manner of api.cu.
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "paged.cuh"
 
 namespace bastion {
@@ -63,9 +65,26 @@ bool apart(const void *a, const void *b, size_t bytes) {
 }
 bool same_or_apart(const void *a, const void *b, size_t bytes) { return a == b || apart(a, b, bytes); }
 
+// A contiguous array; null where an optional one is left out.
+struct Array {
+  const void *p;
+  size_t bytes;
+};
+// Whether each of the first is disjoint from each of the second.
+bool all_apart(std::initializer_list<Array> a, std::initializer_list<Array> b) {
+  for (const Array &x : a)
+    for (const Array &y : b) {
+      if (!x.p || !y.p) continue;
+      const uintptr_t u = (uintptr_t)x.p, v = (uintptr_t)y.p;
+      if (u < v + y.bytes && v < u + x.bytes) return false;
+    }
+  return true;
+}
+
 size_t slots_bytes(const bastion_paged_cache *c) {  // of acc and of pos
   return (size_t)c->B * c->Hkv * (size_t)c->max_pages * c->page_size * 4;
 }
+Array table_of(const bastion_paged_cache *c) { return {c->page_table, (size_t)c->B * c->max_pages * 4}; }
 
 // The batch's 128-key tiles are counted in 31 bits.
 bool tiles_ok(const bastion_paged_cache *c) {
@@ -123,6 +142,14 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
         !(apart(seq_len_out, n_seen_out, lens) || (seq_len_out == n_seen_out && seq_len == n_seen)))
       return BASTION_ERR_UNSUPPORTED;
   }
+  // a request's last CTA writes its lengths while others still read their lists
+  const size_t slots = slots_bytes(cache);
+  const Array table = table_of(cache), list = {rows, (size_t)cache->B * m * 4}, weights = {acc, slots}, places = {pos, slots},
+              flags = {status, lens};
+  if (!all_apart({{seq_len_out, lens}, {n_seen_out, lens}}, {list, table, weights, places, flags}) ||
+      !all_apart({weights, places, flags}, {{seq_len, lens}, {n_seen, lens}, {n_new, lens}, list, table}) ||
+      !all_apart({weights}, {places, flags}) || !all_apart({places}, {flags}))
+    return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_append_workspace_bytes(cache->B)) return BASTION_ERR_WORKSPACE;
   return bastion::launch_paged_append(bastion::paged_args(*cache), k_new, v_new, n_rows,
                                       cache->B > 1 ? new_stride_b : 0, n_rows > 1 ? new_stride_row : 0,

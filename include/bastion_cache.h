@@ -77,8 +77,9 @@ typedef struct {
  *               position of the next token); the same or disjoint.  Needed
  *               with acc and pos, else both may be NULL.  Where nothing is ever
  *               evicted they may be seq_len and seq_len_out.
- *               No output overlaps part of an input or of the other output
- *               (BASTION_ERR_UNSUPPORTED).
+ *               No output (the lengths, acc, pos, status) overlaps part of
+ *               another input or output (BASTION_ERR_UNSUPPORTED; the pools and
+ *               the new rows are the caller's to keep apart).
  * acc, pos      [B, Hkv, max_pages * page_size], both or neither NULL: the new
  *               slots get weight 0 and their token's position.
  * A request whose rows do not fit (seq_len + rows > max_pages * page_size)

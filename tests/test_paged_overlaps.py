@@ -1,0 +1,41 @@
+"""Arrays of the paged cache's calls that lie over one another: refused by the C ABI's host checks (fake pointers, never
+dereferenced).  A call whose arrays are apart gets as far as the last check, the workspace's size."""
+import ctypes
+
+import pytest
+
+from test_paged_refusals import UNSUPPORTED, WORKSPACE, _call, b  # noqa: F401
+
+vp = ctypes.c_void_p
+B, SLOTS = 4, 4 * 8 * 20 * 16 * 4  # requests; bytes of acc and of pos
+
+
+def _is(b, which, over, code):  # noqa: F811
+    """Refused for the overlap before the workspace is looked at, or for the workspace alone."""
+    assert _call(b, which, ws_bytes=0, **over) == code
+
+
+ROWS = dict(rows=vp(0xc00000), m=17)  # B * 17 entries
+
+
+@pytest.mark.parametrize("over", [
+    dict(ROWS, seq_len=vp(0xd00000), seq_len_out=vp(0xc00000)), dict(ROWS, seq_len=vp(0xd00000), seq_len_out=vp(0xc00000 + B * 17 * 4 - 4)),
+    dict(ROWS, n_seen=vp(0xd00000), n_seen_out=vp(0xc00040)), dict(ROWS, rows=vp(0x600008)),  # in place, the list over it
+    dict(seq_len_out=vp(0x300000)), dict(n_seen_out=vp(0x300000 + 4 * 20 * 4 - 4)),      # the page table
+    dict(seq_len_out=vp(0x800000)), dict(seq_len_out=vp(0x900000 + SLOTS - 4)), dict(seq_len_out=vp(0xb00000)),
+    dict(ROWS, rows=vp(0x800000 + SLOTS - 16)), dict(pos=vp(0x800000)), dict(pos=vp(0x800000 + SLOTS - 16)),
+    dict(acc=vp(0x600000)), dict(pos=vp(0x300000)), dict(status=vp(0x900000)), dict(status=vp(0x600000)),
+    dict(n_new=vp(0x800010)), dict(n_new=vp(0xb00000)),
+])
+def test_append(b, over):  # noqa: F811
+    _is(b, "append", over, UNSUPPORTED)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), ROWS, dict(ROWS, rows=vp(0x600000 + B * 4)), dict(ROWS, rows=vp(0x600000 - B * 17 * 4)),
+    dict(seq_len_out=vp(0x800000 - B * 4)), dict(seq_len_out=vp(0x800000 + SLOTS)), dict(pos=vp(0x800000 + SLOTS)),
+    dict(acc=None, pos=None, n_seen=None, n_seen_out=None), dict(n_new=vp(0xd00000)), dict(n_new=vp(0x600000)),
+    dict(n_seen=vp(0x600000), n_seen_out=vp(0x600000)),
+])
+def test_append_apart(b, over):  # noqa: F811
+    _is(b, "append", over, WORKSPACE)
