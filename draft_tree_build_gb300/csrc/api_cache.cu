@@ -212,6 +212,14 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
   if (!same_or_apart(seq_len, seq_len_out, lens) || !apart(n_seen, seq_len_out, lens) ||
       !same_or_apart(acc, acc_out, slots_bytes(cache)) || !same_or_apart(pos, pos_out, slots_bytes(cache)))
     return BASTION_ERR_UNSUPPORTED;
+  const size_t slots = slots_bytes(cache);
+  const Array table = table_of(cache), len = {seq_len, lens}, len_out = {seq_len_out, lens}, seen = {n_seen, lens},
+              weights = {acc, slots}, weights_out = {acc_out, slots}, places = {pos, slots}, places_out = {pos_out, slots},
+              flags = {status, lens};
+  if (!all_apart({len_out, flags}, {table, weights, weights_out, places, places_out}) ||
+      !all_apart({flags}, {len, len_out, seen}) || !all_apart({weights_out, places_out}, {table, len, seen}) ||
+      !all_apart({weights_out}, {places, places_out}) || !all_apart({places_out}, {weights}))
+    return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_evict_workspace_bytes(cache->B, cache->Hkv,
                                                             (int64_t)cache->max_pages * cache->page_size))
     return BASTION_ERR_WORKSPACE;

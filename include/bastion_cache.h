@@ -151,8 +151,9 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
  * seq_len_out   [B]: min(seq_len, budget).
  * acc_out, pos_out: slots below min(seq_len, budget) are written, the others
  *               left as they are.
- * Each output is its input's array or disjoint from every input
- * (BASTION_ERR_UNSUPPORTED where seq_len_out overlaps n_seen).
+ * Each output is its input's array or disjoint from every input, and from the
+ * other outputs and status (BASTION_ERR_UNSUPPORTED otherwise; the pools are the
+ * caller's to keep apart).
  * Limits: 1 <= budget, n_sink, n_recent >= 0, n_sink + n_recent <= budget
  * (BASTION_ERR_SIZE).
  * Workspace: bastion_paged_evict_workspace_bytes(B, Hkv,

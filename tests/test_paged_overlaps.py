@@ -39,3 +39,28 @@ def test_append(b, over):  # noqa: F811
 ])
 def test_append_apart(b, over):  # noqa: F811
     _is(b, "append", over, WORKSPACE)
+
+
+A0, P0, L0 = 0x10000000, 0x20000000, 0x400000  # evict's acc, pos and seq_len, each in place
+
+
+@pytest.mark.parametrize("over", [
+    dict(acc_out=vp(P0)), dict(pos_out=vp(A0)), dict(acc_out=vp(P0 + SLOTS - 16)), dict(pos_out=vp(A0 - SLOTS + 16)),
+    dict(acc_out=vp(0x30000000), pos_out=vp(0x30000000)), dict(acc_out=vp(0x30000000), pos_out=vp(0x30000000 + SLOTS - 16)),
+    dict(pos=vp(A0), pos_out=vp(P0)),  # acc in place over pos
+    dict(seq_len_out=vp(A0)), dict(seq_len_out=vp(P0 + SLOTS - 4)), dict(seq_len_out=vp(0x300000)),
+    dict(seq_len_out=vp(0xb00000)), dict(acc_out=vp(L0)), dict(pos_out=vp(0x500000)), dict(acc_out=vp(0x300000)),
+    dict(status=vp(L0)), dict(status=vp(0x500000)), dict(status=vp(A0)), dict(status=vp(P0 + 4)),
+    dict(acc_out=vp(0x30000000), seq_len_out=vp(0x30000000)), dict(status=vp(0x300000)),
+])
+def test_evict(b, over):  # noqa: F811
+    _is(b, "evict", over, UNSUPPORTED)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(acc_out=vp(A0 + SLOTS), pos_out=vp(P0 + SLOTS), seq_len_out=vp(L0 + B * 4)),
+    dict(pos=vp(A0 + SLOTS), pos_out=vp(A0 + SLOTS)), dict(acc_out=vp(P0 - SLOTS)), dict(acc=vp(P0), acc_out=vp(A0)) | dict(pos=vp(P0 + SLOTS), pos_out=vp(P0 + SLOTS)),
+    dict(seq_len_out=vp(0x500000 + B * 4)),
+])
+def test_evict_apart(b, over):  # noqa: F811
+    _is(b, "evict", over, WORKSPACE)
