@@ -81,6 +81,15 @@ bool all_apart(std::initializer_list<Array> a, std::initializer_list<Array> b) {
   return true;
 }
 
+// Whether an array is disjoint from each of n rows, `stride` >= 0 bytes apart.
+bool apart_from_rows(Array a, const void *first, int64_t row, int64_t stride, int64_t n) {
+  if (!a.p) return true;
+  const int64_t lo = (int64_t)((uintptr_t)a.p - (uintptr_t)first), hi = lo + (int64_t)a.bytes;
+  if (stride < row) return hi <= 0 || lo >= (n - 1) * stride + row;  // the rows leave no gaps
+  const int64_t i = lo < row ? 0 : (lo - row) / stride + 1;  // the first row that ends past the array's begin
+  return i >= n || i * stride >= hi;
+}
+
 size_t slots_bytes(const bastion_paged_cache *c) {  // of acc and of pos
   return (size_t)c->B * c->Hkv * (size_t)c->max_pages * c->page_size * 4;
 }
@@ -181,6 +190,14 @@ int bastion_paged_attention(const bastion_paged_cache *cache, const void *q, int
   const int64_t row = (int64_t)Hq * cache->D, q_st = cache->B > 1 ? q_stride_b : row;
   const uintptr_t q0 = (uintptr_t)q, q1 = q0 + 2 * (uintptr_t)((cache->B - 1) * q_st + row), o0 = (uintptr_t)out;
   if (!(q0 == o0 && q_st == row) && o0 < q1 && q0 < o0 + 2 * (uintptr_t)(cache->B * row)) return BASTION_ERR_UNSUPPORTED;
+  const size_t slots = slots_bytes(cache), lens = (size_t)cache->B * 4;
+  const Array table = table_of(cache), len = {seq_len, lens}, flags = {status, lens}, result = {out, (size_t)(2 * cache->B * row)},
+              logs = {lse, lens * Hq}, weights = {acc, slots}, weights_out = {acc_out, slots};
+  if (!all_apart({result, logs, weights_out, flags}, {table, len}) || !all_apart({logs, flags}, {result, weights, weights_out}) ||
+      !all_apart({logs}, {flags}) || !all_apart({result}, {weights, weights_out}))
+    return BASTION_ERR_UNSUPPORTED;
+  for (const Array &x : {logs, weights_out, flags})
+    if (!apart_from_rows(x, q, 2 * row, 2 * q_st, cache->B)) return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_attention_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D,
                                                                 (int64_t)cache->max_pages * cache->page_size,
                                                                 acc != nullptr))

@@ -113,6 +113,9 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
  * acc, acc_out  [B, Hkv, max_pages * page_size] float, 16-byte aligned, both or
  *          neither NULL; the same array or disjoint ones.  Slots at or past seq_len[r] of
  *          acc_out are left as they are.
+ * out, lse, acc_out and status lie apart from one another and, but for the two
+ * places in place above, from every input (BASTION_ERR_UNSUPPORTED; the pools
+ * are the caller's to keep apart).
  * scale    finite and > 0, else BASTION_ERR_SIZE.
  * NaN in a used key or query gives NaN in the heads that see it.
  * A request that BASTION_STATUS_TIMEOUT flags may lack the outputs of some or

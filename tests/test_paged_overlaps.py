@@ -64,3 +64,31 @@ def test_evict(b, over):  # noqa: F811
 ])
 def test_evict_apart(b, over):  # noqa: F811
     _is(b, "evict", over, WORKSPACE)
+
+
+Q0, Q, O0, W0, WO = 0x400000, 32 * 128 * 2, 0x600000, 0x10000000, 0x20000000  # q, a row of it, out, acc, acc_out
+WIDE = dict(q_stride_b=2 * 32 * 128)  # rows of a fused projection: gaps as wide as they are
+LSE = B * 32 * 4
+
+
+@pytest.mark.parametrize("over", [
+    dict(lse=vp(0x500000)), dict(lse=vp(0x300000)), dict(lse=vp(O0)), dict(lse=vp(O0 + B * Q - 4)), dict(lse=vp(W0)),
+    dict(lse=vp(WO + SLOTS - 4)), dict(lse=vp(0xb00000)), dict(lse=vp(Q0)), dict(lse=vp(Q0 + B * Q - 4)),
+    dict(lse=vp(Q0 - LSE + 4)), dict(WIDE, lse=vp(Q0 + 2 * Q - 4)), dict(WIDE, lse=vp(Q0 + 2 * Q - LSE + 4)),
+    dict(WIDE, lse=vp(Q0 + 6 * Q)), dict(WIDE, status=vp(Q0 + 7 * Q - 4)), dict(q_stride_b=0, lse=vp(Q0 + Q - 4)),
+    dict(out=vp(0x500000)), dict(out=vp(0x300000)), dict(out=vp(W0)), dict(out=vp(WO + SLOTS - 16)), dict(out=vp(0xb00000)),
+    dict(acc_out=vp(0x500000)), dict(acc_out=vp(0x300000)), dict(acc_out=vp(Q0)), dict(WIDE, acc_out=vp(Q0 + Q)),
+    dict(status=vp(0x500000)), dict(status=vp(0x300000)), dict(status=vp(W0)), dict(status=vp(O0)),
+])
+def test_attention(b, over):  # noqa: F811
+    _is(b, "attend", over, UNSUPPORTED)
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(lse=vp(O0 + B * Q)), dict(lse=vp(O0 - LSE)), dict(lse=vp(Q0 + B * Q)), dict(lse=vp(Q0 - LSE)),
+    dict(WIDE, lse=vp(Q0 + Q)), dict(WIDE, lse=vp(Q0 + 2 * Q - LSE)), dict(WIDE, lse=vp(Q0 + 7 * Q)),
+    dict(WIDE, status=vp(Q0 + 5 * Q)), dict(q_stride_b=0, lse=vp(Q0 + Q)), dict(q_stride_b=0, lse=vp(Q0 - LSE)),
+    dict(out=vp(Q0)), dict(acc_out=vp(W0)), dict(acc=None, acc_out=None, lse=vp(WO)), dict(acc_out=vp(W0 + SLOTS)),
+])
+def test_attention_apart(b, over):  # noqa: F811
+    _is(b, "attend", over, WORKSPACE)
