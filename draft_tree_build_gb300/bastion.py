@@ -544,7 +544,7 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
         if rc is not None:
             return _check(rc, "bastion_paged_evict")
     dev, B, Hkv, _, cap, cache = _cache(k_pool, v_pool, page_table)
-    if max(budget, n_sink, n_recent) >= 1 << 31:  # ctypes would cut it to 32 bits
+    if not all(-(1 << 31) <= x < 1 << 31 for x in (budget, n_sink, n_recent)):  # ctypes would cut it to 32 bits
         raise BastionError("paged evict: budget, n_sink and n_recent must fit 32 bits")
     _need("seq_len n_seen seq_len_out status", dev, torch.int32, (B,), seq_len, n_seen, seq_len_out, status)
     _need("acc acc_out", dev, torch.float32, (B, Hkv, cap), acc, acc_out)
