@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kLT, 1)
   const int mt = blockIdx.x % a.MT, j0 = blockIdx.x / a.MT;
   const int ntile = j0 < a.NT ? (a.NT - j0 + a.CPM - 1) / a.CPM : 0;  // N-tiles of this CTA
   const int steps = ntile * a.KC;
-  // the request of the CTA's first row takes a timeout bit (rows past the
-  // batch never get one)
+  // the request of the CTA's first row takes the bit of a wait that ran out
+  // (rows past the batch never get one); the epilogue flags the other rows' requests
   int32_t *st0 = &a.status[min(mt * kBM, a.rows - 1) / a.b];
 
   if (tid == 0) {
@@ -433,7 +433,11 @@ __global__ void __launch_bounds__(kLT, 1)
     };
     for (int t = 0; t < ntile; ++t) {
       const int buf = t & 1;
-      if (!__all_sync(kFull, wait_bar(&bs.acc_full[buf], (uint32_t)(t >> 1) & 1u, abort, st0))) break;
+      if (!__all_sync(kFull, wait_bar(&bs.acc_full[buf], (uint32_t)(t >> 1) & 1u, abort, st0))) {
+        // some of the vocabulary is missing from every row of the tile, whose rows are several requests'
+        if (live) atomicOr(&a.status[row / a.b], BASTION_STATUS_TIMEOUT);
+        break;
+      }
       tc_fence_after();
       const int n = j0 + t * a.CPM;
       const uint32_t tbase = lane_base + (uint32_t)buf * kBN;
