@@ -1,5 +1,6 @@
 """Python binding of the C ABI in ``include/bastion.h`` and
-``include/bastion_cache.h`` (ctypes; argument marshalling only).  Every function takes CUDA tensors, passes their device
+``include/bastion_cache.h`` (ctypes; argument checks and marshalling, the paged cache's also in C, csrc/marshal.c).
+Every function takes CUDA tensors, passes their device
 pointers and the current stream to ``libbastion.so``, and raises on a negative
 return code.  All computation happens in the library's kernels; there is no
 fallback path: if the library cannot be loaded, every call raises.

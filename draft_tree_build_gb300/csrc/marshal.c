@@ -2,7 +2,7 @@
  *
  * A call of a few microseconds on the GPU should not take ten on the host: this
  * module checks a call's tensors and calls the library without ctypes and with
- * no Python code in between (attention 10.2 -> 6 us, of which the launch is
+ * no Python code in between (attention 10.2 -> 7.0 us, of which the launch is
  * 2.5).  It accepts what is plainly right and nothing else: every function
  * returns the library's return code, or None, with nothing called, where any
  * argument is not what the call takes; the binding then checks again, in

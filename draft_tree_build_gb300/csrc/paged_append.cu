@@ -3,9 +3,10 @@
 // slots.  A copy, bound by HBM: each row is read once and written once, 16
 // bytes a thread with eight loads in flight, consecutive threads on consecutive
 // bytes of a row (rows of 2 * D bytes, or Hkv of them in a slot-major pool).
-// Prompts (8 requests of up to 8,192 tokens, 304 MB both ways): 49.3 us, 91% of
-// the copy bandwidth (four loads in flight: 50.8).  The accepted paths of 32
-// requests (17 rows): 3.9 us, a launch and three dependent reads.
+// Prompts (8 requests of up to 8,192 tokens, 292 MB both ways): 50.0 us, 86% of
+// the copy bandwidth (four loads in flight: 3% slower).  The accepted paths of 32
+// requests (17 rows): 4.0 us, a launch and three dependent reads (as a captured graph
+// replays them; a call from Python takes the host 8.4).
 #include "paged.cuh"
 
 namespace bastion {
@@ -142,7 +143,8 @@ int launch_paged_append(const Paged &c, const void *k_new, const void *v_new, in
   a.m = m;
   a.arrived = static_cast<uint32_t *>(ws);
   a.status = status;
-  // fewer rows a CTA while the device has SMs to spare (17 rows of 32 requests: 5.6 us with 16, 4.1 with 4)
+  // fewer rows a CTA while the device has SMs to spare (17 rows of 32 requests: 5.7 us with 16, 4.5 with 8, 4.2 with 4, 2
+  // and the 1 that this takes; prompts of 8 x 8,192 rows: 51 us with 16, as this takes, 56 with 8, 69 with 4)
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

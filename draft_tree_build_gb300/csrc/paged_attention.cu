@@ -25,11 +25,13 @@
 //    maximum, otherwise the references move and O is rescaled.  Sums stay in
 //    the threads until the segment ends;
 //  * P is written as a high and a low 16-bit term in separate columns (N = 2 x 8
-//    or 2 x 16), which the tensor cores multiply alike: the weights keep
-//    16 bits or more, where one bf16 term would add 2^-9 of noise to the output.
+//    or 2 x 16), which the tensor cores multiply alike, where one bf16 term would
+//    add 2^-9 of noise to the output.  bf16: every weight to 2^-17 of itself.
+//    Half precision: its low term ends at 2^-24, so that the weights are scaled
+//    by 2^6 and are off by at most 2^-31 of the part's largest (and 2^-22 of
+//    themselves); those below it are 0 in the product, but not in the sum.
 //    P is stored key by key (16 bytes a thread, an MN-major operand without
-//    swizzle).  Half precision weights are scaled by 2^6, so that those below
-//    2^-24 of the largest are not lost.
+//    swizzle).
 //  * value rows past the sequence's end (a page's unused slots may hold NaN) are
 //    zeroed in shared memory; their scores are masked.
 //
@@ -37,12 +39,13 @@
 // sum_h exp2(s - lse_h) to each slot's accumulated weight.
 //
 // Measured, cold caches, 32 query heads on 8 KV heads, D = 128: 64 requests of up to 16,384
-// tokens (2.4 GB) 368 us, 98% of the copy bandwidth; 8 of 4,096 (134 MB) 28.4 us, 70%; one of
-// 131,072 (537 MB) 89 us, 89%; one of 300 (1.2 MB) 6.8 us.  What is left of the small ones is
+// tokens (2.5 GB) 369 us, the copy bandwidth; 8 of 4,096 (134 MB) 29.1 us, 68%; one of
+// 131,072 (537 MB) 89 us, 89%; one of 300 (1.2 MB) 7.2 us.  What is left of the small ones is
 // latency: a launch (2.2 us), the dependent reads of lengths and page table before the first copy
 // (1.5 us), the last tile's chain of products and softmax (1 us) and, where a unit is shared, the
 // join (1.4 us).  The accumulated weights add 5 us to 32 requests of 2,065 tokens (53 us) and 12 us to 8 of
-// up to 32,768 (70 us): the scores, stored once and read back from L2, and the second launch.
+// up to 32,768 (153,588 in all, 70 us): the scores, stored once and read back from L2, and the second
+// launch, which covers the whole capacity (those 32 requests: 81 us in tables of 32,768 slots).
 // With D = 64 the tile's 12 products and the softmax have half the time: 98% all the same (2.6 GB).
 //
 // Every wait is bounded (~1 s); after one ran out the CTA flags every request of

@@ -15,9 +15,9 @@
 // what another writes.  Weights and positions are read once (the keys stay in
 // shared memory) and only the holes' rows move.
 //
-// Few tokens leaving (32 requests x 8 heads, 2,065 slots cut to 2,048): 10.2 us, a chain of some
-// ten phases with a barrier each, against 1.9 us of traffic; as two launches it took 14.2 us.
-// Prompts cut (8 x 8 heads, up to 32,768 slots to 4,096): 55 us, of which the moves take two
+// Few tokens leaving (32 requests x 8 heads, 2,065 slots cut to 2,048): 10.2 us with the weights in L2
+// (11.6 without), a chain of some ten phases with a barrier each, against 1.9 us of traffic; as two
+// launches it took 14.2 us.  Prompts cut (8 x 8 heads, up to 32,768 slots to 4,096): 56 us, of which the moves take two
 // thirds at 5.5 TB/s (rows of 256 bytes in no order) and the selection the rest; as two
 // launches, one CTA a head selecting, 88 us.  11, 12 or 13 bits in the first histogram are alike
 // within 3% (12 leaves fewer keys in the bin than 11 and clears faster than 13).  The loops take a
