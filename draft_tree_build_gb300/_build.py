@@ -45,7 +45,10 @@ def _inputs():
 
 
 def _newer(path, inputs) -> bool:
-    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
+    if not os.path.exists(path):
+        return False
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t for f in inputs)
 
 
 def up_to_date() -> bool:
@@ -53,8 +56,8 @@ def up_to_date() -> bool:
 
 
 def marshal_up_to_date() -> bool:
-    return _newer(MARSHAL, [os.path.join(CSRC, "marshal.c")] +
-                  [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")])
+    files = [os.path.join(CSRC, "marshal.c")] + [os.path.join(INCLUDE, f) for f in ("bastion.h", "bastion_cache.h")]
+    return _newer(MARSHAL, [f for f in files if os.path.exists(f)])  # a built tree may come without its sources
 
 
 def build_marshal() -> None:

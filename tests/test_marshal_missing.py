@@ -89,3 +89,11 @@ def test_another_interpreter_has_a_file_of_its_own():
     tag = sysconfig.get_config_var("EXT_SUFFIX")
     assert name == "bastion_marshal" + tag and tag in importlib.machinery.EXTENSION_SUFFIXES
     assert f"{sys.version_info[0]}{sys.version_info[1]}" in tag  # such as .cpython-312-aarch64-linux-gnu.so
+
+
+def test_a_built_tree_without_its_sources(fresh, tmp_path):
+    """The built files alone are enough where nothing is to be built."""
+    fresh.setattr(_build, "CSRC", str(tmp_path / "csrc"))
+    fresh.setattr(_build, "INCLUDE", str(tmp_path / "include"))
+    bastion.lib(build_if_missing=False)
+    assert bastion._marshal is not None
