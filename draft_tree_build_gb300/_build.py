@@ -26,7 +26,8 @@ MARSHAL = os.path.join(BUILD, "bastion_marshal" + sysconfig.get_config_var("EXT_
 SOURCES = ["api.cu", "topk_marginals.cu", "build_tree.cu", "verify_greedy.cu", "tree_attention.cu",
            "verify_noalloc.cu", "verify_sample.cu", "calibrate.cu",
            "build_tree_mixture.cu", "lm_head_topk.cu",
-           "api_cache.cu", "paged_append.cu", "paged_attention.cu", "paged_evict.cu"]
+           "api_cache.cu", "paged_append.cu", "paged_attention.cu", "paged_evict.cu",
+           "paged_plan.cu", "qk_norm_rope.cu", "paged_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 import struct
 import warnings
@@ -31,6 +32,8 @@ STATUS_BAD_TREE = 16
 STATUS_BAD_WEIGHT = 32
 STATUS_BAD_PAGE = 64
 STATUS_BAD_ROW = 128
+STATUS_NO_PAGE = 256
+STATUS_BAD_GROUP = 512
 STATUS_TIMEOUT = 1 << 30
 
 # the exported C symbols, in header order
@@ -51,6 +54,8 @@ CACHE_SYMBOLS = (
     "bastion_paged_append_workspace_bytes", "bastion_paged_append",
     "bastion_paged_attention_workspace_bytes", "bastion_paged_attention",
     "bastion_paged_evict_workspace_bytes", "bastion_paged_evict",
+    "bastion_paged_plan_workspace_bytes", "bastion_paged_plan", "bastion_qk_norm_rope",
+    "bastion_paged_prefix_attention_workspace_bytes", "bastion_paged_prefix_attention",
 )
 
 
@@ -75,6 +80,8 @@ def _load_marshal(L):
     m.init(torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8, torch._C._cuda_getDevice,
            torch._C._cuda_getCurrentRawStream, address(L.bastion_paged_append), address(L.bastion_paged_attention),
            address(L.bastion_paged_evict))
+    m.init_layer(torch.int64, torch.float64, address(L.bastion_paged_plan), address(L.bastion_qk_norm_rope),
+                 address(L.bastion_paged_prefix_attention))
     return m
 
 
@@ -157,6 +164,18 @@ def lib(build_if_missing: bool = True):
     L.bastion_paged_evict_workspace_bytes.argtypes = [i32, i32, i64]
     L.bastion_paged_evict.restype = i32
     L.bastion_paged_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
+    L.bastion_paged_plan_workspace_bytes.restype = sz
+    L.bastion_paged_plan_workspace_bytes.argtypes = [i32]
+    L.bastion_paged_plan.restype = i32
+    L.bastion_paged_plan.argtypes = [vp, i32, i32, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp,
+                                     vp, sz, vp, vp]
+    L.bastion_qk_norm_rope.restype = i32
+    L.bastion_qk_norm_rope.argtypes = [i32] * 5 + [vp, i64, i64] * 3 + [vp, vp, f32, vp, vp, i32, i32, f32] \
+        + [vp, i64, i64] * 2 + [vp, vp, vp, vp]
+    L.bastion_paged_prefix_attention_workspace_bytes.restype = sz
+    L.bastion_paged_prefix_attention_workspace_bytes.argtypes = [i32] * 5
+    L.bastion_paged_prefix_attention.restype = i32
+    L.bastion_paged_prefix_attention.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, i64, vp, f32, vp, vp, vp, sz, vp, vp]
     _marshal = _short_way(L)
     _lib = L
     return L
@@ -409,6 +428,10 @@ def _launch_on(dev, stream, workspace):
     if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise BastionError("paged cache: the workspace must be contiguous uint8 (bastion.workspace) on the tensors' "
                            "device")
+    return _stream_on(dev, stream)
+
+
+def _stream_on(dev, stream):
     if dev < 0:
         raise BastionError("tensor must live on a CUDA device")
     if dev != torch.cuda.current_device():
@@ -556,6 +579,176 @@ def bastion_paged_evict(k_pool, v_pool, page_table, seq_len, n_seen, acc, pos, b
                                    pos_out.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr(),
                                    st_cuda)
     _check(rc, "bastion_paged_evict")
+
+
+def bastion_paged_plan_workspace_bytes(B: int) -> int:
+    return int(lib().bastion_paged_plan_workspace_bytes(B))
+
+
+def bastion_paged_plan(page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos,
+                       workspace, status, n_new=None, row_start=None, seq_len_out=None, trim=False, stream=None):
+    """Pages and slots for the next n_new (all: m) tokens of every request.  page_table [B, max_pages]; held [B] pages
+    in it; free_pages [n_pages] a stack of n_free [1]; slots int64 and pos int32 of B * m rows (request by request), or,
+    with row_start [B + 1], of any number of rows, packed.  held_out, n_free_out and seq_len_out may be their inputs."""
+    if _marshal is not None:
+        rc = _marshal.plan(page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos,
+                           workspace, status, n_new, row_start, seq_len_out, trim, stream)
+        if rc is not None:
+            return _check(rc, "bastion_paged_plan")
+    table, dev = page_table.shape, page_table.get_device()
+    if len(table) != 2 or page_table.dtype is not torch.int32 or not page_table.is_contiguous():
+        raise BastionError("paged plan: page_table must be contiguous int32 [B, max_pages]")
+    if not all(-(1 << 31) <= x < 1 << 31 for x in (page_size, m)):
+        raise BastionError("paged plan: page_size and m must fit 32 bits")
+    B, max_pages = table
+    n_rows = slots.numel()
+    _need("seq_len held held_out status n_new seq_len_out", dev, torch.int32, (B,), seq_len, held, held_out, status, n_new,
+          seq_len_out)
+    _need("n_free n_free_out", dev, torch.int32, (1,), n_free, n_free_out)
+    _need("free_pages", dev, torch.int32, (free_pages.numel(),), free_pages)
+    _need("slots", dev, torch.int64, slots.shape, slots)
+    _need("pos", dev, torch.int32, slots.shape, pos)
+    _need("row_start", dev, torch.int32, (B + 1,), row_start)
+    st_cuda = _launch_on(dev, stream, workspace)
+    rc = lib().bastion_paged_plan(page_table.data_ptr(), B, max_pages, page_size, free_pages.numel(), seq_len.data_ptr(),
+                                  _ptr(n_new), m, _ptr(seq_len_out), held.data_ptr(), held_out.data_ptr(),
+                                  free_pages.data_ptr(), n_free.data_ptr(), n_free_out.data_ptr(), 1 if trim else 0,
+                                  slots.data_ptr(), pos.data_ptr(), n_rows, _ptr(row_start), workspace.data_ptr(),
+                                  workspace.numel(), status.data_ptr(), st_cuda)
+    _check(rc, "bastion_paged_plan")
+
+
+def rope_frequencies(rot_dim, base=10000.0, device="cuda", scaling=None, factor=1.0, low=1.0, high=4.0, length=8192):
+    """(inv_freq [rot_dim / 2] float64, the factor of cosines and sines) for bastion_qk_norm_rope.
+
+    scaling None: base ** (-2 i / rot_dim).  For contexts `factor` times longer than the `length` that a model was
+    trained on: "linear" divides every frequency by it; "base" raises the base so that the slowest pair is slowed by
+    it and the fastest not at all; "bands" divides the frequencies that turn fewer than `low` times over the length,
+    keeps those that turn more than `high` times, and goes over evenly in between; "yarn" does so by the pairs' number
+    instead (low and high the turns, 1 and 32 by default in that method), and scales cosines and sines by
+    0.1 log(factor) + 1."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    f, size = base ** (-i / rot_dim), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "base":
+        f = (base * factor ** (rot_dim / (rot_dim - 2))) ** (-i / rot_dim)
+    elif scaling == "bands":
+        turns = length * f / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling == "yarn":
+        # the pair that turns n times over the length
+        pair = lambda n: rot_dim * math.log(length / (n * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rot_dim - 1)
+        slow = ((i / 2 - first) / max(last - first, 1e-3)).clamp(0, 1)
+        f = f * (1 - slow + slow / factor)
+        size = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling is not None:
+        raise BastionError(f"rope frequencies: scaling must be None, linear, base, bands or yarn, got {scaling!r}")
+    return f.to(device), size
+
+
+def _heads(name, t, dev, dtype, shape):
+    """(address, token stride, head stride) of [T, H, D] rows with a contiguous last dimension; None: no rows."""
+    if t is None:
+        return None, 0, 0
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or st[2] != 1:
+        raise BastionError(f"norm and rope: {name} must be {dtype} {list(shape)} with a contiguous last dimension on "
+                           f"device {dev}, got {t.dtype} {list(t.shape)}, strides {st}, on {t.device}")
+    return t.data_ptr(), st[0], st[1]
+
+
+def bastion_qk_norm_rope(q, k, pos, inv_freq, q_out, status, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
+                         interleaved=False, factor=1.0, v=None, k_pool=None, v_pool=None, slots=None, stream=None):
+    """q [T, Hq, D], k and v [T, Hkv, D] (any strides, last dim contiguous), pos [T] int32, inv_freq [rot_dim / 2]
+    float64 (None: nothing is turned); q_out and k_out may be q and k, or None.  With k_pool, v_pool [n_pages,
+    page_size, Hkv, D] and slots [T] int64, keys and values go into the cache.  status [1]."""
+    if _marshal is not None:
+        rc = _marshal.rope(q, k, pos, inv_freq, q_out, status, k_out, q_weight, k_weight, eps, interleaved, factor, v,
+                           k_pool, v_pool, slots, stream)
+        if rc is not None:
+            return _check(rc, "bastion_qk_norm_rope")
+    if q.dim() != 3 or k.dim() != 3:
+        raise BastionError("norm and rope: q must be [T, Hq, D] and k [T, Hkv, D]")
+    T, Hq, D = q.shape
+    Hkv, dtype, dev = k.shape[1], q.dtype, q.get_device()
+    dt = _CACHE_DTYPES.get(dtype)
+    if dt is None:
+        raise BastionError(f"norm and rope: q must be bfloat16 or float16, got {dtype}")
+    rows = (*_heads("q", q, dev, dtype, (T, Hq, D)), *_heads("k", k, dev, dtype, (T, Hkv, D)),
+            *_heads("v", v, dev, dtype, (T, Hkv, D)))
+    outs = (*_heads("q_out", q_out, dev, dtype, (T, Hq, D)), *_heads("k_out", k_out, dev, dtype, (T, Hkv, D)))
+    _need("q_weight k_weight", dev, dtype, (D,), q_weight, k_weight)
+    _need("pos", dev, torch.int32, (T,), pos)
+    _need("slots", dev, torch.int64, (T,), slots)
+    _need("status", dev, torch.int32, (1,), status)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need("inv_freq", dev, torch.float64, (rot // 2,), inv_freq)
+    cache = None
+    if k_pool is not None or v_pool is not None:
+        if k_pool is None or v_pool is None:
+            raise BastionError("norm and rope: k_pool and v_pool go together")
+        shape, st = k_pool.shape, k_pool.stride()
+        if len(shape) != 4 or shape != v_pool.shape or k_pool.dtype is not dtype or v_pool.dtype is not dtype \
+                or st[3] != 1 or not _same_strides(k_pool, v_pool):
+            raise BastionError("norm and rope: the pools must be [n_pages, page_size, Hkv, D] of q's dtype, of one shape "
+                               "and equal strides, with a contiguous last dimension")
+        if k_pool.get_device() != dev or v_pool.get_device() != dev:
+            raise BastionError("norm and rope: the pools must be on q's device")
+        # the struct's table is not read: any address of the right alignment serves
+        cache = _PAGED_CACHE.pack(k_pool.data_ptr(), v_pool.data_ptr(), shape[0], st[0], st[1], st[2],
+                                  status.data_ptr(), dt, 1, shape[2], shape[3], shape[1], 1)
+    st_cuda = _stream_on(dev, stream)
+    rc = lib().bastion_qk_norm_rope(dt, T, Hq, Hkv, D, *rows, _ptr(q_weight), _ptr(k_weight), eps, pos.data_ptr(),
+                                    _ptr(inv_freq), rot, 1 if interleaved else 0, factor, *outs, cache, _ptr(slots),
+                                    status.data_ptr(), st_cuda)
+    _check(rc, "bastion_qk_norm_rope")
+
+
+def bastion_paged_prefix_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, n_groups: int) -> int:
+    return int(lib().bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D, n_groups))
+
+
+def bastion_paged_prefix_attention(q, k_pool, v_pool, page_table, seq_len, prefix_table, prefix_len, group_start, scale,
+                                   out, workspace, status, lse=None, stream=None):
+    """bastion_paged_attention over each group's prefix, pages prefix_table [n_groups, max_prefix_pages] and slots
+    prefix_len [n_groups], and then over each request's own slots; group g is the requests group_start[g] up to
+    group_start[g + 1] ([n_groups + 1], ascending).  q [B, Hq, D] (heads contiguous, any stride between requests), out
+    [B, Hq, D] contiguous, lse [B, Hq] float32 or None."""
+    if _marshal is not None:
+        rc = _marshal.prefix(q, k_pool, v_pool, page_table, seq_len, prefix_table, prefix_len, group_start, scale, out,
+                             workspace, status, lse, stream)
+        if rc is not None:
+            return _check(rc, "bastion_paged_prefix_attention")
+    dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
+    qs, st, dtype = q.shape, q.stride(), q.dtype
+    if len(qs) != 3 or dtype is not k_pool.dtype or qs[0] != B or qs[2] != D:
+        raise BastionError("prefix attention: q must be [B, Hq, D] of the pools' dtype")
+    Hq = qs[1]
+    if st[2] != 1 or (Hq > 1 and st[1] != D):
+        raise BastionError("prefix attention: the heads of q must be contiguous")
+    if q.get_device() != dev:
+        raise BastionError("prefix attention: q must be on the pools' device")
+    if prefix_table.dim() != 2:
+        raise BastionError("prefix attention: prefix_table must be [n_groups, max_prefix_pages]")
+    groups, pages = prefix_table.shape
+    _need("out", dev, dtype, qs, out)
+    _need("seq_len status", dev, torch.int32, (B,), seq_len, status)
+    _need("prefix_table", dev, torch.int32, (groups, pages), prefix_table)
+    _need("prefix_len", dev, torch.int32, (groups,), prefix_len)
+    _need("group_start", dev, torch.int32, (groups + 1,), group_start)
+    if lse is not None:
+        _need("lse", dev, torch.float32, (B, Hq), lse)
+    st_cuda = _launch_on(dev, stream, workspace)
+    rc = lib().bastion_paged_prefix_attention(cache, prefix_table.data_ptr(), pages, prefix_len.data_ptr(),
+                                              group_start.data_ptr(), groups, q.data_ptr(), Hq, st[0],
+                                              seq_len.data_ptr(), scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                                              workspace.numel(), status.data_ptr(), st_cuda)
+    _check(rc, "bastion_paged_prefix_attention")
 
 
 # --------------------------------------------------------------------------- buffers

@@ -82,6 +82,8 @@ const char *bastion_status_string(int code) {
     case BASTION_STATUS_BAD_WEIGHT: return "a mixture weight is negative or not finite";
     case BASTION_STATUS_BAD_PAGE: return "a used page table entry outside the pool";
     case BASTION_STATUS_BAD_ROW: return "an appended row index outside the new rows";
+    case BASTION_STATUS_NO_PAGE: return "too few free pages for the request's new tokens";
+    case BASTION_STATUS_BAD_GROUP: return "a group of requests outside the batch";
     case BASTION_STATUS_TIMEOUT: return "a bounded device wait ran out";
     default: return "unknown code";
   }

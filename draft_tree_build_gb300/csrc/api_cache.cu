@@ -21,6 +21,22 @@ size_t paged_evict_workspace_bytes(int B, int Hkv, int64_t cap);
 int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_seen, const float *acc,
                        const int32_t *pos, int budget, int n_sink, int n_recent, int32_t *seq_len_out,
                        float *acc_out, int32_t *pos_out, void *ws, int32_t *status, cudaStream_t stream);
+int launch_paged_plan(int32_t *table, int B, int max_pages, int page, int64_t n_pages, const int32_t *seq_len,
+                      const int32_t *n_new, int m, int32_t *seq_len_out, const int32_t *held, int32_t *held_out,
+                      int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
+                      int32_t *pos, int64_t n_rows, int32_t *row_start, void *ws, int32_t *status,
+                      cudaStream_t stream);
+int launch_qk_norm_rope(bool half, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t, int64_t q_st_h,
+                        const void *k, int64_t k_st_t, int64_t k_st_h, const void *v, int64_t v_st_t, int64_t v_st_h,
+                        const void *q_weight, const void *k_weight, float eps, const int32_t *pos,
+                        const double *inv_freq, int rot, bool pairs, float factor, void *q_out, int64_t q_out_st_t,
+                        int64_t q_out_st_h, void *k_out, int64_t k_out_st_t, int64_t k_out_st_h, const Paged &c,
+                        const int64_t *slots, int32_t *status, cudaStream_t stream);
+size_t paged_prefix_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups);
+int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, int max_prefix_pages,
+                        const int32_t *prefix_len, const int32_t *group_start, int n_groups, const void *q, int Hq,
+                        int64_t q_st_b, const int32_t *seq_len, float scale, void *out, float *lse, void *ws,
+                        int32_t *status, cudaStream_t stream);
 
 Paged paged_args(const bastion_paged_cache &c) {
   Paged p;
@@ -98,6 +114,23 @@ Array table_of(const bastion_paged_cache *c) { return {c->page_table, (size_t)c-
 // The batch's 128-key tiles are counted in 31 bits.
 bool tiles_ok(const bastion_paged_cache *c) {
   return (int64_t)c->B * c->Hkv * (((int64_t)c->max_pages * c->page_size + 127) / 128) < (1LL << 31);
+}
+
+// Rows of T tokens and H heads of D elements, at st_t and st_h elements.
+struct Rows {
+  const void *p;
+  int64_t T, st_t, H, st_h, D;
+  int64_t token() const { return (H - 1) * st_h + D; }  // from a token's first element to past its last
+  Array span() const { return {p, (size_t)(2 * ((T - 1) * st_t + token()))}; }
+};
+// Whether two such arrays are disjoint: apart as a whole, or slices of the same tokens' rows.
+bool rows_apart(const Rows &a, const Rows &b) {
+  if (!a.p || !b.p || all_apart({a.span()}, {b.span()})) return true;
+  if (a.T == 1 || b.T == 1 || a.st_t != b.st_t || a.token() > a.st_t || b.token() > b.st_t) return false;
+  const int64_t diff = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  if (diff % 2) return false;
+  const int64_t off = ((diff / 2) % a.st_t + a.st_t) % a.st_t;  // where b's tokens begin within a's
+  return off >= a.token() && off + b.token() <= a.st_t;
 }
 
 // Checks that every call makes of the cache.
@@ -242,6 +275,154 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
     return BASTION_ERR_WORKSPACE;
   return bastion::launch_paged_evict(bastion::paged_args(*cache), seq_len, n_seen, acc, pos, budget, n_sink, n_recent,
                                      seq_len_out, acc_out, pos_out, workspace, status, (cudaStream_t)stream);
+}
+
+size_t bastion_paged_plan_workspace_bytes(int B) {
+  if (B < 1 || B > kMaxB) return 0;
+  return (size_t)kMaxB * sizeof(uint32_t);  // an arrival counter
+}
+
+int bastion_paged_plan(int32_t *page_table, int B, int max_pages, int page_size, int64_t n_pages,
+                       const int32_t *seq_len, const int32_t *n_new, int m, int32_t *seq_len_out,
+                       const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                       const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
+                       int32_t *pos, int64_t n_rows, int32_t *row_start, void *workspace,
+                       size_t workspace_bytes, int32_t *status, bastion_stream_t stream) {
+  if (!page_table || !seq_len || !held || !held_out || !free_pages || !n_free || !n_free_out || !slots || !pos ||
+      !workspace || !status)
+    return BASTION_ERR_NULL;
+  const int64_t cap = (int64_t)max_pages * page_size;
+  if (B < 1 || B > kMaxB || max_pages < 1 || page_size < 1 || cap > kMaxCap || n_pages < 1 || n_pages >= (1LL << 31) ||
+      m < 1 || m > cap || n_rows < 1 || n_rows >= (1LL << 31) || (!row_start && n_rows != (int64_t)B * m))
+    return BASTION_ERR_SIZE;
+  if (page_size < 8 || page_size > 128 || (page_size & (page_size - 1))) return BASTION_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || !aligned(slots, 8) || !aligned(pos, 4) || !aligned(page_table, 4)) return BASTION_ERR_ALIGN;
+  const size_t lens = (size_t)B * 4;
+  if ((seq_len_out && !same_or_apart(seq_len, seq_len_out, lens)) || !same_or_apart(held, held_out, lens) ||
+      !same_or_apart(n_free, n_free_out, 4))
+    return BASTION_ERR_UNSUPPORTED;
+  const Array table = {page_table, (size_t)B * max_pages * 4}, stack = {free_pages, (size_t)n_pages * 4},
+              len = {seq_len, lens}, len_out = {seq_len_out, lens}, add = {n_new, lens}, have = {held, lens},
+              have_out = {held_out, lens}, left = {n_free, 4}, left_out = {n_free_out, 4},
+              at = {slots, (size_t)n_rows * 8}, place = {pos, (size_t)n_rows * 4}, begin = {row_start, lens + 4},
+              flags = {status, lens};
+  // every output against every other array but its own pair's
+  if (!all_apart({table}, {stack, len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
+      !all_apart({stack}, {len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
+      !all_apart({at}, {len, len_out, add, have, have_out, left, left_out, place, begin, flags}) ||
+      !all_apart({place}, {len, len_out, add, have, have_out, left, left_out, begin, flags}) ||
+      !all_apart({begin}, {len, len_out, add, have, have_out, left, left_out, flags}) ||
+      !all_apart({flags}, {len, len_out, add, have, have_out, left, left_out}) ||
+      !all_apart({len_out}, {add, have, have_out, left, left_out}) ||
+      !all_apart({have_out}, {len, add, left, left_out}) || !all_apart({left_out}, {len, add, have}))
+    return BASTION_ERR_UNSUPPORTED;
+  if (workspace_bytes < bastion_paged_plan_workspace_bytes(B)) return BASTION_ERR_WORKSPACE;
+  return bastion::launch_paged_plan(page_table, B, max_pages, page_size, n_pages, seq_len, n_new, m, seq_len_out, held,
+                                    held_out, free_pages, n_free, n_free_out, trim, slots, pos, n_rows, row_start,
+                                    workspace, status, (cudaStream_t)stream);
+}
+
+int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t,
+                         int64_t q_st_h, const void *k, int64_t k_st_t, int64_t k_st_h,
+                         const void *v, int64_t v_st_t, int64_t v_st_h, const void *q_weight,
+                         const void *k_weight, float eps, const int32_t *pos,
+                         const double *inv_freq, int rot_dim, int interleaved, float factor,
+                         void *q_out, int64_t q_out_st_t, int64_t q_out_st_h, void *k_out,
+                         int64_t k_out_st_t, int64_t k_out_st_h, const bastion_paged_cache *cache,
+                         const int64_t *slots, int32_t *status, bastion_stream_t stream) {
+  if (!q || !k || !pos || !status || (rot_dim > 0 && !inv_freq) || (q_weight == nullptr) != (k_weight == nullptr) ||
+      (cache == nullptr) != (slots == nullptr) || (cache == nullptr) != (v == nullptr) || (!q_out && !k_out && !cache))
+    return BASTION_ERR_NULL;
+  if (dtype != BASTION_BF16 && dtype != BASTION_F16) return BASTION_ERR_DTYPE;
+  if (T < 1 || Hq < 1 || Hkv < 1 || D < 1 || (int64_t)Hq + 2 * (int64_t)Hkv > 65535 ||
+      (int64_t)T * ((int64_t)Hq + 2 * (int64_t)Hkv) >= (1LL << 31))
+    return BASTION_ERR_SIZE;
+  if (D != 64 && D != 128) return BASTION_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || !(eps >= 0.f) || !(eps < 1e30f) || !(factor > -1e30f) ||
+      !(factor < 1e30f))
+    return BASTION_ERR_SIZE;
+  if (cache) {
+    const int rc = check_cache(cache);
+    if (rc != BASTION_OK) return rc;
+    if (cache->dtype != dtype) return BASTION_ERR_DTYPE;
+    if (cache->D != D || cache->Hkv != Hkv) return BASTION_ERR_SIZE;
+  }
+  // the stride of a dimension of length 1 is never used
+  auto rows = [&](const void *p, int64_t st_t, int64_t H, int64_t st_h) {
+    return Rows{p, T, T > 1 ? st_t : 0, H, H > 1 ? st_h : D, D};
+  };
+  const Rows rq = rows(q, q_st_t, Hq, q_st_h), rk = rows(k, k_st_t, Hkv, k_st_h), rv = rows(v, v_st_t, Hkv, v_st_h),
+             oq = rows(q_out, q_out_st_t, Hq, q_out_st_h), ok = rows(k_out, k_out_st_t, Hkv, k_out_st_h);
+  for (const Rows *x : {&rq, &rk, &rv})
+    if (x->p && (!stride_ok(T, x->st_t, 0) || !stride_ok(x->H, x->st_h, D))) return BASTION_ERR_SIZE;
+  for (const Rows *x : {&oq, &ok})
+    if (x->p && (!stride_ok(x->H, x->st_h, D) || !stride_ok(T, x->st_t, x->token()))) return BASTION_ERR_SIZE;
+  for (const void *p : {q, k, v, (const void *)q_out, (const void *)k_out, q_weight, k_weight})
+    if (!aligned(p, 16)) return BASTION_ERR_ALIGN;
+  if (!aligned(inv_freq, 8) || !aligned(slots, 8)) return BASTION_ERR_ALIGN;
+  auto in_place = [](const Rows &x, const Rows &y) { return x.p == y.p && x.st_t == y.st_t && x.st_h == y.st_h; };
+  if (!(in_place(oq, rq) || rows_apart(oq, rq)) || !(in_place(ok, rk) || rows_apart(ok, rk)) || !rows_apart(oq, rk) ||
+      !rows_apart(oq, rv) || !rows_apart(ok, rq) || !rows_apart(ok, rv) || !rows_apart(oq, ok))
+    return BASTION_ERR_UNSUPPORTED;
+  const size_t tokens = (size_t)T;
+  auto span = [](const Rows &x) { return x.p ? x.span() : Array{nullptr, 0}; };
+  const Array qw = {q_weight, (size_t)D * 2}, kw = {k_weight, (size_t)D * 2}, places = {pos, tokens * 4},
+              freq = {rot_dim ? inv_freq : nullptr, (size_t)rot_dim * 4}, at = {slots, tokens * 8}, flags = {status, 4};
+  if (!all_apart({span(oq), span(ok)}, {qw, kw, places, freq, at, flags}) ||
+      !all_apart({flags}, {span(rq), span(rk), span(rv), qw, kw, places, freq, at}))
+    return BASTION_ERR_UNSUPPORTED;
+  return bastion::launch_qk_norm_rope(dtype == BASTION_F16, T, Hq, Hkv, D, q, rq.st_t, rq.st_h, k, rk.st_t, rk.st_h, v,
+                                      rv.st_t, rv.st_h, q_weight, k_weight, eps, pos, inv_freq, rot_dim,
+                                      interleaved != 0, factor, q_out, oq.st_t, oq.st_h, k_out, ok.st_t, ok.st_h,
+                                      cache ? bastion::paged_args(*cache) : bastion::Paged{}, slots, status,
+                                      (cudaStream_t)stream);
+}
+
+size_t bastion_paged_prefix_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups) {
+  if (!sizes_ok(B, Hkv, 1) || Hq < 1 || Hq % Hkv || Hq / Hkv > 16 || (D != 64 && D != 128) || n_groups < 1 ||
+      n_groups > kMaxB)
+    return 0;
+  return bastion::paged_prefix_workspace_bytes(B, Hq, Hkv, D, n_groups);
+}
+
+int bastion_paged_prefix_attention(const bastion_paged_cache *cache, const int32_t *prefix_table,
+                                   int max_prefix_pages, const int32_t *prefix_len,
+                                   const int32_t *group_start, int n_groups, const void *q, int Hq,
+                                   int64_t q_stride_b, const int32_t *seq_len, float scale,
+                                   void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   int32_t *status, bastion_stream_t stream) {
+  if (!q || !seq_len || !out || !workspace || !status || !prefix_table || !prefix_len || !group_start)
+    return BASTION_ERR_NULL;
+  const int rc = check_cache(cache);
+  if (rc != BASTION_OK) return rc;
+  if (Hq < 1 || Hq % cache->Hkv || !(scale > 0.f) || !(scale < 1e30f)) return BASTION_ERR_SIZE;
+  const int G = Hq / cache->Hkv;
+  if (G > 16) return BASTION_ERR_UNSUPPORTED;
+  const int64_t cap = (int64_t)max_prefix_pages * cache->page_size;
+  if (n_groups < 1 || n_groups > kMaxB || max_prefix_pages < 1 || cap > kMaxCap || !tiles_ok(cache) ||
+      (int64_t)n_groups * cache->Hkv * ((cap + 127) / 128) * (1 + (int64_t)cache->B * G / 128) >= (1LL << 31))
+    return BASTION_ERR_SIZE;
+  if (!stride_ok(cache->B, q_stride_b, (int64_t)Hq * cache->D)) return BASTION_ERR_SIZE;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(prefix_table, 4))
+    return BASTION_ERR_ALIGN;
+  const int64_t row = (int64_t)Hq * cache->D, q_st = cache->B > 1 ? q_stride_b : row;
+  const size_t lens = (size_t)cache->B * 4;
+  const Array table = table_of(cache), len = {seq_len, lens}, flags = {status, lens},
+              result = {out, (size_t)(2 * cache->B * row)}, logs = {lse, lens * Hq},
+              pre = {prefix_table, (size_t)n_groups * max_prefix_pages * 4}, pre_len = {prefix_len, (size_t)n_groups * 4},
+              start = {group_start, (size_t)(n_groups + 1) * 4};
+  if (!(out == q && q_st == row) && !apart_from_rows(result, q, 2 * row, 2 * q_st, cache->B)) return BASTION_ERR_UNSUPPORTED;
+  if (!all_apart({result, logs, flags}, {table, len, pre, pre_len, start}) || !all_apart({logs, flags}, {result}) ||
+      !all_apart({logs}, {flags}))
+    return BASTION_ERR_UNSUPPORTED;
+  for (const Array &x : {logs, flags})
+    if (!apart_from_rows(x, q, 2 * row, 2 * q_st, cache->B)) return BASTION_ERR_UNSUPPORTED;
+  if (workspace_bytes < bastion_paged_prefix_attention_workspace_bytes(cache->B, Hq, cache->Hkv, cache->D, n_groups))
+    return BASTION_ERR_WORKSPACE;
+  return bastion::launch_paged_prefix(bastion::paged_args(*cache), cache->dtype == BASTION_F16, prefix_table,
+                                      max_prefix_pages, prefix_len, group_start, n_groups, q, Hq,
+                                      cache->B > 1 ? q_stride_b : 0, seq_len, scale, out, lse, workspace, status,
+                                      (cudaStream_t)stream);
 }
 
 }  // extern "C"

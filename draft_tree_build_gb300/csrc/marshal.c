@@ -24,10 +24,17 @@
 typedef __typeof__(&bastion_paged_append) append_fn;
 typedef __typeof__(&bastion_paged_attention) attention_fn;
 typedef __typeof__(&bastion_paged_evict) evict_fn;
+typedef __typeof__(&bastion_paged_plan) plan_fn;
+typedef __typeof__(&bastion_qk_norm_rope) rope_fn;
+typedef __typeof__(&bastion_paged_prefix_attention) prefix_fn;
 
 static append_fn f_append;
 static attention_fn f_attention;
 static evict_fn f_evict;
+static plan_fn f_plan;
+static rope_fn f_rope;
+static prefix_fn f_prefix;
+static PyObject *dt_i64, *dt_f64;
 static PyObject *dt_bf16, *dt_f16, *dt_f32, *dt_i32, *dt_u8, *fn_device, *fn_stream;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_cuda_stream;
 
@@ -272,6 +279,178 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
+/* Whether dev is a CUDA device, and the current one. */
+static int is_current(long dev) {
+  if (dev < 0) return 0;
+  PyObject *x = PyObject_CallNoArgs(fn_device);
+  if (!x) return 0;
+  const long current = PyLong_AsLong(x);
+  Py_DECREF(x);
+  return current == dev;
+}
+
+/* page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos, workspace, status, n_new,
+ * row_start, seq_len_out, trim, stream */
+static PyObject *plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  tensor table, stack, slots;
+  void *at, *len, *held, *held_out, *pages, *left, *left_out, *slot, *pos, *ws, *st, *n_new, *start, *len_out;
+  int page, m;
+  size_t bytes;
+  bastion_stream_t stream;
+  if (n != 18 || !f_plan || !look(a[0], &table) || table.dim != 2 || !is_current(table.dev)) return declined();
+  const long dev = table.dev;
+  if (!contiguous(a[0], dev, dt_i32, 2, table.shape, &at) || table.shape[0] > INT32_MAX - 1 || table.shape[1] > INT32_MAX ||
+      !int32_of(a[1], &page) || !int32_of(a[3], &m) || !look(a[6], &stack) || stack.dim != 1 || !look(a[9], &slots) ||
+      slots.dim < 1)
+    return declined();
+  int64_t rows = 1;
+  for (int i = 0; i < slots.dim; ++i) {
+    if (slots.shape[i] > INT32_MAX || rows > INT32_MAX) return declined();
+    rows *= slots.shape[i];
+  }
+  const int64_t B[1] = {table.shape[0]}, more[1] = {table.shape[0] + 1}, one[1] = {1};
+  const int trim = PyObject_IsTrue(a[16]);
+  if (trim < 0 || !contiguous(a[2], dev, dt_i32, 1, B, &len) || !contiguous(a[4], dev, dt_i32, 1, B, &held) ||
+      !contiguous(a[5], dev, dt_i32, 1, B, &held_out) || !contiguous(a[6], dev, dt_i32, 1, stack.shape, &pages) ||
+      !contiguous(a[7], dev, dt_i32, 1, one, &left) || !contiguous(a[8], dev, dt_i32, 1, one, &left_out) ||
+      !contiguous(a[9], dev, dt_i64, slots.dim, slots.shape, &slot) ||
+      !contiguous(a[10], dev, dt_i32, slots.dim, slots.shape, &pos) || !workspace_of(a[11], dev, &ws, &bytes) ||
+      !contiguous(a[12], dev, dt_i32, 1, B, &st) || !contiguous_or_none(a[13], dev, dt_i32, 1, B, &n_new) ||
+      !contiguous_or_none(a[14], dev, dt_i32, 1, more, &start) || !contiguous_or_none(a[15], dev, dt_i32, 1, B, &len_out) ||
+      !stream_on(a[17], dev, &stream))
+    return declined();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_plan(at, (int)table.shape[0], (int)table.shape[1], page, stack.shape[0], len, n_new, m, len_out, held, held_out,
+              pages, left, left_out, trim, slot, pos, rows, start, ws, bytes, st, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* A token-by-token array [T, H, D] of the type on the device, or None: a null address. */
+static int heads_of(PyObject *o, long dev, PyObject *dtype, int64_t T, int64_t H, int64_t D, tensor *t) {
+  t->ptr = NULL;
+  t->stride[0] = t->stride[1] = 0;
+  if (o == Py_None) return 1;
+  return look_strided(o, t) && t->dim == 3 && t->dtype == dtype && t->dev == dev && t->shape[0] == T && t->shape[1] == H &&
+         t->shape[2] == D && t->stride[2] == 1;
+}
+
+/* q, k, pos, inv_freq, q_out, status, k_out, q_weight, k_weight, eps, interleaved, factor, v, k_pool, v_pool, slots,
+ * stream */
+static PyObject *rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  bastion_paged_cache c;
+  tensor q, k, v, q_out, k_out, freq, tk, tv;
+  void *pos, *at = NULL, *st, *qw, *kw, *slots;
+  bastion_stream_t stream;
+  if (n != 17 || !f_rope || !look_strided(a[0], &q) || !look(a[1], &k) || q.dim != 3 || k.dim != 3 || q.stride[2] != 1 ||
+      !is_current(q.dev) || (q.dtype != dt_bf16 && q.dtype != dt_f16))
+    return declined();
+  const long dev = q.dev;
+  const int64_t T = q.shape[0], Hq = q.shape[1], D = q.shape[2], Hkv = k.shape[1];
+  if (T > INT32_MAX || Hq > INT32_MAX || D > INT32_MAX || Hkv > INT32_MAX || !heads_of(a[1], dev, q.dtype, T, Hkv, D, &k) ||
+      !heads_of(a[12], dev, q.dtype, T, Hkv, D, &v) || !heads_of(a[4], dev, q.dtype, T, Hq, D, &q_out) ||
+      !heads_of(a[6], dev, q.dtype, T, Hkv, D, &k_out))
+    return declined();
+  const double eps = PyFloat_AsDouble(a[9]), factor = PyFloat_AsDouble(a[11]);
+  const int inter = PyObject_IsTrue(a[10]);
+  if (PyErr_Occurred() || inter < 0) return declined();
+  int rot = 0;
+  if (a[3] != Py_None) {
+    if (!look(a[3], &freq) || freq.dim != 1 || freq.shape[0] > 65536 || !contiguous(a[3], dev, dt_f64, 1, freq.shape, &at))
+      return declined();
+    rot = 2 * (int)freq.shape[0];
+  }
+  const int64_t tokens[1] = {T}, one[1] = {1}, width[1] = {D};
+  if (!contiguous(a[2], dev, dt_i32, 1, tokens, &pos) || !contiguous(a[5], dev, dt_i32, 1, one, &st) ||
+      !contiguous_or_none(a[7], dev, q.dtype, 1, width, &qw) || !contiguous_or_none(a[8], dev, q.dtype, 1, width, &kw) ||
+      !contiguous_or_none(a[15], dev, dt_i64, 1, tokens, &slots))
+    return declined();
+  const int store = a[13] != Py_None;
+  if (store != (a[14] != Py_None)) return declined();
+  if (store) {
+    if (!look_strided(a[13], &tk) || !look_strided(a[14], &tv) || tk.dim != 4 || tv.dim != 4 || tk.dtype != q.dtype ||
+        tv.dtype != q.dtype || tk.dev != dev || tv.dev != dev || tk.stride[3] != 1)
+      return declined();
+    for (int i = 0; i < 4; ++i)
+      if (tk.shape[i] != tv.shape[i] || (tk.shape[i] != 1 && tk.stride[i] != tv.stride[i]) || (i > 0 && tk.shape[i] > INT32_MAX))
+        return declined();
+    c.k_pool = tk.ptr;
+    c.v_pool = tv.ptr;
+    c.n_pages = tk.shape[0];
+    c.stride_page = tk.stride[0];
+    c.stride_slot = tk.stride[1];
+    c.stride_head = tk.stride[2];
+    c.page_table = st; /* not read: any address of the right alignment serves */
+    c.dtype = tk.dtype == dt_bf16 ? BASTION_BF16 : BASTION_F16;
+    c.B = 1;
+    c.Hkv = (int32_t)tk.shape[2];
+    c.D = (int32_t)tk.shape[3];
+    c.page_size = (int32_t)tk.shape[1];
+    c.max_pages = 1;
+  }
+  if (!stream_on(a[16], dev, &stream)) return declined();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_rope(q.dtype == dt_bf16 ? BASTION_BF16 : BASTION_F16, (int)T, (int)Hq, (int)Hkv, (int)D, q.ptr, q.stride[0],
+              q.stride[1], k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1], qw, kw, (float)eps, pos, at, rot,
+              inter, (float)factor, q_out.ptr, q_out.stride[0], q_out.stride[1], k_out.ptr, k_out.stride[0], k_out.stride[1],
+              store ? &c : NULL, slots, st, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* q, k_pool, v_pool, page_table, seq_len, prefix_table, prefix_len, group_start, scale, out, workspace, status, lse,
+ * stream */
+static PyObject *prefix(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  bastion_paged_cache c;
+  tensor q, table;
+  PyObject *dtype;
+  long dev;
+  void *len, *at, *pre_len, *start, *out, *ws, *st, *lse;
+  size_t bytes;
+  bastion_stream_t stream;
+  if (n != 14 || !f_prefix || !cache_of(a[1], a[2], a[3], &c, &dev, &dtype)) return declined();
+  if (!look_strided(a[0], &q) || q.dim != 3 || q.dtype != dtype || q.dev != dev || q.shape[0] != c.B ||
+      q.shape[2] != c.D || q.shape[1] > INT32_MAX || q.stride[2] != 1 || (q.shape[1] > 1 && q.stride[1] != c.D))
+    return declined();
+  const double scale = PyFloat_AsDouble(a[8]);
+  if (scale == -1.0 && PyErr_Occurred()) return declined();
+  if (!look(a[5], &table) || table.dim != 2 || table.shape[0] > INT32_MAX - 1 || table.shape[1] > INT32_MAX) return declined();
+  const int64_t B[1] = {c.B}, heads[2] = {c.B, q.shape[1]}, groups[1] = {table.shape[0]}, more[1] = {table.shape[0] + 1};
+  if (!contiguous(a[4], dev, dt_i32, 1, B, &len) || !contiguous(a[5], dev, dt_i32, 2, table.shape, &at) ||
+      !contiguous(a[6], dev, dt_i32, 1, groups, &pre_len) || !contiguous(a[7], dev, dt_i32, 1, more, &start) ||
+      !contiguous(a[9], dev, dtype, 3, q.shape, &out) || !workspace_of(a[10], dev, &ws, &bytes) ||
+      !contiguous(a[11], dev, dt_i32, 1, B, &st) || !contiguous_or_none(a[12], dev, dt_f32, 2, heads, &lse) ||
+      !stream_on(a[13], dev, &stream))
+    return declined();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = f_prefix(&c, at, (int)table.shape[1], pre_len, start, (int)table.shape[0], q.ptr, (int)q.shape[1], q.stride[0], len,
+                (float)scale, out, lse, ws, bytes, st, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* int64, float64, and the addresses of the page plan, the norm and rotation and the shared-prefix attention */
+static PyObject *init_layer(PyObject *self, PyObject *args) {
+  (void)self;
+  PyObject *i64, *f64;
+  unsigned long long f[3];
+  if (!PyArg_ParseTuple(args, "OOKKK", &i64, &f64, &f[0], &f[1], &f[2])) return NULL;
+  Py_INCREF(i64);
+  Py_XSETREF(dt_i64, i64);
+  Py_INCREF(f64);
+  Py_XSETREF(dt_f64, f64);
+  f_plan = (plan_fn)(uintptr_t)f[0];
+  f_rope = (rope_fn)(uintptr_t)f[1];
+  f_prefix = (prefix_fn)(uintptr_t)f[2];
+  Py_RETURN_NONE;
+}
+
 /* bfloat16, float16, float32, int32, uint8, current device, raw stream of a device, and the addresses of the
  * library's three functions */
 static PyObject *init(PyObject *self, PyObject *args) {
@@ -295,6 +474,10 @@ static PyMethodDef methods[] = {{"init", init, METH_VARARGS, NULL},
                                 {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
                                 {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, NULL},
                                 {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
+                                {"init_layer", init_layer, METH_VARARGS, NULL},
+                                {"plan", (PyCFunction)(void (*)(void))plan, METH_FASTCALL, NULL},
+                                {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, NULL},
+                                {"prefix", (PyCFunction)(void (*)(void))prefix, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "bastion_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};

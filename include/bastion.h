@@ -68,6 +68,8 @@ enum {
   BASTION_STATUS_BAD_WEIGHT = 32,  /* a mixture weight pi is negative or not finite */
   BASTION_STATUS_BAD_PAGE = 64,    /* a page table entry outside [0, n_pages) is in use */
   BASTION_STATUS_BAD_ROW = 128,    /* an appended row index outside [0, n_rows) */
+  BASTION_STATUS_NO_PAGE = 256,    /* too few free pages for the request's new tokens */
+  BASTION_STATUS_BAD_GROUP = 512,  /* a group of requests outside [0, B], or one that ends before it begins */
   BASTION_STATUS_TIMEOUT = 1 << 30 /* a bounded device wait ran out */
 };
 

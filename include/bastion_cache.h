@@ -179,6 +179,136 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
                         int32_t *pos_out, void *workspace, size_t workspace_bytes,
                         int32_t *status, bastion_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Page plan: the pages and slots of each request's next tokens, found on the
+ * GPU from the requests' lengths.
+ *
+ * Request r, with n = seq_len[r] used slots and held[r] pages, gets
+ * c = min(m, max(n_new[r], 0)) new slots (m where n_new is NULL), and pages for
+ * them where ceil((n + c) / page_size) exceeds held[r]; with trim != 0 it gives
+ * back the pages that it holds beyond that many (a request that has ended:
+ * seq_len = n_new = 0).  The free pages are a stack, free_pages[0 .. n_free[0]):
+ * first the pages given back are pushed, requests in order and each one's in the
+ * order of its table, then new pages are popped, requests in order.
+ *
+ * page_table    [B, max_pages] int32: entries [held[r], ceil((n + c) /
+ *               page_size)) are written, the others left as they are.
+ * seq_len, n_new, seq_len_out  [B] int32; n_new may be NULL (m for each) and
+ *               seq_len_out NULL or seq_len: n + c.
+ * held, held_out  [B] int32: pages held before and after; may be one array.
+ * free_pages    [n_pages] int32, n_free, n_free_out [1] int32 (may be one).
+ *               Entries at or past n_free are written where more pages come
+ *               back than go, the others left as they are.
+ * slots, pos    [n_rows] int64 and int32: slot (page * page_size + slot in the
+ *               page) and position n + i of every new token, -1 in rows that have
+ *               none.  row_start NULL: request r's are rows r * m + i, and
+ *               n_rows = B * m (BASTION_ERR_SIZE otherwise).  row_start [B+1]
+ *               int32: they are packed, request r's are rows row_start[r] + i.
+ * A request that cannot be served gets no rows and no pages, gives none back and
+ * keeps its length: seq_len outside [0, max_pages * page_size] or n + c beyond
+ * it, or packed rows that would end past n_rows (BASTION_STATUS_KV_OVERFLOW);
+ * held outside [0, max_pages], or held pages too few for n slots
+ * (BASTION_STATUS_BAD_PAGE); too few free pages (BASTION_STATUS_NO_PAGE: first
+ * come, first served; after the first such request none that needs a page gets
+ * one).  Packed rows are first come, first served too.
+ * A page number outside [0, n_pages) sets BASTION_STATUS_BAD_PAGE; its rows'
+ * slots are -1.  n_free is taken as lying in [0, n_pages]; where it does not
+ * status[0] gets BASTION_STATUS_BAD_PAGE.
+ * Limits: as the cache's; 1 <= m <= max_pages * page_size, 1 <= n_rows < 2^31.
+ * Apart from the pairs above no output overlaps another array
+ * (BASTION_ERR_UNSUPPORTED).
+ * Workspace: bastion_paged_plan_workspace_bytes(B) bytes.  One launch.
+ */
+size_t bastion_paged_plan_workspace_bytes(int B);
+int bastion_paged_plan(int32_t *page_table, int B, int max_pages, int page_size, int64_t n_pages,
+                       const int32_t *seq_len, const int32_t *n_new, int m, int32_t *seq_len_out,
+                       const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                       const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
+                       int32_t *pos, int64_t n_rows, int32_t *row_start, void *workspace,
+                       size_t workspace_bytes, int32_t *status, bastion_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norm and rotation of T tokens' queries and keys, in one pass that may also
+ * store keys and values into the cache.
+ *
+ * Each head x of q and k is normed, where weights are given,
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * and its first rot_dim elements turned by the token's position: the pair
+ * (a, b), number i, becomes factor * (a cos t - b sin t, b cos t + a sin t)
+ * with t = pos * inv_freq[i].  Pair i is elements (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) with interleaved != 0.  Sums and products are formed in 32 bits
+ * and rounded once; t is reduced to a fraction of a turn in 64-bit fixed point,
+ * exactly, so that far positions are as good as near ones.
+ *
+ * q, k, v       [T, Hq, D], [T, Hkv, D], [T, Hkv, D] at *_st_t elements a token
+ *               and *_st_h a head (multiples of 8, st_h >= D), 16-byte aligned:
+ *               slices of one projection's output fit.  v with a cache only.
+ * q_weight, k_weight  [D], of the same dtype, 16-byte aligned; both or neither
+ *               NULL (no norm).  eps >= 0, finite.
+ * pos           [T] int32.  A token whose position is negative is left out: none
+ *               of its outputs is written.
+ * inv_freq      [rot_dim / 2] double (8-byte aligned), finite; scaled for a long
+ *               context by the caller.  rot_dim a multiple of 16 in [0, D]; 0:
+ *               nothing is turned, inv_freq may be NULL.
+ * q_out, k_out  as q and k, or NULL: not written.  q_out may be q, k_out k, with
+ *               the same strides; otherwise they lie apart from every input (not
+ *               checked row by row: BASTION_ERR_UNSUPPORTED where the spans of
+ *               two arrays overlap that are not slices of the same tokens' rows).
+ * cache, slots  NULL, or the cache and [T] int64: the token's key and value go to
+ *               slot slots[t] (as bastion_paged_plan gives it); a negative slot
+ *               stores nothing, one past the pools sets BASTION_STATUS_BAD_PAGE.
+ *               A slot listed twice holds one of the two rows' values in each of
+ *               its 16-byte pieces.  The cache's B, page_table and max_pages are
+ *               checked and not used; its pools lie apart from the inputs.
+ * status        [1] int32.
+ * Limits: D = 64 or 128 (BASTION_ERR_UNSUPPORTED); T, Hq, Hkv >= 1, Hq + 2 Hkv
+ * <= 65535, T * (Hq + 2 Hkv) < 2^31; factor finite.  One launch.
+ */
+int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t,
+                         int64_t q_st_h, const void *k, int64_t k_st_t, int64_t k_st_h,
+                         const void *v, int64_t v_st_t, int64_t v_st_h, const void *q_weight,
+                         const void *k_weight, float eps, const int32_t *pos,
+                         const double *inv_freq, int rot_dim, int interleaved, float factor,
+                         void *q_out, int64_t q_out_st_t, int64_t q_out_st_h, void *k_out,
+                         int64_t k_out_st_t, int64_t k_out_st_h, const bastion_paged_cache *cache,
+                         const int64_t *slots, int32_t *status, bastion_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token per request, over a prefix that its group of
+ * requests shares and then its own used slots: bastion_paged_attention over
+ * both, with the prefix's keys and values read once for the whole group.
+ *
+ * prefix_table  [n_groups, max_prefix_pages] int32: the pages of each group's
+ *               prefix, in the cache's pools.
+ * prefix_len    [n_groups] int32: the prefix's slots.
+ * group_start   [n_groups+1] int32, ascending: group g is the requests
+ *               group_start[g] .. group_start[g+1] - 1.  A request of no group
+ *               attends to its own slots alone.  A group outside [0, B], or that
+ *               ends before it begins, is left out and sets
+ *               BASTION_STATUS_BAD_GROUP (in the status of its first request, taken
+ *               to the nearest of the batch); what a group shares with the groups
+ *               before it, up to the largest end among them, is not its own.
+ * cache, q, seq_len, scale, out, lse, status: as bastion_paged_attention; the
+ *               cache's page_table and seq_len are of the request's own slots, and
+ *               q_stride_b is at least Hq * D.
+ *               A group's prefix_len outside [0, max_prefix_pages * page_size] or
+ *               page outside the pool sets its first request's status bit.
+ * Limits: as bastion_paged_attention; 1 <= n_groups <= 1024, max_prefix_pages *
+ * page_size <= 2^28, n_groups * Hkv * ceil(max_prefix_pages * page_size / 128) *
+ * (1 + B * Hq / Hkv / 128) < 2^31.
+ * Weights enter the products as there: as two 16-bit terms.  Results do not
+ * depend on the order in which the parts of a split prefix finish.
+ * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
+ * n_groups) bytes.
+ */
+size_t bastion_paged_prefix_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups);
+int bastion_paged_prefix_attention(const bastion_paged_cache *cache, const int32_t *prefix_table,
+                                   int max_prefix_pages, const int32_t *prefix_len,
+                                   const int32_t *group_start, int n_groups, const void *q, int Hq,
+                                   int64_t q_stride_b, const int32_t *seq_len, float scale,
+                                   void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                   int32_t *status, bastion_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
