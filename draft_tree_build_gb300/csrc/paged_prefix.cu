@@ -1,104 +1,832 @@
 // Attention of one new token per request over its group's shared prefix and its
-// own slots.  A warp a query head: lane = D / 32 elements of the head, one key
-// after the other with a running maximum and sum.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+// own slots.
+//
+//   out = (sum_prefix exp(s_j) v_j + sum_own exp(s_j) v_j) / (sum_prefix exp(s_j) + sum_own exp(s_j))
+//
+// Three launches: the own slots, by the one-token kernel of paged_attention.cu,
+// in 32 bits; the prefixes; and the join of each row's parts.
+//
+// The prefixes.  A group's n requests are n * G query rows of a KV head, which
+// read each key and value once per 256 rows: 512 flops a byte at 256 rows of
+// D = 128, about where HBM and the tensor cores take equally long, so that
+// neither may wait for the other:
+//  * one persistent CTA per SM.  A unit is (group, KV head, up to 256 rows); the
+//    batch is a list of 128-key tiles, unit by unit, of which every CTA takes an
+//    equal contiguous share (paged_walk.cuh);
+//  * warp 0 streams keys and warp 2 values through one ring in shared memory,
+//    warp 3 the queries of the next M tile of 128 rows, with TMA;
+//  * warp 1 issues the products, S = Q K^T from shared memory and O += P V with P
+//    in tensor memory: P takes the place of its scores.  Visits (a key tile and
+//    an M tile) alternate between two softmax warpgroups, which own 128 columns
+//    of S and up to 128 of O each, so that one's softmax runs under the other's
+//    products.  A unit of two M tiles gives each warpgroup one; a unit of one
+//    gives them alternate key tiles, as two parts;
+//  * a thread is a row.  The reference maximum moves, and O is rescaled, only
+//    where a score exceeds it by 2^8;
+//  * P enters the product as a high and a low 16-bit term, as in
+//    paged_attention.cu, twice the instructions for weights to 2^-17.
+// Rows of a unit are whole requests (floor(128 / G) of them an M tile), so that a
+// box of the query tensor is an M tile, whatever G is.
+//
+// A part is the unnormalised row in 32 bits with its reference and sum.  Units
+// that one CTA finishes go to a row of their own, others to a slot of the CTA;
+// the join's warps work out from the shares where a row's parts are.
+//
+// Every wait is bounded (~1 s); after one ran out the CTA flags the requests of
+// its remaining tiles, waits for its own copies and products (bounded), frees its
+// TMEM and returns.
 #include "paged.cuh"
+#include "paged_tc.cuh"
+#include "paged_walk.cuh"
 
 namespace bastion {
 
+size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t cap, int weights);
+int launch_paged_attention32(const Paged &c, bool half, const void *q, int Hq, int64_t q_st_b, const int32_t *seq_len,
+                             float scale, float *out32, float *lse2, void *ws, int32_t *status, cudaStream_t stream);
+
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kPer = (kMaxRequests + kThreads - 1) / kThreads;  // groups of a thread in the prologue, at most
+constexpr int kBatch = 4;      // tiles whose table entries are read together
+constexpr float kGrow = 8.0f;  // a score may exceed its row's reference by 2^8
 
 struct PrefixArgs {
   const int32_t *table, *len, *start;  // the groups' prefixes
   int n_groups, max_pages, cap;
-  const uint16_t *q;
-  int64_t q_st_b;
-  int Hq, G;
-  const int32_t *seq_len;
-  float scale;
+  int Hq, G, nb;  // nb = 128 / G requests an M tile
+  float scale_log2;
+  int swap;
+  int4 *rec;       // [B]: first tile of the request's group, tiles, requests of the group, its place among them
+  int *total;      // tiles of the batch
+  float *own;      // [B, Hq, D], normalised
+  float *own_lse;  // [B, Hq], base 2
+  float *rows;     // [2][B, Hq, D]: units of one CTA
+  float2 *rows_ml;
+  float *parts;    // [2 kMaxParts][2][128][D]: units of several
+  float2 *parts_ml;
+  int n_ctas;
   uint16_t *out;
   float *lse;
   int32_t *status;
 };
 
-template <bool kHalf>
-__device__ __forceinline__ float to32(uint16_t x) {
-  return kHalf ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x));
-}
-template <bool kHalf>
-__device__ __forceinline__ uint16_t to16(float x) {
-  return kHalf ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+// --------------------------------------------------------------------------- shared memory
+
+// The value tiles' operand has D = N rows of MN-major blocks, all inside the stage.
+template <int D>
+struct Layout {
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kBlocks = D / 64;
+  static constexpr uint32_t kBlock = kTileKeys * 128;  // a 64-element column block of 128 rows
+  static constexpr uint32_t kTile = kBlocks * kBlock;
+  static constexpr uint32_t kOffQ = kStages * kTile;   // two M tiles
+  static constexpr uint32_t kOffList = kOffQ + 2 * kTile;
+  static constexpr uint32_t kOffMisc = kOffList + kMaxRequests * 16;
+};
+
+struct Misc {
+  uint64_t full[8], empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], mma_done;
+  int2 warp_sum[kThreads / 32];
+  int warp_max[kThreads / 32];
+  int li0, off0, f0, f1, groups;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int D>
+constexpr uint32_t smem_bytes() {
+  constexpr uint32_t n = Layout<D>::kOffMisc + (uint32_t)sizeof(Misc) + 1024;  // + alignment slack
+  static_assert(n <= 227 * 1024, "shared memory of one CTA");
+  return n;
 }
 
-__device__ __forceinline__ bool group_ok(const PrefixArgs &a, int B, int g) {
-  const int x = a.start[g], y = a.start[g + 1];
-  return x >= 0 && x <= y && y <= B;
+// --------------------------------------------------------------------------- tensor memory
+
+// A in tensor memory (two 16-bit elements a column), B in shared memory.
+__device__ __forceinline__ void mma_ta(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
+                                       uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(accum), "r"(one));
+}
+
+__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// --------------------------------------------------------------------------- a CTA's tiles
+
+// Tile t of the unit (group, KV head, pair of M tiles).  list: the groups that
+// have tiles: first request (and the group's number in the upper half), requests,
+// slots of the prefix, first tile.
+template <bool kUniform>
+struct Units {
+  const int4 *list;
+  int li, group, req, n, len, tiles, m_tiles, head, pair, t, left;
+  bool first;  // the first tile of its segment
+  static __device__ __forceinline__ int uniform(int x) {
+    return kUniform ? __shfl_sync(kFull, x, 0) : x;
+  }
+  __device__ __forceinline__ void load(int nb) {
+    const int4 e = list[li];
+    group = uniform(e.x >> 16);
+    req = uniform(e.x & 0xffff);
+    n = uniform(e.y);
+    len = uniform(e.z);
+    tiles = (len + kTileKeys - 1) / kTileKeys;
+    m_tiles = (n + nb - 1) / nb;
+  }
+  __device__ __forceinline__ void start(const int4 *l, int index, int off, int count, int nb) {
+    list = l;
+    li = index;
+    left = count;
+    first = true;
+    if (left > 0) {
+      load(nb);
+      const int u = off / tiles, pairs = (m_tiles + 1) / 2;
+      t = off - u * tiles;
+      head = u / pairs;
+      pair = u - head * pairs;
+    }
+  }
+  __device__ __forceinline__ int ms() const { return min(2, m_tiles - 2 * pair); }  // M tiles of the unit
+  __device__ __forceinline__ void step(int heads, int nb) {
+    first = false;
+    --left;
+    if (++t == tiles) {
+      t = 0;
+      first = true;
+      if (++pair * 2 >= m_tiles) {
+        pair = 0;
+        if (++head == heads) {
+          head = 0;
+          ++li;
+          if (left > 0) load(nb);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == 1; }
+};
+
+template <bool kHalf, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, Paged c, PrefixArgs a) {
+  using Lay = Layout<D>;
+  constexpr int kStages = Lay::kStages, kBlocks = Lay::kBlocks;
+  constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Misc &ms = *reinterpret_cast<Misc *>(smem + Lay::kOffMisc);
+  int4 *list = reinterpret_cast<int4 *>(smem + Lay::kOffList);
+  volatile int *abort = &ms.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ms.full[s], 1);
+      mbar_init(&ms.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms.q_full[s], 1);
+      mbar_init(&ms.q_empty[s], 1);
+      mbar_init(&ms.s_full[s], 1);
+      mbar_init(&ms.p_full[s], 4);
+      mbar_init(&ms.pv_done[s], 1);
+    }
+    mbar_init(&ms.mma_done, 1);
+    ms.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ms.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ------------------------------------------------------------ this CTA's share
+  // A thread has consecutive groups.  A group begins where the ones before it end, at the earliest.
+  const int chunk = (a.n_groups + kThreads - 1) / kThreads, g0 = tid * chunk;
+  int from[kPer], n_req[kPer], len[kPer], idx[kPer];
+  int ends = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int g = g0 + i;
+    from[i] = n_req[i] = len[i] = 0;
+    idx[i] = g;
+    if (i >= chunk || g >= a.n_groups) continue;
+    const int x = a.start[g], y = a.start[g + 1];
+    if (x >= 0 && x <= y && y <= c.B) {
+      from[i] = x;
+      n_req[i] = y;  // for now, the end
+      len[i] = a.len[g];
+      ends = max(ends, y);
+    } else if (blockIdx.x == 0) {
+      atomicOr(&a.status[min(max(x, 0), c.B - 1)], BASTION_STATUS_BAD_GROUP);
+    }
+  }
+  int before = ends;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, before, o);
+    if (lane >= o) before = max(before, x);
+  }
+  if (lane == 31) ms.warp_max[warp] = before;
+  before = __shfl_up_sync(kFull, before, 1);
+  if (lane == 0) before = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+  for (int x = 0; x < warp; ++x) before = max(before, ms.warp_max[x]);
+  int cnt = 0, til = 0, unit_tiles[kPer], group_tiles[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int end = n_req[i];
+    from[i] = max(from[i], before);
+    n_req[i] = max(0, end - from[i]);
+    before = max(before, end);
+    if (n_req[i] > 0 && (len[i] < 0 || len[i] > a.cap) && blockIdx.x == 0)
+      atomicOr(&a.status[from[i]], BASTION_STATUS_KV_OVERFLOW);
+    len[i] = min(max(len[i], 0), a.cap);
+    unit_tiles[i] = n_req[i] > 0 ? (len[i] + kTileKeys - 1) / kTileKeys : 0;
+    group_tiles[i] = unit_tiles[i] * (((n_req[i] + a.nb - 1) / a.nb + 1) / 2) * c.Hkv;
+    cnt += group_tiles[i] > 0;
+    til += group_tiles[i];
+  }
+  int cnt_i = cnt, til_i = til;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kFull, cnt_i, o), y = __shfl_up_sync(kFull, til_i, o);
+    if (lane >= o) {
+      cnt_i += x;
+      til_i += y;
+    }
+  }
+  if (lane == 31) ms.warp_sum[warp] = make_int2(cnt_i, til_i);
+  __syncthreads();
+  int rank = cnt_i - cnt, at = til_i - til, total = 0, groups = 0;
+#pragma unroll
+  for (int x = 0; x < kThreads / 32; ++x) {
+    const int2 y = ms.warp_sum[x];
+    if (x < warp) {
+      rank += y.x;
+      at += y.y;
+    }
+    groups += y.x;
+    total += y.y;
+  }
+  Shares sh;
+  sh.n = min((int)gridDim.x, total);
+  sh.quot = sh.n > 0 ? total / sh.n : 0;
+  sh.big = total - sh.quot * sh.n;
+  const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
+  const bool busy = (int)blockIdx.x < sh.n;
+  if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (group_tiles[i] == 0) continue;
+    const int t = unit_tiles[i], end = at + group_tiles[i];
+    list[rank] = make_int4(from[i] | idx[i] << 16, n_req[i], len[i], at);
+    if (busy) {
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {  // the share's begin and end
+        const int f = k ? b1 : b0;
+        if (f < at || f >= end) continue;
+        const int off = (f - at) % t, to = Shares::moved(f, off, t);
+        if (k) {
+          ms.f1 = to;
+        } else {
+          ms.f0 = to;
+          ms.li0 = to == end ? rank + 1 : rank;  // the next group's begin
+          ms.off0 = to == end ? 0 : to - at;
+        }
+      }
+    }
+    ++rank;
+    at = end;
+  }
+  __syncthreads();
+  const int share = __shfl_sync(kFull, busy ? ms.f1 - ms.f0 : 0, 0), li0 = __shfl_sync(kFull, ms.li0, 0),
+            off0 = __shfl_sync(kFull, ms.off0, 0);
+  Units<true> w;
+  w.start(list, li0, off0, share, a.nb);
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA: warp 0 keys, warp 2 values
+    // tile x of the share has its keys in stage 2 x and its values in stage 2 x + 1 of the ring
+    const int odd = warp >> 1;
+    const CUtensorMap *map = odd ? &tm_v : &tm_k;
+    const uint32_t one = elect_one();
+    // Table entries are read in batches of kBatch tiles, a batch ahead of their use, so that the
+    // reads' latency never holds up the copies.  Lane: page lane % ppt of the batch's tile lane / ppt.
+    const int psh = 7 - c.shift, ppt = 1 << psh, batch = min(kBatch, 32 >> psh);
+    Units<false> lw;  // this lane's tile
+    lw.start(list, li0, off0, share, a.nb);
+    int lead = lane >> psh;
+    auto next_entry = [&]() {  // walks on by `lead` tiles and reads there
+#pragma unroll 1
+      for (int x = 0; x < lead && lw.left > 0; ++x) lw.step(c.Hkv, a.nb);
+      lead = batch;
+      const int pg = (lw.t << psh) + (lane & (ppt - 1));
+      const bool on = (lane >> psh) < batch && lw.left > 0 && (pg << c.shift) < lw.len;
+      int e = on ? a.table[(size_t)lw.group * a.max_pages + pg] : 0;
+      if (e < 0 || e >= c.n_pages) {  // no page of the pool: page 0 stands in
+        atomicOr(&a.status[lw.req], BASTION_STATUS_BAD_PAGE);
+        e = 0;
+      }
+      __syncwarp();
+      return e;
+    };
+    int entry = 0, entry_n = next_entry(), in_batch = batch;
+    // a prefix that one unit a head reads: not at the parts' expense; several units: the others find it in L2
+    const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+    const uint32_t ring32 = smem_u32(smem), full32 = smem_u32(ms.full);
+    int issued = 0;
+#pragma unroll 1
+    for (; w.left > 0; w.step(c.Hkv, a.nb)) {
+      if (in_batch == batch) {
+        entry = entry_n;
+        entry_n = next_entry();
+        in_batch = 0;
+      }
+      const int x = 2 * issued + odd, slot = x % kStages;
+      if (!__all_sync(kFull, wait_bar(&ms.empty[slot], ((uint32_t)(x / kStages) & 1u) ^ 1u, abort, &a.status[w.req]))) break;
+      const int np = (min(kTileKeys, w.len - w.t * kTileKeys) + c.page - 1) >> c.shift;
+      if (one) mbar_arrive_expect_tx(&ms.full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
+      uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
+      const int c1 = a.swap ? w.head : 0, c2 = a.swap ? 0 : w.head;
+#pragma unroll 4
+      for (int p = 0; p < np; ++p) {
+        const int id = __shfl_sync(kFull, entry, (in_batch << psh) + p);
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+          tma_load_4d(one, dst + (uint32_t)blk * Lay::kBlock, map, blk * 64, c1, c2, id, full32 + 8u * (uint32_t)slot,
+                      w.m_tiles > 2 ? again : once);
+        dst += (uint32_t)(128 << c.shift);
+      }
+      ++issued;
+      ++in_batch;
+    }
+    // our last copies have landed (bounded) before the CTA may exit
+    if (lane == 0) {
+      for (int u = max(0, issued - kStages / 2); u < issued; ++u)
+        mbar_wait_bounded(&ms.full[(2 * u + odd) % kStages], (uint32_t)((2 * u + odd) / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    // Visit i (a key tile and an M tile) belongs to warpgroup i % 2.  S of visit i + 2 goes out right
+    // after P V of visit i, whose P it overwrites: products of one thread execute in order.
+    constexpr uint32_t id_s = idesc<kHalf>(false, false, kTileKeys), id_o = idesc<kHalf>(false, true, D);
+    const uint32_t one = elect_one();
+    const uint64_t d_ring = desc(smem_u32(smem), 16, 1024, 2), d_q = desc(smem_u32(smem + Lay::kOffQ), 16, 1024, 2);
+    const uint64_t d_v = desc(smem_u32(smem), Lay::kBlock, 1024, 2);
+    Units<true> pw = w;
+    int i_s = 0, m_s = 0, x_s = 0, q_s = 0;        // of the next S: visit, M tile, key tile, M tiles of segments before
+    int i_p = 0, m_p = 0, x_p = 0, seg_p = 0;      // of the next P V: ..., key tile of its segment
+    auto scores = [&]() {
+      const int wg = i_s & 1, x = 2 * x_s, slot = x % kStages, q = q_s + m_s, count = w.ms();
+      int32_t *st = &a.status[w.req];
+      if (!__all_sync(kFull, (!w.first || wait_bar(&ms.q_full[q & 1], (uint32_t)(q >> 1) & 1u, abort, st)) &&
+                                 wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st)))
+        return false;
+      tc_fence_after();
+      const uint64_t dk = d_ring + (uint32_t)slot * (Lay::kTile >> 4), dq = d_q + (uint32_t)(q & 1) * (Lay::kTile >> 4);
+#pragma unroll
+      for (int y = 0; y < D / 16; ++y) {
+        const uint32_t off = (uint32_t)(y >> 2) * (Lay::kBlock >> 4) + (uint32_t)(y & 3) * 2u;
+        mma(one, tmem + 128u * (uint32_t)wg, dq + off, dk + off, id_s, y > 0);
+      }
+      mma_commit(one, &ms.s_full[wg]);
+      if (w.last()) mma_commit(one, &ms.q_empty[q & 1]);
+      ++i_s;
+      if (++m_s == count) {
+        mma_commit(one, &ms.empty[slot]);
+        m_s = 0;
+        ++x_s;
+        if (w.last()) q_s += count;
+        w.step(c.Hkv, a.nb);
+      }
+      return true;
+    };
+    auto values = [&]() {
+      const int wg = i_p & 1, x = 2 * x_p + 1, slot = x % kStages, count = pw.ms();
+      int32_t *st = &a.status[pw.req];
+      if (!__all_sync(kFull, wait_bar(&ms.p_full[wg], (uint32_t)(i_p >> 1) & 1u, abort, st) &&
+                                 wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st)))
+        return false;
+      tc_fence_after();
+      const bool fresh = seg_p < 3 - count;  // the segment's first visit of this warpgroup: key tile 0, or 0 and 1
+      const uint64_t dv = d_v + (uint32_t)slot * (Lay::kTile >> 4);
+      const uint32_t p_col = tmem + 128u * (uint32_t)wg, o_col = tmem + 256u + 128u * (uint32_t)wg;
+#pragma unroll
+      for (int y = 0; y < kTileKeys / 16; ++y) {  // 16 keys: 8 columns of high terms, 16 further on those of low terms
+        const uint32_t p = p_col + 32u * (uint32_t)(y >> 1) + 8u * (uint32_t)(y & 1);
+        mma_ta(one, o_col, p, dv + 128u * (uint32_t)y, id_o, y > 0 ? 1u : fresh ? 0u : 1u);
+        mma_ta(one, o_col, p + 16u, dv + 128u * (uint32_t)y, id_o, 1u);
+      }
+      mma_commit(one, &ms.pv_done[wg]);
+      ++i_p;
+      if (++m_p == count) {
+        mma_commit(one, &ms.empty[slot]);
+        m_p = 0;
+        ++x_p;
+        ++seg_p;
+        if (pw.last()) seg_p = 0;
+        pw.step(c.Hkv, a.nb);
+      }
+      return true;
+    };
+    bool ok = true;
+    for (int y = 0; y < 2; ++y) ok = ok && (w.left == 0 || scores());
+    while (ok && pw.left > 0) ok = values() && (w.left == 0 || scores());
+    // every product issued has completed (bounded) before the CTA may free its TMEM
+    mma_commit(one, &ms.mma_done);
+    mbar_wait_bounded(&ms.mma_done, 0);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ queries of each segment
+    const uint32_t one = elect_one();
+    const uint64_t policy = l2_evict_first_policy();
+    const uint32_t q32 = smem_u32(smem + Lay::kOffQ), full32 = smem_u32(ms.q_full);
+    int q = 0;
+    for (; w.left > 0; w.step(c.Hkv, a.nb)) {
+      if (!w.first) continue;
+      bool ok = true;
+      for (int m = 0; ok && m < w.ms(); ++m, ++q) {
+        const int slot = q & 1;
+        ok = __all_sync(kFull, wait_bar(&ms.q_empty[slot], ((uint32_t)(q >> 1) & 1u) ^ 1u, abort, &a.status[w.req]));
+        if (!ok) break;
+        if (one) mbar_arrive_expect_tx(&ms.q_full[slot], (uint32_t)(a.nb * a.G) * (uint32_t)(D * 2));
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+          tma_load_4d(one, q32 + (uint32_t)slot * Lay::kTile + (uint32_t)blk * Lay::kBlock, &tm_q, blk * 64, 0, w.head,
+                      w.req + (2 * w.pair + m) * a.nb, full32 + 8u * (uint32_t)slot, policy);
+      }
+      if (!ok) break;
+    }
+    // where the join finds each request's parts
+    if (blockIdx.x == 0 && lane == 0) *a.total = total;
+    for (int b = blockIdx.x * 32 + lane; b < c.B; b += gridDim.x * 32) {
+      int lo = 0, hi = groups;
+      while (hi - lo > 1) {  // the last group that begins at b or before
+        const int mid = (lo + hi) >> 1;
+        if ((list[mid].x & 0xffff) <= b) lo = mid; else hi = mid;
+      }
+      int4 e = make_int4(0, 0, 0, 0);
+      if (groups > 0) {
+        const int4 l = list[lo];
+        const int place = b - (l.x & 0xffff);
+        if (place >= 0 && place < l.y) e = make_int4(l.w, (l.z + kTileKeys - 1) / kTileKeys, l.y, place);
+      }
+      a.rec[b] = e;
+    }
+    if (lane == 0)
+      for (int u = max(0, q - 2); u < q; ++u) mbar_wait_bounded(&ms.q_full[u & 1], (uint32_t)(u >> 1) & 1u);
+  } else {
+    // ------------------------------------------------------------ softmax and parts: a thread is a row
+    const int wg = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t s_col = tmem + ((uint32_t)(quad * 32) << 16) + 128u * (uint32_t)wg, o_col = s_col + 256u;
+    int visits = 0, x_t = 0;  // this warpgroup's visits; the share's key tiles
+    int par = 0, par0 = 0, t0 = 0, rows = 0, m = 0;
+    bool any = false, ok = true;
+    float ref = -INFINITY, l = 0.f;
+    for (; w.left > 0; w.step(c.Hkv, a.nb), ++x_t) {
+      const int count = w.ms();
+      int32_t *st = &a.status[w.req];
+      if (w.first) {
+        par0 = par;
+        t0 = w.t;
+        m = count == 2 ? wg ^ par : 0;
+        rows = min(a.nb, w.n - (2 * w.pair + m) * a.nb) * a.G;
+        any = false;
+        ref = -INFINITY;
+        l = 0.f;
+      }
+      if (count == 2 || par == wg) {
+        const int valid = w.len - w.t * kTileKeys;  // keys of the tile, where it is the last
+        ok = __all_sync(kFull, wait_bar(&ms.s_full[wg], (uint32_t)visits & 1u, abort, st));
+        if (!ok) break;
+        tc_fence_after();
+        if (quad * 32 < rows) {
+          float v[32], top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ld32(s_col + 32u * (uint32_t)k, v);
+            if (valid < 32 * (k + 1)) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) v[y] = 32 * k + y < valid ? v[y] : -INFINITY;
+            }
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) top = max3f(top, v[y], v[y + 1]);
+          }
+          top *= a.scale_log2;
+          const bool grow = top > ref + (kBias + kGrow);
+          const float to = grow ? top - kBias : ref, alpha = grow ? ex2f(ref - to) : 1.0f;
+          if (any && __any_sync(kFull, grow)) {  // S is there: the products before it, all of this O, are done
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+              float o[32];
+              uint32_t z[32];
+              ld32(o_col + 32u * (uint32_t)k, o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) z[y] = __float_as_uint(o[y] * alpha);
+              st32(o_col + 32u * (uint32_t)k, z);
+            }
+          }
+          ref = to;
+          l *= alpha;
+          const float base = ref == -INFINITY ? 0.f : -ref;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ld32(s_col + 32u * (uint32_t)k, v);
+            if (valid < 32 * (k + 1)) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) v[y] = 32 * k + y < valid ? v[y] : -INFINITY;
+            }
+            uint32_t z[32];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              const float p0 = ex2f(fmaf(v[y], a.scale_log2, base)), p1 = ex2f(fmaf(v[y + 1], a.scale_log2, base));
+              sum0 += p0;
+              sum1 += p1;
+              split2<kHalf>(p0, p1, z[y / 2], z[16 + y / 2]);
+            }
+            st32(s_col + 32u * (uint32_t)k, z);
+          }
+          l += sum0 + sum1;
+          wait_st();
+        }
+        if (valid < kTileKeys && (count == 1 || m == 0)) {  // the rows past the end: zeros, whatever the page holds there
+          const int x = 2 * x_t + 1, slot = x % kStages;
+          ok = __all_sync(kFull, wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st));
+          if (!ok) break;
+          unsigned char *tile = smem + slot * Lay::kTile;
+#pragma unroll 1
+          for (int y = valid * 128 + row * 16; y < kTileKeys * 128; y += 128 * 16)
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk)
+              *reinterpret_cast<uint4 *>(tile + blk * Lay::kBlock + y) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full[wg]);
+        any = true;
+        ++visits;
+      }
+      if (count == 1) par ^= 1;
+      if (!w.last()) continue;
+
+      // ---------------------------------------------------------- the segment's end
+      const bool whole = t0 == 0 && w.t == w.tiles - 1;
+      const int plane = count == 2 ? m : wg ^ par0;
+      if (any) {
+        ok = __all_sync(kFull, wait_bar(&ms.pv_done[wg], (uint32_t)(visits - 1) & 1u, abort, st));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (quad * 32 < rows) {
+        float *dst;
+        float2 *ml;
+        if (whole) {
+          const int b = w.req + (2 * w.pair + m) * a.nb + row / a.G;
+          const size_t at_row = ((size_t)(count == 2 ? 0 : plane) * c.B + b) * a.Hq + w.head * a.G + row % a.G;
+          dst = a.rows + at_row * D;
+          ml = a.rows_ml + at_row;
+        } else {
+          const size_t at_row = ((size_t)(2 * blockIdx.x + (t0 == 0)) * 2 + plane) * 128 + row;
+          dst = a.parts + at_row * D;
+          ml = a.parts_ml + at_row;
+        }
+        if (any) {
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            float o[32];
+            ld32(o_col + 32u * (uint32_t)k, o);
+            if (row < rows) {
+#pragma unroll
+              for (int y = 0; y < 32; y += 4)
+                *reinterpret_cast<float4 *>(dst + 32 * k + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            }
+          }
+        }
+        if (row < rows) *ml = make_float2(ref, l);
+        tc_fence_before();  // the next segment's products overwrite O after this warp's next arrival
+      }
+    }
+    if (!ok) {  // a wait ran out, of which only one request has been told
+      for (; w.left > 0; w.step(c.Hkv, a.nb))
+        for (int b = w.req + row; b < w.req + w.n; b += 128) atomicOr(&a.status[b], BASTION_STATUS_TIMEOUT);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// --------------------------------------------------------------------------- the join
+
+// A row's parts: its own slots', then those of its prefix in the order of their
+// keys.  kWarps warps a row take every kWarps-th part; lane = D / 32 elements.
+template <bool kHalf, int D, int kWarps>
+__global__ void __launch_bounds__(256) paged_prefix_join(Paged c, PrefixArgs a) {
+  constexpr int E = D / 32, kRows = 8 / kWarps;
+  __shared__ float s_ref[8], s_sum[8], s_o[8][D];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part0 = warp % kWarps;
+  const int row = blockIdx.x * kRows + warp / kWarps, n_rows = c.B * a.Hq;
+  float o[E] = {}, ref = -INFINITY, l = 0.f;
+  if (row < n_rows) {
+    const int b = row / a.Hq, h = row - b * a.Hq, head = h / a.G;
+    const int4 e = a.rec[b];
+    int np = 0, planes = 0, c0 = 0, plane0 = 0, in_tile = 0;
+    bool whole = false;
+    if (e.y > 0) {
+      const int m_tiles = (e.z + a.nb - 1) / a.nb, pairs = (m_tiles + 1) / 2, m = e.w / a.nb, pair = m >> 1;
+      const bool two = m_tiles - 2 * pair >= 2;
+      const int u0 = e.x + (head * pairs + pair) * e.y, u1 = u0 + e.y, total = *a.total;
+      Shares sh;
+      sh.n = min(a.n_ctas, total);
+      sh.quot = total / sh.n;
+      sh.big = total - sh.quot * sh.n;
+      c0 = sh.first_cta(u0);
+      const int ctas = sh.last_cta(u1) - c0 + 1;
+      whole = e.y <= kWhole || ctas <= 1;
+      planes = two ? 1 : 2;
+      plane0 = two ? m & 1 : 0;
+      np = (whole ? 1 : ctas) * planes;
+      in_tile = (e.w - m * a.nb) * a.G + (h - head * a.G);
+    }
+    for (int p = part0; p <= np; p += kWarps) {
+      const float *src;
+      float2 ml;
+      if (p == 0) {
+        src = a.own + (size_t)row * D;
+        ml = make_float2(a.own_lse[row], 1.f);
+      } else if (whole) {
+        const size_t at = (size_t)(p - 1) * n_rows + row;
+        src = a.rows + at * D;
+        ml = a.rows_ml[at];
+      } else {
+        const int x = (p - 1) / planes, plane = plane0 + (p - 1) - x * planes;
+        const size_t at = ((size_t)(2 * (c0 + x) + (x == 0)) * 2 + plane) * 128 + in_tile;
+        src = a.parts + at * D;
+        ml = a.parts_ml[at];
+      }
+      float v[E];
+#pragma unroll
+      for (int y = 0; y < E; ++y) v[y] = __ldcg(src + lane * E + y);
+      const bool none = ml.x == -INFINITY && !(ml.y != ml.y);  // nothing was seen: what the row holds does not count
+      const float top = fmaxf(ref, ml.x), f0 = ref == -INFINITY ? 0.f : exp2f(ref - top), f1 = none ? 0.f : exp2f(ml.x == -INFINITY ? 0.f : ml.x - top);
+      l = l * f0 + (none ? 0.f : ml.y * f1);
+#pragma unroll
+      for (int y = 0; y < E; ++y) o[y] = o[y] * f0 + (none ? 0.f : v[y] * f1);
+      ref = top;
+    }
+  }
+  if (kWarps > 1) {
+    if (lane == 0) {
+      s_ref[warp] = ref;
+      s_sum[warp] = l;
+    }
+#pragma unroll
+    for (int y = 0; y < E; ++y) s_o[warp][lane * E + y] = o[y];
+    __syncthreads();
+    if (part0 > 0) return;
+    for (int x = 1; x < kWarps; ++x) {
+      const float r = s_ref[warp + x], s = s_sum[warp + x];
+      const float top = fmaxf(ref, r), f0 = ref == -INFINITY ? 0.f : exp2f(ref - top), f1 = r == -INFINITY ? 0.f : exp2f(r - top);
+      l = l * f0 + s * f1;
+#pragma unroll
+      for (int y = 0; y < E; ++y) o[y] = o[y] * f0 + s_o[warp + x][lane * E + y] * f1;
+      ref = top;
+    }
+  }
+  if (row >= n_rows) return;
+  uint16_t z[E];
+#pragma unroll
+  for (int y = 0; y < E; ++y) z[y] = to16<kHalf>(l == 0.f ? 0.f : __fdividef(o[y], l));
+  uint16_t *dst = a.out + (size_t)row * D + lane * E;
+  if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(z[0] | (uint32_t)z[1] << 16, z[E - 2] | (uint32_t)z[E - 1] << 16);
+  else *reinterpret_cast<uint32_t *>(dst) = z[0] | (uint32_t)z[1] << 16;
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Queries as (D, head of the group, KV head, request); a box is an M tile's rows, 64 elements wide.
+bool make_q_map(CUtensorMap *m, const void *q, const Paged &c, int Hq, int64_t q_st_b, int nb, bool half) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t G = (cuuint64_t)(Hq / c.Hkv), D = (cuuint64_t)c.D;
+  cuuint64_t dims[4] = {D, G, (cuuint64_t)c.Hkv, (cuuint64_t)c.B};
+  cuuint64_t strides[3] = {D * 2, G * D * 2, (cuuint64_t)(c.B > 1 ? q_st_b : (int64_t)Hq * c.D) * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)nb};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kHalf, int D>
-__global__ void __launch_bounds__(kThreads) paged_prefix_simple(Paged c, PrefixArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (blockIdx.x == 0)
-    for (int g = threadIdx.x; g < a.n_groups; g += kThreads) {
-      const int first = min(max(a.start[g], 0), c.B - 1);
-      if (!group_ok(a, c.B, g)) atomicOr(&a.status[first], BASTION_STATUS_BAD_GROUP);
-      else if (a.start[g] < a.start[g + 1] && (a.len[g] < 0 || a.len[g] > a.cap)) atomicOr(&a.status[first], BASTION_STATUS_KV_OVERFLOW);
-    }
-  if (row >= c.B * a.Hq) return;
-  const int r = row / a.Hq, h = row % a.Hq, head = h / a.G;
-  int g = -1;
-  for (int g0 = 0; g0 < a.n_groups && g < 0; g0 += 32) {
-    const int x = g0 + lane;
-    const bool on = x < a.n_groups && group_ok(a, c.B, x) && a.start[x] <= r && r < a.start[x + 1];
-    const unsigned m = __ballot_sync(kFull, on);
-    if (m) g = g0 + __ffs(m) - 1;
-  }
-  constexpr int E = D / 32;
-  float q[E], o[E] = {}, top = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = to32<kHalf>(a.q[r * a.q_st_b + (int64_t)h * D + lane + 32 * e]);
-  auto over = [&](const int32_t *table, int n, int told) {
-    int page = 0;
-    for (int j = 0; j < n; ++j) {
-      if ((j & (c.page - 1)) == 0) {
-        page = table[j >> c.shift];
-        if (page < 0 || page >= c.n_pages) {
-          if (lane == 0) atomicOr(&a.status[told], BASTION_STATUS_BAD_PAGE);
-          page = 0;
-        }
-      }
-      const int64_t at = paged_row(c, page, j, head) + lane;
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s += q[e] * to32<kHalf>(c.k[at + 32 * e]);
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFull, s, x);
-      s *= a.scale;
-      const float m = fmaxf(top, s);
-      if (m == -INFINITY && s == s) continue;
-      const float f = expf(top - m), p = expf(s - m);
-      l = l * f + p;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to32<kHalf>(c.v[at + 32 * e]);
-      top = m;
-    }
-  };
-  if (g >= 0) over(a.table + (int64_t)g * a.max_pages, min(max(a.len[g], 0), a.cap), a.start[g]);
-  over(c.table + (int64_t)r * c.max_pages, paged_len(c, a.seq_len, r, a.status), r);
-  for (int e = 0; e < E; ++e) a.out[(int64_t)row * D + lane + 32 * e] = to16<kHalf>(l == 0.f ? 0.f : o[e] / l);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : top + logf(l);
+cudaError_t launch_parts(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, int dev, const Paged &c,
+                         const PrefixArgs &a, cudaStream_t stream) {
+  constexpr uint32_t smem = smem_bytes<D>();
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(paged_prefix_kernel<kHalf, D>, (int)smem, dev, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_prefix_kernel<kHalf, D>, dim3((unsigned)a.n_ctas), dim3(kThreads), smem, stream, mq, mk, mv, c, a);
+}
+
+template <bool kHalf, int D>
+cudaError_t launch_join(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
+  const int rows = c.B * a.Hq;
+  // eight warps a row where rows are few and their parts, then, many
+  return rows <= 16 * sms ? launch_pdl(paged_prefix_join<kHalf, D, 8>, dim3((unsigned)rows), dim3(256), 0, stream, c, a)
+                          : launch_pdl(paged_prefix_join<kHalf, D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, c, a);
+}
+
+struct Sizes {
+  size_t own_ws, own, own_lse, rec, total, rows, rows_ml, parts, parts_ml;
+  size_t all() const { return own_ws + own + own_lse + rec + total + rows + rows_ml + parts + parts_ml; }
+};
+Sizes sizes_of(int B, int Hq, int Hkv, int D) {
+  const size_t rows = (size_t)B * Hq, parts = (size_t)2 * kMaxParts * 2 * 128;
+  Sizes s;
+  s.own_ws = up256(paged_attention_workspace_bytes(B, Hq, Hkv, D, 1, 0));
+  s.own = up256(rows * D * 4);
+  s.own_lse = up256(rows * 4);
+  s.rec = up256((size_t)B * 16);
+  s.total = 256;
+  s.rows = 2 * rows * D * 4;
+  s.rows_ml = up256(2 * rows * 8);
+  s.parts = parts * D * 4;
+  s.parts_ml = parts * 8;
+  return s;
 }
 
 }  // namespace
 
-size_t paged_prefix_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups) { return kCounterBytes; }
+size_t paged_prefix_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups) {
+  (void)n_groups;
+  return sizes_of(B, Hq, Hkv, D).all();
+}
 
 int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, int max_prefix_pages,
                         const int32_t *prefix_len, const int32_t *group_start, int n_groups, const void *q, int Hq,
                         int64_t q_st_b, const int32_t *seq_len, float scale, void *out, float *lse, void *ws,
                         int32_t *status, cudaStream_t stream) {
+  const Sizes sz = sizes_of(c.B, Hq, c.Hkv, c.D);
   PrefixArgs a;
   a.table = prefix_table;
   a.len = prefix_len;
@@ -106,21 +834,45 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
   a.n_groups = n_groups;
   a.max_pages = max_prefix_pages;
   a.cap = max_prefix_pages * c.page;
-  a.q = static_cast<const uint16_t *>(q);
-  a.q_st_b = q_st_b;
   a.Hq = Hq;
   a.G = Hq / c.Hkv;
-  a.seq_len = seq_len;
-  a.scale = scale;
+  a.nb = 128 / a.G;
+  a.scale_log2 = scale * kLog2e;
+  a.swap = c.Hkv > 1 && c.st_head < c.st_slot;
+  char *at = static_cast<char *>(ws) + sz.own_ws;
+  auto take = [&](size_t n) {
+    char *p = at;
+    at += n;
+    return p;
+  };
+  a.own = reinterpret_cast<float *>(take(sz.own));
+  a.own_lse = reinterpret_cast<float *>(take(sz.own_lse));
+  a.rec = reinterpret_cast<int4 *>(take(sz.rec));
+  a.total = reinterpret_cast<int *>(take(sz.total));
+  a.rows = reinterpret_cast<float *>(take(sz.rows));
+  a.rows_ml = reinterpret_cast<float2 *>(take(sz.rows_ml));
+  a.parts = reinterpret_cast<float *>(take(sz.parts));
+  a.parts_ml = reinterpret_cast<float2 *>(take(sz.parts_ml));
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = status;
-  const dim3 grid((unsigned)((c.B * Hq + 7) / 8));
-  const cudaError_t e =
-      half ? (c.D == 128 ? launch_pdl(paged_prefix_simple<true, 128>, grid, dim3(kThreads), 0, stream, c, a)
-                         : launch_pdl(paged_prefix_simple<true, 64>, grid, dim3(kThreads), 0, stream, c, a))
-           : (c.D == 128 ? launch_pdl(paged_prefix_simple<false, 128>, grid, dim3(kThreads), 0, stream, c, a)
-                         : launch_pdl(paged_prefix_simple<false, 64>, grid, dim3(kThreads), 0, stream, c, a));
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, q, c, Hq, q_st_b, a.nb, half) || !make_map(&mk, c.k, c, a.swap, half) ||
+      !make_map(&mv, c.v, c, a.swap, half))
+    return BASTION_ERR_LAUNCH;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return BASTION_ERR_LAUNCH;
+  a.n_ctas = sms < kMaxParts ? sms : kMaxParts;
+  const int rc = launch_paged_attention32(c, half, q, Hq, q_st_b, seq_len, scale, a.own, a.own_lse, ws, status, stream);
+  if (rc != BASTION_OK) return rc;
+  const bool wide = c.D == 128;
+  cudaError_t e = half ? (wide ? launch_parts<true, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<true, 64>(mq, mk, mv, dev, c, a, stream))
+                       : (wide ? launch_parts<false, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<false, 64>(mq, mk, mv, dev, c, a, stream));
+  if (e == cudaSuccess)
+    e = half ? (wide ? launch_join<true, 128>(sms, c, a, stream) : launch_join<true, 64>(sms, c, a, stream))
+             : (wide ? launch_join<false, 128>(sms, c, a, stream) : launch_join<false, 64>(sms, c, a, stream));
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? BASTION_OK : BASTION_ERR_LAUNCH;
 }
 
