@@ -88,7 +88,7 @@ struct Layout {
 
 struct Misc {
   uint64_t full[8], empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], mma_done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], mma_done;  // p_full: of a warpgroup's upper, lower keys
   int2 warp_sum[kThreads / 32];
   int warp_max[kThreads / 32];
   int li0, off0, f0, f1, groups;
@@ -114,8 +114,8 @@ __device__ __forceinline__ void mma_ta(uint32_t one, uint32_t d_tmem, uint32_t a
       "r"(a_tmem), "l"(b), "r"(id), "r"(accum), "r"(one));
 }
 
-__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of the thread's lane; the registers hold them once wait_ld has returned.
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -124,9 +124,15 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// N loaded registers, for the compiler: not to be read before this.
+template <int N>
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                 "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -139,6 +145,19 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Eight columns of O times alpha; the stores are complete after wait_st.
+__device__ __forceinline__ void move_o(uint32_t taddr, float alpha) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  wait_ld(r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
@@ -147,11 +166,80 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   return pol;
 }
 
+// Two products and sums at once: (x0, x1) * m + a.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float m, float a0, float a1) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %4};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(x0), "+f"(x1)
+      : "f"(m), "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+
+// The scores of a tile's keys past its end become -inf.
+__device__ __noinline__ void mask_scores(uint32_t s_col, int valid) {
+#pragma unroll 1
+  for (int k = valid / 32; k < kTileKeys / 32; ++k) {
+    uint32_t v[32];
+    ld32(s_col + 32u * (uint32_t)k, v);
+    wait_ld(v);
+#pragma unroll
+    for (int y = 0; y < 32; ++y) v[y] = 32 * k + y < valid ? v[y] : 0xff800000u;
+    st32(s_col + 32u * (uint32_t)k, v);
+  }
+  wait_st();
+}
+
+// Four running maxima over 32 scores more.
+__device__ __forceinline__ void top_of(float (&top)[4], const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int y = 0; y < 32; y += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = max3f(top[k], __uint_as_float(v[y + 2 * k]), __uint_as_float(v[y + 2 * k + 1]));
+}
+
+// split2 of paged_tc.cuh with both differences in one instruction.
+template <bool kHalf>
+__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+  float h0, h1;
+  if (kHalf) {
+    const __half2 h = __floats2half2_rn(p0, p1);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    h0 = f.x;
+    h1 = f.y;
+  } else {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
+    h0 = bf16lo(hi);
+    h1 = bf16hi(hi);
+  }
+  fma2(h0, h1, -1.f, p0, p1);  // p - h, exactly
+  if (kHalf) {
+    const __half2 x = __floats2half2_rn(h0, h1);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+  } else {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(h1), "f"(h0));
+  }
+}
+
+// --------------------------------------------------------------------------- parts
+
+// A part is an M tile's rows: element d of row i of R at (place * D + d * R + i),
+// its reference and sum at place + i.
+__device__ __forceinline__ size_t whole_part(int plane, int head, int req, const Paged &c, int G) {
+  return (((size_t)plane * c.Hkv + head) * c.B + req) * G;
+}
+__device__ __forceinline__ size_t cut_part(int slot, int plane) { return ((size_t)slot * 2 + plane) * 128; }
 
 // --------------------------------------------------------------------------- a CTA's tiles
 
@@ -235,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.q_full[s], 1);
       mbar_init(&ms.q_empty[s], 1);
       mbar_init(&ms.s_full[s], 1);
-      mbar_init(&ms.p_full[s], 4);
+      mbar_init(&ms.p_full[s][0], 4);
+      mbar_init(&ms.p_full[s][1], 4);
       mbar_init(&ms.pv_done[s], 1);
     }
     mbar_init(&ms.mma_done, 1);
@@ -246,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  griddep_wait();
+  // No wait for the launch before: it attends to the own slots, of which nothing is read here, and let this one begin
+  // after everything before it was complete.  This launch ends after it (below), and the join waits for this one.
   griddep_launch_dependents();
 
   // ------------------------------------------------------------ this CTA's share
@@ -260,11 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     from[i] = n_req[i] = len[i] = 0;
     idx[i] = g;
     if (i >= chunk || g >= a.n_groups) continue;
-    const int x = a.start[g], y = a.start[g + 1];
+    const int x = a.start[g], y = a.start[g + 1], n = a.len[g];
     if (x >= 0 && x <= y && y <= c.B) {
       from[i] = x;
       n_req[i] = y;  // for now, the end
-      len[i] = a.len[g];
+      len[i] = n;
       ends = max(ends, y);
     } else if (blockIdx.x == 0) {
       atomicOr(&a.status[min(max(x, 0), c.B - 1)], BASTION_STATUS_BAD_GROUP);
@@ -457,18 +547,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto values = [&]() {
       const int wg = i_p & 1, x = 2 * x_p + 1, slot = x % kStages, count = pw.ms();
       int32_t *st = &a.status[pw.req];
-      if (!__all_sync(kFull, wait_bar(&ms.p_full[wg], (uint32_t)(i_p >> 1) & 1u, abort, st) &&
-                                 wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st)))
-        return false;
-      tc_fence_after();
       const bool fresh = seg_p < 3 - count;  // the segment's first visit of this warpgroup: key tile 0, or 0 and 1
       const uint64_t dv = d_v + (uint32_t)slot * (Lay::kTile >> 4);
       const uint32_t p_col = tmem + 128u * (uint32_t)wg, o_col = tmem + 256u + 128u * (uint32_t)wg;
 #pragma unroll
-      for (int y = 0; y < kTileKeys / 16; ++y) {  // 16 keys: 8 columns of high terms, 16 further on those of low terms
-        const uint32_t p = p_col + 32u * (uint32_t)(y >> 1) + 8u * (uint32_t)(y & 1);
-        mma_ta(one, o_col, p, dv + 128u * (uint32_t)y, id_o, y > 0 ? 1u : fresh ? 0u : 1u);
-        mma_ta(one, o_col, p + 16u, dv + 128u * (uint32_t)y, id_o, 1u);
+      for (int part = 0; part < 2; ++part) {  // the upper 64 keys, whose weights are formed first, then the lower
+        if (!__all_sync(kFull, wait_bar(&ms.p_full[wg][part], (uint32_t)(i_p >> 1) & 1u, abort, st) &&
+                                   (part > 0 || wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st))))
+          return false;
+        tc_fence_after();
+#pragma unroll
+        for (int z = 0; z < kTileKeys / 32; ++z) {  // 16 keys: 8 columns of high terms, 16 further on those of low terms
+          const int y = z + (part == 0 ? kTileKeys / 32 : 0);
+          const uint32_t p = p_col + 32u * (uint32_t)(y >> 1) + 8u * (uint32_t)(y & 1);
+          mma_ta(one, o_col, p, dv + 128u * (uint32_t)y, id_o, part + z > 0 ? 1u : fresh ? 0u : 1u);
+          mma_ta(one, o_col, p + 16u, dv + 128u * (uint32_t)y, id_o, 1u);
+        }
       }
       mma_commit(one, &ms.pv_done[wg]);
       ++i_p;
@@ -552,57 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFull, wait_bar(&ms.s_full[wg], (uint32_t)visits & 1u, abort, st));
         if (!ok) break;
         tc_fence_after();
-        if (quad * 32 < rows) {
-          float v[32], top = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ld32(s_col + 32u * (uint32_t)k, v);
-            if (valid < 32 * (k + 1)) {
-#pragma unroll
-              for (int y = 0; y < 32; ++y) v[y] = 32 * k + y < valid ? v[y] : -INFINITY;
-            }
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) top = max3f(top, v[y], v[y + 1]);
-          }
-          top *= a.scale_log2;
-          const bool grow = top > ref + (kBias + kGrow);
-          const float to = grow ? top - kBias : ref, alpha = grow ? ex2f(ref - to) : 1.0f;
-          if (any && __any_sync(kFull, grow)) {  // S is there: the products before it, all of this O, are done
-#pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
-              float o[32];
-              uint32_t z[32];
-              ld32(o_col + 32u * (uint32_t)k, o);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) z[y] = __float_as_uint(o[y] * alpha);
-              st32(o_col + 32u * (uint32_t)k, z);
-            }
-          }
-          ref = to;
-          l *= alpha;
-          const float base = ref == -INFINITY ? 0.f : -ref;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ld32(s_col + 32u * (uint32_t)k, v);
-            if (valid < 32 * (k + 1)) {
-#pragma unroll
-              for (int y = 0; y < 32; ++y) v[y] = 32 * k + y < valid ? v[y] : -INFINITY;
-            }
-            uint32_t z[32];
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              const float p0 = ex2f(fmaf(v[y], a.scale_log2, base)), p1 = ex2f(fmaf(v[y + 1], a.scale_log2, base));
-              sum0 += p0;
-              sum1 += p1;
-              split2<kHalf>(p0, p1, z[y / 2], z[16 + y / 2]);
-            }
-            st32(s_col + 32u * (uint32_t)k, z);
-          }
-          l += sum0 + sum1;
-          wait_st();
-        }
-        if (valid < kTileKeys && (count == 1 || m == 0)) {  // the rows past the end: zeros, whatever the page holds there
+        if (valid < kTileKeys && (count == 1 || m == 0)) {  // value rows past the end: zeros, whatever the page holds there
           const int x = 2 * x_t + 1, slot = x % kStages;
           ok = __all_sync(kFull, wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st));
           if (!ok) break;
@@ -614,9 +658,69 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4 *>(tile + blk * Lay::kBlock + y) = make_uint4(0, 0, 0, 0);
           fence_async_smem();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_full[wg]);
+        const auto hand_over = [&](int part) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.p_full[wg][part]);
+        };
+        if (quad * 32 < rows) {
+          // 32 keys at a time, the next ones' load under the work on the last; the upper half of the scores
+          // stays in registers from the maximum to the weights
+          uint32_t va[32], vb[32], vc[32], vd[32];
+          if (valid < kTileKeys) mask_scores(s_col, valid);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          ld32(s_col, va);
+          wait_ld(va);
+          ld32(s_col + 32u, vb);
+          top_of(tops, va);
+          wait_ld(vb);
+          ld32(s_col + 64u, vc);
+          top_of(tops, vb);
+          wait_ld(vc);
+          ld32(s_col + 96u, vd);
+          top_of(tops, vc);
+          wait_ld(vd);
+          top_of(tops, vd);
+          const float top = fmaxf(max3f(tops[0], tops[1], tops[2]), tops[3]) * a.scale_log2;
+          const bool grow = top > ref + (kBias + kGrow);
+          const float to = grow ? top - kBias : ref, alpha = grow ? ex2f(ref - to) : 1.0f;
+          if (any && __any_sync(kFull, grow)) {  // S is there: the products before it, all of this O, are done
+#pragma unroll 1
+            for (int k = 0; k < D / 8; ++k) move_o(o_col + 8u * (uint32_t)k, alpha);
+          }
+          ref = to;
+          l *= alpha;
+          const float base = ref == -INFINITY ? 0.f : -ref;
+          float sum0 = 0.f, sum1 = 0.f;
+          const auto weights = [&](const uint32_t (&v)[32], int k) {
+            uint32_t z[32];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              float p0 = __uint_as_float(v[y]), p1 = __uint_as_float(v[y + 1]);
+              fma2(p0, p1, a.scale_log2, base, base);
+              p0 = ex2f(p0);
+              p1 = ex2f(p1);
+              add2(sum0, sum1, p0, p1);
+              split_pair<kHalf>(p0, p1, z[y / 2], z[16 + y / 2]);
+            }
+            st32(s_col + 32u * (uint32_t)k, z);
+          };
+          weights(vc, 2);
+          weights(vd, 3);
+          ld32(s_col, va);
+          wait_st();
+          hand_over(0);
+          wait_ld(va);
+          ld32(s_col + 32u, vb);
+          weights(va, 0);
+          wait_ld(vb);
+          weights(vb, 1);
+          l += sum0 + sum1;
+          wait_st();
+        } else {
+          hand_over(0);
+        }
+        hand_over(1);
         any = true;
         ++visits;
       }
@@ -632,27 +736,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (quad * 32 < rows) {
-        float *dst;
-        float2 *ml;
-        if (whole) {
-          const int b = w.req + (2 * w.pair + m) * a.nb + row / a.G;
-          const size_t at_row = ((size_t)(count == 2 ? 0 : plane) * c.B + b) * a.Hq + w.head * a.G + row % a.G;
-          dst = a.rows + at_row * D;
-          ml = a.rows_ml + at_row;
-        } else {
-          const size_t at_row = ((size_t)(2 * blockIdx.x + (t0 == 0)) * 2 + plane) * 128 + row;
-          dst = a.parts + at_row * D;
-          ml = a.parts_ml + at_row;
-        }
+        // column by column, so that a warp's rows lie side by side
+        const size_t place = whole ? whole_part(count == 2 ? 0 : plane, w.head, w.req + (2 * w.pair + m) * a.nb, c, a.G)
+                                   : cut_part(2 * blockIdx.x + (t0 == 0), plane);
+        float *dst = (whole ? a.rows : a.parts) + place * D + row;
+        float2 *ml = (whole ? a.rows_ml : a.parts_ml) + place + row;
         if (any) {
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
-            float o[32];
+            uint32_t o[32];
             ld32(o_col + 32u * (uint32_t)k, o);
+            wait_ld(o);
             if (row < rows) {
 #pragma unroll
-              for (int y = 0; y < 32; y += 4)
-                *reinterpret_cast<float4 *>(dst + 32 * k + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+              for (int y = 0; y < 32; ++y) dst[(size_t)(32 * k + y) * rows] = __uint_as_float(o[y]);
             }
           }
         }
@@ -671,95 +768,121 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
+  griddep_wait();  // the join, which waits for this launch, reads what the one before wrote
 }
 
 // --------------------------------------------------------------------------- the join
 
 // A row's parts: its own slots', then those of its prefix in the order of their
-// keys.  kWarps warps a row take every kWarps-th part; lane = D / 32 elements.
-template <bool kHalf, int D, int kWarps>
+// keys.  A thread takes eight elements of a row, of every kSplit-th part; the
+// lanes of a warp are consecutive rows of a KV head, which lie side by side in the
+// parts.  First the parts' references, then, scaled by the largest, the rows, four
+// parts' loads in flight.
+template <bool kHalf, int D, int kSplit>
 __global__ void __launch_bounds__(256) paged_prefix_join(Paged c, PrefixArgs a) {
-  constexpr int E = D / 32, kRows = 8 / kWarps;
-  __shared__ float s_ref[8], s_sum[8], s_o[8][D];
+  constexpr int kWide = 8 / kSplit;  // groups of eight elements of a CTA
+  __shared__ float s_ref[8][32], s_sum[8][32], s_o[8][8][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part0 = warp % kWarps;
-  const int row = blockIdx.x * kRows + warp / kWarps, n_rows = c.B * a.Hq;
-  float o[E] = {}, ref = -INFINITY, l = 0.f;
-  if (row < n_rows) {
-    const int b = row / a.Hq, h = row - b * a.Hq, head = h / a.G;
-    const int4 e = a.rec[b];
-    int np = 0, planes = 0, c0 = 0, plane0 = 0, in_tile = 0;
-    bool whole = false;
-    if (e.y > 0) {
-      const int m_tiles = (e.z + a.nb - 1) / a.nb, pairs = (m_tiles + 1) / 2, m = e.w / a.nb, pair = m >> 1;
-      const bool two = m_tiles - 2 * pair >= 2;
-      const int u0 = e.x + (head * pairs + pair) * e.y, u1 = u0 + e.y, total = *a.total;
-      Shares sh;
-      sh.n = min(a.n_ctas, total);
-      sh.quot = total / sh.n;
-      sh.big = total - sh.quot * sh.n;
-      c0 = sh.first_cta(u0);
-      const int ctas = sh.last_cta(u1) - c0 + 1;
-      whole = e.y <= kWhole || ctas <= 1;
-      planes = two ? 1 : 2;
-      plane0 = two ? m & 1 : 0;
-      np = (whole ? 1 : ctas) * planes;
-      in_tile = (e.w - m * a.nb) * a.G + (h - head * a.G);
-    }
-    for (int p = part0; p <= np; p += kWarps) {
-      const float *src;
-      float2 ml;
-      if (p == 0) {
-        src = a.own + (size_t)row * D;
-        ml = make_float2(a.own_lse[row], 1.f);
-      } else if (whole) {
-        const size_t at = (size_t)(p - 1) * n_rows + row;
-        src = a.rows + at * D;
-        ml = a.rows_ml[at];
-      } else {
-        const int x = (p - 1) / planes, plane = plane0 + (p - 1) - x * planes;
-        const size_t at = ((size_t)(2 * (c0 + x) + (x == 0)) * 2 + plane) * 128 + in_tile;
-        src = a.parts + at * D;
-        ml = a.parts_ml[at];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part0 = warp % kSplit;
+  const int i = blockIdx.x * 32 + lane, head = blockIdx.y, d0 = 8 * (blockIdx.z * kWide + warp / kSplit);
+  const bool on = i < c.B * a.G;
+  const int b = on ? i / a.G : 0, h = on ? i - b * a.G : 0;
+  const size_t row = (size_t)b * a.Hq + head * a.G + h;
+  int np = 0, planes = 1, c0 = 0, plane0 = 0, in_tile = 0, rows = 0, tile_req = 0;
+  bool whole = true;
+  const int4 e = on ? a.rec[b] : make_int4(0, 0, 0, 0);
+  if (e.y > 0) {
+    const int m_tiles = (e.z + a.nb - 1) / a.nb, pairs = (m_tiles + 1) / 2, m = e.w / a.nb, pair = m >> 1;
+    const bool two = m_tiles - 2 * pair >= 2;
+    const int u0 = e.x + (head * pairs + pair) * e.y, u1 = u0 + e.y, total = *a.total;
+    Shares sh;
+    sh.n = min(a.n_ctas, total);
+    sh.quot = total / sh.n;
+    sh.big = total - sh.quot * sh.n;
+    c0 = sh.first_cta(u0);
+    const int ctas = sh.last_cta(u1) - c0 + 1;
+    whole = e.y <= kWhole || ctas <= 1;
+    planes = two ? 1 : 2;
+    plane0 = two && !whole ? m & 1 : 0;
+    np = (whole ? 1 : ctas) * planes;
+    in_tile = (e.w - m * a.nb) * a.G + h;
+    rows = min(a.nb, e.z - m * a.nb) * a.G;
+    tile_req = b - (e.w - m * a.nb);
+  }
+  auto place = [&](int p) {  // of part p >= 1
+    const int x = planes == 2 ? (p - 1) >> 1 : p - 1, plane = plane0 + (planes == 2 ? (p - 1) & 1 : 0);
+    return whole ? whole_part(plane, head, tile_req, c, a.G) : cut_part(2 * (c0 + x) + (x == 0), plane);
+  };
+  const float *part = whole ? a.rows : a.parts;
+  const float2 *part_ml = whole ? a.rows_ml : a.parts_ml;
+  auto ml_of = [&](int p) {
+    return p == 0 ? make_float2(a.own_lse[row], 1.f) : __ldcg(part_ml + place(p) + in_tile);
+  };
+  float o[8] = {}, ref = -INFINITY, l = 0.f;
+  if (on) {
+#pragma unroll 4
+    for (int p = part0; p <= np; p += kSplit) ref = fmaxf(ref, ml_of(p).x);
+    const float base = ref == -INFINITY ? 0.f : ref;
+    for (int p0 = part0; p0 <= np; p0 += 4 * kSplit) {
+      float v[4][8], f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int p = p0 + u * kSplit;
+        f[u] = 0.f;
+        if (p > np) continue;
+        const float2 ml = ml_of(p);
+        if (ml.x == -INFINITY && ml.y == ml.y) continue;  // nothing was seen: what the rows hold does not count
+        f[u] = exp2f(ml.x == -INFINITY ? 0.f : ml.x - base);
+        l += f[u] * ml.y;
+        if (p == 0) {
+#pragma unroll
+          for (int y = 0; y < 8; y += 4)
+            *reinterpret_cast<float4 *>(&v[u][y]) = *reinterpret_cast<const float4 *>(a.own + row * D + d0 + y);
+        } else {
+          const float *src = part + place(p) * D + in_tile + (size_t)d0 * rows;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[u][y] = __ldcg(src + (size_t)y * rows);
+        }
       }
-      float v[E];
 #pragma unroll
-      for (int y = 0; y < E; ++y) v[y] = __ldcg(src + lane * E + y);
-      const bool none = ml.x == -INFINITY && !(ml.y != ml.y);  // nothing was seen: what the row holds does not count
-      const float top = fmaxf(ref, ml.x), f0 = ref == -INFINITY ? 0.f : exp2f(ref - top), f1 = none ? 0.f : exp2f(ml.x == -INFINITY ? 0.f : ml.x - top);
-      l = l * f0 + (none ? 0.f : ml.y * f1);
+      for (int u = 0; u < 4; ++u)
+        if (f[u] != 0.f) {
 #pragma unroll
-      for (int y = 0; y < E; ++y) o[y] = o[y] * f0 + (none ? 0.f : v[y] * f1);
-      ref = top;
+          for (int y = 0; y < 8; ++y) o[y] += f[u] * v[u][y];
+        }
     }
   }
-  if (kWarps > 1) {
-    if (lane == 0) {
-      s_ref[warp] = ref;
-      s_sum[warp] = l;
-    }
+  if (kSplit > 1) {
+    s_ref[warp][lane] = ref;
+    s_sum[warp][lane] = l;
 #pragma unroll
-    for (int y = 0; y < E; ++y) s_o[warp][lane * E + y] = o[y];
+    for (int y = 0; y < 8; ++y) s_o[warp][y][lane] = o[y];
     __syncthreads();
     if (part0 > 0) return;
-    for (int x = 1; x < kWarps; ++x) {
-      const float r = s_ref[warp + x], s = s_sum[warp + x];
-      const float top = fmaxf(ref, r), f0 = ref == -INFINITY ? 0.f : exp2f(ref - top), f1 = r == -INFINITY ? 0.f : exp2f(r - top);
-      l = l * f0 + s * f1;
 #pragma unroll
-      for (int y = 0; y < E; ++y) o[y] = o[y] * f0 + s_o[warp + x][lane * E + y] * f1;
-      ref = top;
+    for (int x = 1; x < kSplit; ++x) ref = fmaxf(ref, s_ref[warp + x][lane]);
+    const float base = ref == -INFINITY ? 0.f : ref;
+    l = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) o[y] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kSplit; ++x) {
+      const float r = s_ref[warp + x][lane], f = exp2f(r == -INFINITY ? 0.f : r - base);
+      l += f * s_sum[warp + x][lane];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] += f * s_o[warp + x][y][lane];
     }
   }
-  if (row >= n_rows) return;
-  uint16_t z[E];
+  if (!on) return;
+  uint32_t z[4];
 #pragma unroll
-  for (int y = 0; y < E; ++y) z[y] = to16<kHalf>(l == 0.f ? 0.f : __fdividef(o[y], l));
-  uint16_t *dst = a.out + (size_t)row * D + lane * E;
-  if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(z[0] | (uint32_t)z[1] << 16, z[E - 2] | (uint32_t)z[E - 1] << 16);
-  else *reinterpret_cast<uint32_t *>(dst) = z[0] | (uint32_t)z[1] << 16;
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+  for (int y = 0; y < 8; y += 2) {
+    const float x0 = l == 0.f ? 0.f : __fdividef(o[y], l), x1 = l == 0.f ? 0.f : __fdividef(o[y + 1], l);
+    z[y / 2] = to16<kHalf>(x0) | (uint32_t)to16<kHalf>(x1) << 16;
+  }
+  *reinterpret_cast<uint4 *>(a.out + row * D + d0) = make_uint4(z[0], z[1], z[2], z[3]);
+  if (a.lse && d0 == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -790,10 +913,10 @@ cudaError_t launch_parts(const CUtensorMap &mq, const CUtensorMap &mk, const CUt
 
 template <bool kHalf, int D>
 cudaError_t launch_join(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  const int rows = c.B * a.Hq;
-  // eight warps a row where rows are few and their parts, then, many
-  return rows <= 16 * sms ? launch_pdl(paged_prefix_join<kHalf, D, 8>, dim3((unsigned)rows), dim3(256), 0, stream, c, a)
-                          : launch_pdl(paged_prefix_join<kHalf, D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, c, a);
+  // eight warps to a row's parts where rows are few and their parts, then, many
+  const unsigned x = (unsigned)((c.B * a.G + 31) / 32), y = (unsigned)c.Hkv;
+  return c.B * a.Hq <= 16 * sms ? launch_pdl(paged_prefix_join<kHalf, D, 8>, dim3(x, y, D / 8), dim3(256), 0, stream, c, a)
+                                : launch_pdl(paged_prefix_join<kHalf, D, 2>, dim3(x, y, D / 32), dim3(256), 0, stream, c, a);
 }
 
 struct Sizes {
