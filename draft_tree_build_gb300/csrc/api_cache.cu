@@ -400,7 +400,7 @@ int bastion_paged_prefix_attention(const bastion_paged_cache *cache, const int32
   if (G > 16) return BASTION_ERR_UNSUPPORTED;
   const int64_t cap = (int64_t)max_prefix_pages * cache->page_size;
   if (n_groups < 1 || n_groups > kMaxB || max_prefix_pages < 1 || cap > kMaxCap || !tiles_ok(cache) ||
-      (int64_t)n_groups * cache->Hkv * ((cap + 127) / 128) * (1 + (int64_t)cache->B * G / 128) >= (1LL << 31))
+      cache->Hkv * ((cap + 127) / 128) * (n_groups + (int64_t)cache->B * G / 112) >= (1LL << 31))
     return BASTION_ERR_SIZE;
   if (!stride_ok(cache->B, q_stride_b, (int64_t)Hq * cache->D)) return BASTION_ERR_SIZE;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(prefix_table, 4))

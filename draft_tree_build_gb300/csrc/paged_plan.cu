@@ -37,30 +37,36 @@ struct PlanArgs {
   int32_t *status;
 };
 
-struct Sums {
-  int64_t warp[2][kThreads / 32];
-};
-
-// Exclusive prefix sums over the threads, in order; the total in *all.
-__device__ __forceinline__ int64_t scan(int64_t x, int64_t *warp_sum, int64_t *all) {
+// Exclusive prefix sums over the threads, in order, of N values at once; the totals in all.
+template <int N>
+__device__ __forceinline__ void scan(int64_t (&x)[N], int64_t (*warp_sum)[kThreads / 32], int64_t (&all)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t y = x;
+  int64_t y[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t z = __shfl_up_sync(kFull, y, o);
-    if (lane >= o) y += z;
-  }
-  if (lane == 31) warp_sum[warp] = y;
+  for (int k = 0; k < N; ++k) y[k] = x[k];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t z = __shfl_up_sync(kFull, y[k], o);
+      if (lane >= o) y[k] += z;
+    }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (lane == 31) warp_sum[k][warp] = y[k];
   __syncthreads();
-  int64_t before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int64_t z = warp_sum[w];
-    before += w < warp ? z : 0;
-    total += z;
+  for (int k = 0; k < N; ++k) {
+    int64_t before = 0;
+    all[k] = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int64_t z = warp_sum[k][w];
+      before += w < warp ? z : 0;
+      all[k] += z;
+    }
+    x[k] = before + y[k] - x[k];
   }
-  *all = total;
-  return before + y - x;
 }
 
 // The last of n ascending entries that is at most x.
@@ -102,22 +108,25 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   // everything that may be updated in place has been read
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
-    if (s_last) *a.arrived = 0;
+    s_last = true;
+    if (gridDim.x > 1) {
+      __threadfence();
+      s_last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+      if (s_last) *a.arrived = 0;
+    }
     if (tell && n_free != free_in) atomicOr(&a.status[0], BASTION_STATUS_BAD_PAGE);
   }
-  int64_t rows = 0;
+  int64_t rows[1] = {0}, all[1];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (n[i] < 0 || (int64_t)n[i] + count[i] > a.cap) bad[i] = BASTION_STATUS_KV_OVERFLOW;
     else if (held[i] < 0 || held[i] > a.max_pages || ((int64_t)held[i] << a.shift) < n[i]) bad[i] = BASTION_STATUS_BAD_PAGE;
     need[i] = bad[i] ? held[i] : (n[i] + count[i] + a.page - 1) >> a.shift;
-    rows += bad[i] ? 0 : count[i];
+    rows[0] += bad[i] ? 0 : count[i];
   }
-  int64_t all;
   if (a.row_start) {  // packed rows: first come, first served
-    int64_t at = scan(rows, sums[0], &all);
+    scan(rows, &sums[0], all);
+    int64_t at = rows[0];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (bad[i]) continue;
@@ -128,19 +137,19 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
       }
     }
   }
-  int64_t back = 0, more = 0, all_back, all_more;
+  int64_t both[2] = {0, 0}, totals[2];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (need[i] < held[i]) {
-      if (a.trim) back += held[i] - need[i];
+      if (a.trim) both[0] += held[i] - need[i];
       else need[i] = held[i];
     }
-    more += max(0, need[i] - held[i]);
+    both[1] += max(0, need[i] - held[i]);
   }
-  back = scan(back, sums[1], &all_back);
-  more = scan(more, sums[2], &all_more);
-  const int64_t there = n_free + all_back;
-  int64_t row = 0;
+  scan(both, &sums[1], totals);
+  int64_t back = both[0], more = both[1];
+  const int64_t all_back = totals[0], all_more = totals[1], there = n_free + all_back;
+  rows[0] = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i;
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
       need[i] = held[i];
     }
     if (bad[i]) count[i] = 0;
-    row += count[i];
+    rows[0] += count[i];
     if (!here) continue;
     s_n[r] = n[i];
     s_held[r] = held[i];
@@ -165,18 +174,21 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
     s_count[r] = count[i];
     if (bad[i] && tell) atomicOr(&a.status[r], bad[i]);
   }
-  row = scan(row, sums[3], &all);
-  const int total_rows = (int)all;  // at most n_rows
+  int total_rows = 0;  // at most n_rows
+  if (a.row_start) {
+    scan(rows, &sums[3], all);
+    total_rows = (int)all[0];
+    int row = (int)rows[0];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = r0 + i;
-    if (i < chunk && r < a.B) {
-      s_row[r] = (int)row;
-      if (a.row_start && tell) a.row_start[r] = (int)row;
+    for (int i = 0; i < kPer; ++i) {
+      const int r = r0 + i;
+      if (i < chunk && r < a.B) {
+        s_row[r] = row;
+        if (tell) a.row_start[r] = row;
+      }
+      row += count[i];
     }
-    row += count[i];
   }
-  // pages taken: up to the first request that there were too few for
   if (tid == 0) {
     s_back[a.B] = all_back;
     s_more[a.B] = all_more;
@@ -252,7 +264,6 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
 
   // ------------------------------------------------------------ table and free list
   const int64_t most = min(all_more, there);
-  int64_t used = 0;  // pages taken: those of the requests before the first that was refused
   for (int64_t x = first; x < most; x += stride) {
     const int r = last_at_most(s_more, a.B, x), idx = s_held[r] + (int)(x - s_more[r]);
     if (idx >= s_need[r]) continue;  // refused
@@ -261,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
     if (p < 0 || p >= a.n_pages) atomicOr(&a.status[r], BASTION_STATUS_BAD_PAGE);
   }
   // the first request that was refused, if any, is where the sum of pages passes what there is
-  used = all_more;
+  int64_t used = all_more;
   if (all_more > there) used = s_more[last_at_most(s_more, a.B + 1, there)];
   const int64_t left = there - used;
   for (int64_t y = first; n_free + y < left && n_free + y < a.n_pages; y += stride) a.free_pages[n_free + y] = given(y);

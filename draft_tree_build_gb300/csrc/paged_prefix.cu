@@ -12,7 +12,7 @@
 // neither may wait for the other:
 //  * one persistent CTA per SM.  A unit is (group, KV head, up to 256 rows); the
 //    batch is a list of 128-key tiles, unit by unit, of which every CTA takes an
-//    equal contiguous share (paged_walk.cuh);
+//    equal contiguous share (paged_units.cuh);
 //  * warp 0 streams keys and warp 2 values through one ring in shared memory,
 //    warp 3 the queries of the next M tile of 128 rows, with TMA;
 //  * warp 1 issues the products, S = Q K^T from shared memory and O += P V with P
@@ -37,7 +37,7 @@
 // TMEM and returns.
 #include "paged.cuh"
 #include "paged_tc.cuh"
-#include "paged_walk.cuh"
+#include "paged_units.cuh"
 
 namespace bastion {
 
@@ -58,8 +58,8 @@ struct PrefixArgs {
   int Hq, G, nb;  // nb = 128 / G requests an M tile
   float scale_log2;
   int swap;
-  int4 *rec;       // [B]: first tile of the request's group, tiles, requests of the group, its place among them
-  int *total;      // tiles of the batch
+  int4 *rec;       // [B]: first item of the request's group, tiles, requests of the group, its place among them
+  int2 *shares;    // items of the batch, items of the heaviest tile
   float *own;      // [B, Hq, D], normalised
   float *own_lse;  // [B, Hq], base 2
   float *rows;     // [2][B, Hq, D]: units of one CTA
@@ -83,7 +83,7 @@ struct Layout {
   static constexpr uint32_t kTile = kBlocks * kBlock;
   static constexpr uint32_t kOffQ = kStages * kTile;   // two M tiles
   static constexpr uint32_t kOffList = kOffQ + 2 * kTile;
-  static constexpr uint32_t kOffMisc = kOffList + kMaxRequests * 16;
+  static constexpr uint32_t kOffMisc = kOffList + kMaxRequests * sizeof(UnitEntry);
 };
 
 struct Misc {
@@ -241,61 +241,6 @@ __device__ __forceinline__ size_t whole_part(int plane, int head, int req, const
 }
 __device__ __forceinline__ size_t cut_part(int slot, int plane) { return ((size_t)slot * 2 + plane) * 128; }
 
-// --------------------------------------------------------------------------- a CTA's tiles
-
-// Tile t of the unit (group, KV head, pair of M tiles).  list: the groups that
-// have tiles: first request (and the group's number in the upper half), requests,
-// slots of the prefix, first tile.
-template <bool kUniform>
-struct Units {
-  const int4 *list;
-  int li, group, req, n, len, tiles, m_tiles, head, pair, t, left;
-  bool first;  // the first tile of its segment
-  static __device__ __forceinline__ int uniform(int x) {
-    return kUniform ? __shfl_sync(kFull, x, 0) : x;
-  }
-  __device__ __forceinline__ void load(int nb) {
-    const int4 e = list[li];
-    group = uniform(e.x >> 16);
-    req = uniform(e.x & 0xffff);
-    n = uniform(e.y);
-    len = uniform(e.z);
-    tiles = (len + kTileKeys - 1) / kTileKeys;
-    m_tiles = (n + nb - 1) / nb;
-  }
-  __device__ __forceinline__ void start(const int4 *l, int index, int off, int count, int nb) {
-    list = l;
-    li = index;
-    left = count;
-    first = true;
-    if (left > 0) {
-      load(nb);
-      const int u = off / tiles, pairs = (m_tiles + 1) / 2;
-      t = off - u * tiles;
-      head = u / pairs;
-      pair = u - head * pairs;
-    }
-  }
-  __device__ __forceinline__ int ms() const { return min(2, m_tiles - 2 * pair); }  // M tiles of the unit
-  __device__ __forceinline__ void step(int heads, int nb) {
-    first = false;
-    --left;
-    if (++t == tiles) {
-      t = 0;
-      first = true;
-      if (++pair * 2 >= m_tiles) {
-        pair = 0;
-        if (++head == heads) {
-          head = 0;
-          ++li;
-          if (left > 0) load(nb);
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == 1; }
-};
-
 template <bool kHalf, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -307,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *smem =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Misc &ms = *reinterpret_cast<Misc *>(smem + Lay::kOffMisc);
-  int4 *list = reinterpret_cast<int4 *>(smem + Lay::kOffList);
+  UnitEntry *list = reinterpret_cast<UnitEntry *>(smem + Lay::kOffList);
   volatile int *abort = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -342,13 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------ this CTA's share
   // A thread has consecutive groups.  A group begins where the ones before it end, at the earliest.
   const int chunk = (a.n_groups + kThreads - 1) / kThreads, g0 = tid * chunk;
-  int from[kPer], n_req[kPer], len[kPer], idx[kPer];
+  int from[kPer], n_req[kPer], len[kPer];
   int ends = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int g = g0 + i;
     from[i] = n_req[i] = len[i] = 0;
-    idx[i] = g;
     if (i >= chunk || g >= a.n_groups) continue;
     const int x = a.start[g], y = a.start[g + 1], n = a.len[g];
     if (x >= 0 && x <= y && y <= c.B) {
@@ -373,8 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-  for (int x = 0; x < warp; ++x) before = max(before, ms.warp_max[x]);
-  int cnt = 0, til = 0, unit_tiles[kPer], group_tiles[kPer];
+#pragma unroll
+  for (int x = 0; x < kThreads / 32; ++x) before = max(before, x < warp ? ms.warp_max[x] : 0);
+  int cnt = 0, sum = 0, items[kPer];
+  bool two = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int end = n_req[i];
@@ -384,23 +330,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_req[i] > 0 && (len[i] < 0 || len[i] > a.cap) && blockIdx.x == 0)
       atomicOr(&a.status[from[i]], BASTION_STATUS_KV_OVERFLOW);
     len[i] = min(max(len[i], 0), a.cap);
-    unit_tiles[i] = n_req[i] > 0 ? (len[i] + kTileKeys - 1) / kTileKeys : 0;
-    group_tiles[i] = unit_tiles[i] * (((n_req[i] + a.nb - 1) / a.nb + 1) / 2) * c.Hkv;
-    cnt += group_tiles[i] > 0;
-    til += group_tiles[i];
+    items[i] = tiles_of(len[i]) * m_tiles_of(n_req[i], a.nb) * c.Hkv;
+    cnt += items[i] > 0;
+    sum += items[i];
+    two |= items[i] > 0 && n_req[i] > a.nb;
   }
-  int cnt_i = cnt, til_i = til;
+  int cnt_i = cnt, sum_i = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kFull, cnt_i, o), y = __shfl_up_sync(kFull, til_i, o);
+    const int x = __shfl_up_sync(kFull, cnt_i, o), y = __shfl_up_sync(kFull, sum_i, o);
     if (lane >= o) {
       cnt_i += x;
-      til_i += y;
+      sum_i += y;
     }
   }
-  if (lane == 31) ms.warp_sum[warp] = make_int2(cnt_i, til_i);
-  __syncthreads();
-  int rank = cnt_i - cnt, at = til_i - til, total = 0, groups = 0;
+  if (lane == 31) ms.warp_sum[warp] = make_int2(cnt_i, sum_i);
+  const int widest = __syncthreads_or(two) ? 2 : 1;
+  int rank = cnt_i - cnt, at = sum_i - sum, total = 0, groups = 0;
 #pragma unroll
   for (int x = 0; x < kThreads / 32; ++x) {
     const int2 y = ms.warp_sum[x];
@@ -411,30 +357,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     groups += y.x;
     total += y.y;
   }
-  Shares sh;
-  sh.n = min((int)gridDim.x, total);
-  sh.quot = sh.n > 0 ? total / sh.n : 0;
-  sh.big = total - sh.quot * sh.n;
+  const UnitShares sh = UnitShares::of((int)gridDim.x, total, widest);
   const int b0 = sh.begin(blockIdx.x), b1 = sh.begin(blockIdx.x + 1);
   const bool busy = (int)blockIdx.x < sh.n;
   if (tid == 0 && busy && (int)blockIdx.x == sh.n - 1) ms.f1 = total;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (group_tiles[i] == 0) continue;
-    const int t = unit_tiles[i], end = at + group_tiles[i];
-    list[rank] = make_int4(from[i] | idx[i] << 16, n_req[i], len[i], at);
-    if (busy) {
+    if (items[i] == 0) continue;
+    const int end = at + items[i];
+    list[rank] = UnitEntry{from[i] | (g0 + i) << 16, n_req[i], len[i], at};
+    if (busy && ((b0 >= at && b0 < end) || (b1 >= at && b1 < end))) {
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
-        const int off = (f - at) % t, to = Shares::moved(f, off, t);
+        const int off = entry_boundary(f - at, tiles_of(len[i]), m_tiles_of(n_req[i], a.nb));
         if (k) {
-          ms.f1 = to;
+          ms.f1 = at + off;
         } else {
-          ms.f0 = to;
-          ms.li0 = to == end ? rank + 1 : rank;  // the next group's begin
-          ms.off0 = to == end ? 0 : to - at;
+          ms.f0 = at + off;
+          ms.li0 = off == items[i] ? rank + 1 : rank;  // the next group's begin
+          ms.off0 = off == items[i] ? 0 : off;
         }
       }
     }
@@ -604,18 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     // where the join finds each request's parts
-    if (blockIdx.x == 0 && lane == 0) *a.total = total;
+    if (blockIdx.x == 0 && lane == 0) *a.shares = make_int2(total, widest);
     for (int b = blockIdx.x * 32 + lane; b < c.B; b += gridDim.x * 32) {
       int lo = 0, hi = groups;
       while (hi - lo > 1) {  // the last group that begins at b or before
         const int mid = (lo + hi) >> 1;
-        if ((list[mid].x & 0xffff) <= b) lo = mid; else hi = mid;
+        if ((list[mid].who & 0xffff) <= b) lo = mid; else hi = mid;
       }
       int4 e = make_int4(0, 0, 0, 0);
       if (groups > 0) {
-        const int4 l = list[lo];
-        const int place = b - (l.x & 0xffff);
-        if (place >= 0 && place < l.y) e = make_int4(l.w, (l.z + kTileKeys - 1) / kTileKeys, l.y, place);
+        const UnitEntry l = list[lo];
+        const int place = b - (l.who & 0xffff);
+        if (place >= 0 && place < l.n) e = make_int4(l.at, tiles_of(l.len), l.n, place);
       }
       a.rec[b] = e;
     }
@@ -789,30 +732,22 @@ __global__ void __launch_bounds__(256) paged_prefix_join(Paged c, PrefixArgs a) 
   const bool on = i < c.B * a.G;
   const int b = on ? i / a.G : 0, h = on ? i - b * a.G : 0;
   const size_t row = (size_t)b * a.Hq + head * a.G + h;
-  int np = 0, planes = 1, c0 = 0, plane0 = 0, in_tile = 0, rows = 0, tile_req = 0;
-  bool whole = true;
+  int np = 0, in_tile = 0, rows = 0, tile_req = 0;
+  UnitParts parts = {true, 0, 0, 1, 0};
   const int4 e = on ? a.rec[b] : make_int4(0, 0, 0, 0);
   if (e.y > 0) {
-    const int m_tiles = (e.z + a.nb - 1) / a.nb, pairs = (m_tiles + 1) / 2, m = e.w / a.nb, pair = m >> 1;
-    const bool two = m_tiles - 2 * pair >= 2;
-    const int u0 = e.x + (head * pairs + pair) * e.y, u1 = u0 + e.y, total = *a.total;
-    Shares sh;
-    sh.n = min(a.n_ctas, total);
-    sh.quot = total / sh.n;
-    sh.big = total - sh.quot * sh.n;
-    c0 = sh.first_cta(u0);
-    const int ctas = sh.last_cta(u1) - c0 + 1;
-    whole = e.y <= kWhole || ctas <= 1;
-    planes = two ? 1 : 2;
-    plane0 = two && !whole ? m & 1 : 0;
-    np = (whole ? 1 : ctas) * planes;
+    const int m = e.w / a.nb;
+    const int2 items = *a.shares;
+    parts = UnitParts::of(UnitShares::of(a.n_ctas, items.x, items.y), e.x, e.y, m_tiles_of(e.z, a.nb), head, m);
+    np = parts.count();
     in_tile = (e.w - m * a.nb) * a.G + h;
     rows = min(a.nb, e.z - m * a.nb) * a.G;
     tile_req = b - (e.w - m * a.nb);
   }
+  const bool whole = parts.whole;
   auto place = [&](int p) {  // of part p >= 1
-    const int x = planes == 2 ? (p - 1) >> 1 : p - 1, plane = plane0 + (planes == 2 ? (p - 1) & 1 : 0);
-    return whole ? whole_part(plane, head, tile_req, c, a.G) : cut_part(2 * (c0 + x) + (x == 0), plane);
+    const int x = parts.planes == 2 ? (p - 1) >> 1 : p - 1, y = parts.planes == 2 ? (p - 1) & 1 : 0;
+    return whole ? whole_part(y, head, tile_req, c, a.G) : cut_part(parts.slot(x), parts.plane + y);
   };
   const float *part = whole ? a.rows : a.parts;
   const float2 *part_ml = whole ? a.rows_ml : a.parts_ml;
@@ -920,8 +855,8 @@ cudaError_t launch_join(int sms, const Paged &c, const PrefixArgs &a, cudaStream
 }
 
 struct Sizes {
-  size_t own_ws, own, own_lse, rec, total, rows, rows_ml, parts, parts_ml;
-  size_t all() const { return own_ws + own + own_lse + rec + total + rows + rows_ml + parts + parts_ml; }
+  size_t own_ws, own, own_lse, rec, shares, rows, rows_ml, parts, parts_ml;
+  size_t all() const { return own_ws + own + own_lse + rec + shares + rows + rows_ml + parts + parts_ml; }
 };
 Sizes sizes_of(int B, int Hq, int Hkv, int D) {
   const size_t rows = (size_t)B * Hq, parts = (size_t)2 * kMaxParts * 2 * 128;
@@ -930,7 +865,7 @@ Sizes sizes_of(int B, int Hq, int Hkv, int D) {
   s.own = up256(rows * D * 4);
   s.own_lse = up256(rows * 4);
   s.rec = up256((size_t)B * 16);
-  s.total = 256;
+  s.shares = 256;
   s.rows = 2 * rows * D * 4;
   s.rows_ml = up256(2 * rows * 8);
   s.parts = parts * D * 4;
@@ -971,7 +906,7 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
   a.own = reinterpret_cast<float *>(take(sz.own));
   a.own_lse = reinterpret_cast<float *>(take(sz.own_lse));
   a.rec = reinterpret_cast<int4 *>(take(sz.rec));
-  a.total = reinterpret_cast<int *>(take(sz.total));
+  a.shares = reinterpret_cast<int2 *>(take(sz.shares));
   a.rows = reinterpret_cast<float *>(take(sz.rows));
   a.rows_ml = reinterpret_cast<float2 *>(take(sz.rows_ml));
   a.parts = reinterpret_cast<float *>(take(sz.parts));

@@ -1,0 +1,144 @@
+// How the tiles of a shared-prefix attention are dealt to the CTAs of a launch,
+// how a CTA walks its share, and how the join finds a unit's parts.  Plain index
+// arithmetic, for the host as well.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "paged_walk.cuh"
+
+namespace bastion {
+
+// A list entry: a group of requests and its prefix.
+struct UnitEntry {
+  int32_t who;  // the first request, and the group's number << 16
+  int32_t n;    // requests
+  int32_t len;  // slots
+  int32_t at;   // first work item
+};
+
+__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+__host__ __device__ __forceinline__ int m_tiles_of(int n, int nb) { return (n + nb - 1) / nb; }
+
+// A unit is an entry, a KV head and a pair of M tiles of nb requests (or the odd one left);
+// a tile of it is 128 keys, which weigh as many work items as it has M tiles.  The
+// items are in order entry, head, pair, tile, and every CTA takes an equal share
+// of them.  A boundary moves to the begin of its tile, and to a unit's begin or end
+// where cutting costs more than it saves: within a unit of at most kWhole tiles,
+// and within kSnap tiles of the ends of a longer one.
+struct UnitShares {
+  int n, quot, big;
+  // widest: the items of the heaviest tile, so that no two boundaries fall into one tile
+  static __host__ __device__ __forceinline__ UnitShares of(int ctas, int total, int widest) {
+    UnitShares s;
+    s.n = total == 0 ? 0 : imin(ctas, total / widest > 0 ? total / widest : 1);
+    s.quot = s.n > 0 ? total / s.n : 0;
+    s.big = total - s.quot * s.n;
+    return s;
+  }
+  __host__ __device__ __forceinline__ int begin(int cta) const { return cta * quot + imin(cta, big); }
+  __host__ __device__ __forceinline__ int owner(int item) const {  // before boundaries move
+    const int edge = big * (quot + 1);
+    return item < edge ? item / (quot + 1) : big + (item - edge) / quot;
+  }
+  // The tile that a boundary `off` items into a unit moves to.
+  static __host__ __device__ __forceinline__ int moved(int off, int tiles, int weight) {
+    if (tiles <= kWhole) return 2 * off <= tiles * weight ? 0 : tiles;
+    const int t = off / weight;
+    return t <= kSnap ? 0 : tiles - t <= kSnap ? tiles : t;
+  }
+  // The CTAs of a unit of more than kWhole tiles, items [u0, u1): those with its first and its last tile.
+  __host__ __device__ __forceinline__ int first_cta(int u0, int weight) const { return owner(u0 + (kSnap + 1) * weight - 1); }
+  __host__ __device__ __forceinline__ int last_cta(int u1, int weight) const { return owner(u1 - kSnap * weight - 1); }
+};
+
+// A CTA's tiles, one after the other.  kUniform: all lanes of a warp walk together,
+// and the compiler is told so.
+template <bool kUniform>
+struct Units {
+  const UnitEntry *list;
+  int li, group, req, n, len, tiles, m_tiles, head, pair, t, left;
+  bool first;  // the first tile of its segment
+  static __host__ __device__ __forceinline__ int uniform(int x) {
+#ifdef __CUDA_ARCH__
+    if (kUniform) return __shfl_sync(0xffffffffu, x, 0);
+#endif
+    return x;
+  }
+  __host__ __device__ __forceinline__ void load(int nb) {
+    const UnitEntry e = list[li];
+    const int who = uniform(e.who);
+    group = who >> 16;
+    req = who & 0xffff;
+    n = uniform(e.n);
+    len = uniform(e.len);
+    tiles = tiles_of(len);
+    m_tiles = m_tiles_of(n, nb);
+  }
+  __host__ __device__ __forceinline__ int ms() const { return imin(2, m_tiles - 2 * pair); }  // M tiles of the unit
+  // Entry `index`, `off` items into it (a tile's begin), `count` items in all.
+  __host__ __device__ __forceinline__ void start(const UnitEntry *l, int index, int off, int count, int nb) {
+    list = l;
+    li = index;
+    left = count;
+    first = true;
+    if (left > 0) {
+      load(nb);
+      const int per_head = tiles * m_tiles;
+      head = off / per_head;
+      off -= head * per_head;
+      pair = off / (2 * tiles);
+      t = (off - pair * 2 * tiles) / ms();
+    }
+  }
+  __host__ __device__ __forceinline__ void step(int heads, int nb) {
+    first = false;
+    left -= ms();
+    if (++t == tiles) {
+      t = 0;
+      first = true;
+      if (++pair * 2 >= m_tiles) {
+        pair = 0;
+        if (++head == heads) {
+          head = 0;
+          ++li;
+          if (left > 0) load(nb);
+        }
+      }
+    }
+  }
+  __host__ __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == ms(); }
+};
+
+// Where boundary `off` items into an entry falls: items into the entry, tiles whole.
+__host__ __device__ __forceinline__ int entry_boundary(int off, int tiles, int m_tiles) {
+  const int per_head = tiles * m_tiles, h = off / per_head, rest = off - h * per_head, pair = rest / (2 * tiles);
+  const int weight = imin(2, m_tiles - 2 * pair);
+  return h * per_head + pair * 2 * tiles + weight * UnitShares::moved(rest - pair * 2 * tiles, tiles, weight);
+}
+
+// A unit's parts as the join sees them.  Each of its CTAs leaves one for every M
+// tile, or two for a unit of one M tile, whose key tiles the two warpgroups take
+// in turn.  A unit that one CTA finishes keeps its parts by request, the others
+// in the CTAs' slots: the last segment of its first CTA, the first of the others.
+struct UnitParts {
+  bool whole;
+  int cta, ctas, planes, plane;  // the first CTA, how many, parts of each and the first of them
+  static __host__ __device__ __forceinline__ UnitParts of(const UnitShares &s, int at, int tiles, int m_tiles, int head,
+                                                          int m) {
+    const int pair = m >> 1, weight = imin(2, m_tiles - 2 * pair);
+    const int u0 = at + (head * m_tiles + 2 * pair) * tiles, u1 = u0 + tiles * weight;
+    UnitParts p;
+    p.cta = tiles > kWhole ? s.first_cta(u0, weight) : 0;
+    p.ctas = tiles > kWhole ? s.last_cta(u1, weight) - p.cta + 1 : 1;
+    p.whole = p.ctas <= 1;
+    p.planes = weight == 2 ? 1 : 2;
+    p.plane = weight == 2 ? m & 1 : 0;
+    return p;
+  }
+  __host__ __device__ __forceinline__ int count() const { return ctas * planes; }
+  __host__ __device__ __forceinline__ int slot(int x) const { return 2 * (cta + x) + (x == 0 ? 1 : 0); }  // of CTA x of them
+};
+
+}  // namespace bastion

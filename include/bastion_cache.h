@@ -294,8 +294,8 @@ int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q
  *               A group's prefix_len outside [0, max_prefix_pages * page_size] or
  *               page outside the pool sets its first request's status bit.
  * Limits: as bastion_paged_attention; 1 <= n_groups <= 1024, max_prefix_pages *
- * page_size <= 2^28, n_groups * Hkv * ceil(max_prefix_pages * page_size / 128) *
- * (1 + B * Hq / Hkv / 128) < 2^31.
+ * page_size <= 2^28, Hkv * ceil(max_prefix_pages * page_size / 128) * (n_groups +
+ * B * Hq / Hkv / 112) < 2^31 (BASTION_ERR_SIZE).
  * Weights enter the products as there: as two 16-bit terms.  Results do not
  * depend on the order in which the parts of a split prefix finish.
  * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
