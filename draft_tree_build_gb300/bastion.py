@@ -937,14 +937,24 @@ class PagedCache:
     page_table None: request r owns pages r * max_pages .. (r + 1) * max_pages - 1, i.e. the pools are a
     contiguous cache [B, max_pages * page_size, Hkv, D], which ``contiguous()`` gives to bastion_tree_attention.
     weights: keep the accumulated attention weight and the position of every slot, which evict() needs.
+    new_tokens: the cache gives its requests their pages itself, out of n_pages (less the first `reserved`, which
+    are the caller's, for prefixes say): reserve() finds pages and slots for up to new_tokens tokens a request and
+    write() fills them.  prefixes: the most groups that attend_shared() will be given.
     After STATUS_TIMEOUT in status, zero ws_attend before the next attend()."""
 
     def __init__(self, B, Hq, Hkv, D, page_size, max_pages, device, dtype=torch.bfloat16, page_table=None,
-                 n_pages=None, weights=False):
+                 n_pages=None, weights=False, new_tokens=0, reserved=0, prefixes=0):
         self.B, self.Hq, self.Hkv, self.D, self.page_size, self.max_pages = B, Hq, Hkv, D, page_size, max_pages
         self.cap, self.device = max_pages * page_size, device
-        self.identity = page_table is None
-        if page_table is None:
+        self.identity = page_table is None and not new_tokens
+        if new_tokens:
+            if page_table is not None or weights:
+                raise BastionError("paged cache: with new_tokens the page table is the cache's own, and no weights are kept")
+            n_pages = B * max_pages + reserved if n_pages is None else n_pages
+            if not 0 <= reserved < n_pages:
+                raise BastionError("paged cache: reserved pages must leave some of n_pages")
+            page_table = torch.full((B, max_pages), -1, dtype=torch.int32)
+        elif page_table is None:
             n_pages = B * max_pages
             page_table = torch.arange(n_pages, dtype=torch.int32).view(B, max_pages)
         elif n_pages is None:
@@ -959,6 +969,16 @@ class PagedCache:
         self.ws_append = workspace(bastion_paged_append_workspace_bytes(B), device)
         self.ws_attend = workspace(bastion_paged_attention_workspace_bytes(B, Hq, Hkv, D, self.cap, weights), device)
         self.ws_evict = workspace(bastion_paged_evict_workspace_bytes(B, Hkv, self.cap), device) if weights else None
+        self.new_tokens = new_tokens
+        if new_tokens:
+            self.held, self.n_free = i32(B), torch.full((1,), n_pages - reserved, dtype=torch.int32, device=device)
+            self.free_pages = torch.zeros(n_pages, dtype=torch.int32, device=device)
+            self.free_pages[:n_pages - reserved] = torch.arange(n_pages - 1, reserved - 1, -1, device=device)
+            self.slots = torch.full((B * new_tokens,), -1, dtype=torch.int64, device=device)
+            self.slot_pos, self.row_start = i32(B * new_tokens), i32(B + 1)
+            self.ws_plan, self.write_status = workspace(bastion_paged_plan_workspace_bytes(B), device), i32(1)
+        self.ws_prefix = workspace(bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D, prefixes), device) \
+            if prefixes else None
 
     def contiguous(self):
         """(k, v) [B, cap, Hkv, D]: the same memory as a contiguous cache."""
@@ -986,3 +1006,30 @@ class PagedCache:
         bastion_paged_evict(self.k_pool, self.v_pool, self.page_table, self.seq_len, self.n_seen, self.acc, self.pos,
                             budget, n_sink, n_recent, self.seq_len, self.acc, self.pos, self.ws_evict, self.status,
                             stream)
+
+    def reserve(self, m, n_new=None, packed=False, n_rows=None, trim=False, stream=None):
+        """Pages and slots for the next n_new [B] (all: m) tokens of every request, whose lengths grow by them: (slots,
+        positions), rows r * m + i for request r's token i, or packed, n_rows (all: B * m) of them from row_start[r]
+        on; -1 in rows without a token.  trim: pages that a request holds beyond its tokens go back (seq_len 0: all)."""
+        rows = self.B * m if n_rows is None or not packed else n_rows
+        if not self.new_tokens or rows > self.slots.numel():
+            raise BastionError("paged cache: reserve needs new_tokens of that many rows")
+        slots, pos = self.slots[:rows], self.slot_pos[:rows]
+        bastion_paged_plan(self.page_table, self.page_size, self.seq_len, m, self.held, self.held, self.free_pages,
+                           self.n_free, self.n_free, slots, pos, self.ws_plan, self.status, n_new,
+                           self.row_start if packed else None, self.seq_len, trim, stream)
+        return slots, pos
+
+    def write(self, q, k, v, pos, slots, inv_freq, q_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+              factor=1.0, stream=None):
+        """Norms and turns the queries and keys of reserve()'s rows and stores keys and values into their slots: q
+        [T, Hq, D], k and v [T, Hkv, D], q_out [T, Hq, D] or q."""
+        bastion_qk_norm_rope(q, k, pos, inv_freq, q_out, self.write_status, None, q_weight, k_weight, eps, interleaved,
+                             factor, v, self.k_pool, self.v_pool, slots, stream)
+
+    def attend_shared(self, q, prefix_table, prefix_len, group_start, scale, out, lse=None, stream=None):
+        """attend() over the groups' prefixes, in pages of this cache, and then over the requests' own slots."""
+        if self.ws_prefix is None:
+            raise BastionError("paged cache: attend_shared needs prefixes")
+        bastion_paged_prefix_attention(q, self.k_pool, self.v_pool, self.page_table, self.seq_len, prefix_table, prefix_len,
+                                       group_start, scale, out, self.ws_prefix, self.status, lse, stream)
