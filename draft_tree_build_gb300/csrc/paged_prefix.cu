@@ -3,8 +3,9 @@
 //
 //   out = (sum_prefix exp(s_j) v_j + sum_own exp(s_j) v_j) / (sum_prefix exp(s_j) + sum_own exp(s_j))
 //
-// Three launches: the own slots, by the one-token kernel of paged_attention.cu,
-// in 32 bits; the prefixes; and the join of each row's parts.
+// Three launches: the own slots, by the one-token kernel of paged_attention.cu, in
+// 32 bits; the prefixes, which begin on the SMs that the own slots leave free; and
+// the join of each row's parts (paged_prefix_join.cu).
 //
 // The prefixes.  A group's n requests are n * G query rows of a KV head, which
 // read each key and value once per 256 rows: 512 flops a byte at 256 rows of
@@ -35,9 +36,8 @@
 // Every wait is bounded (~1 s); after one ran out the CTA flags the requests of
 // its remaining tiles, waits for its own copies and products (bounded), frees its
 // TMEM and returns.
-#include "paged.cuh"
+#include "paged_prefix.cuh"
 #include "paged_tc.cuh"
-#include "paged_units.cuh"
 
 namespace bastion {
 
@@ -51,26 +51,6 @@ constexpr int kThreads = 384;
 constexpr int kPer = (kMaxRequests + kThreads - 1) / kThreads;  // groups of a thread in the prologue, at most
 constexpr int kBatch = 4;      // tiles whose table entries are read together
 constexpr float kGrow = 8.0f;  // a score may exceed its row's reference by 2^8
-
-struct PrefixArgs {
-  const int32_t *table, *len, *start;  // the groups' prefixes
-  int n_groups, max_pages, cap;
-  int Hq, G, nb;  // nb = 128 / G requests an M tile
-  float scale_log2;
-  int swap;
-  int4 *rec;       // [B]: first item of the request's group, tiles, requests of the group, its place among them
-  int2 *shares;    // items of the batch, items of the heaviest tile
-  float *own;      // [B, Hq, D], normalised
-  float *own_lse;  // [B, Hq], base 2
-  float *rows;     // [2][B, Hq, D]: units of one CTA
-  float2 *rows_ml;
-  float *parts;    // [2 kMaxParts][2][128][D]: units of several
-  float2 *parts_ml;
-  int n_ctas;
-  uint16_t *out;
-  float *lse;
-  int32_t *status;
-};
 
 // --------------------------------------------------------------------------- shared memory
 
@@ -231,15 +211,6 @@ __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t &hi, uin
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(h1), "f"(h0));
   }
 }
-
-// --------------------------------------------------------------------------- parts
-
-// A part is an M tile's rows: element d of row i of R at (place * D + d * R + i),
-// its reference and sum at place + i.
-__device__ __forceinline__ size_t whole_part(int plane, int head, int req, const Paged &c, int G) {
-  return (((size_t)plane * c.Hkv + head) * c.B + req) * G;
-}
-__device__ __forceinline__ size_t cut_part(int slot, int plane) { return ((size_t)slot * 2 + plane) * 128; }
 
 template <bool kHalf, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -547,20 +518,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     // where the join finds each request's parts
-    if (blockIdx.x == 0 && lane == 0) *a.shares = make_int2(total, widest);
-    for (int b = blockIdx.x * 32 + lane; b < c.B; b += gridDim.x * 32) {
+    for (int x = blockIdx.x * 32 + lane; x < c.B * c.Hkv; x += gridDim.x * 32) {
+      const int b = x / c.Hkv, head = x - b * c.Hkv;
       int lo = 0, hi = groups;
       while (hi - lo > 1) {  // the last group that begins at b or before
         const int mid = (lo + hi) >> 1;
         if ((list[mid].who & 0xffff) <= b) lo = mid; else hi = mid;
       }
-      int4 e = make_int4(0, 0, 0, 0);
+      PartsRec r = {0, 0, 0, 0, 0, 0, 0, 0};
       if (groups > 0) {
         const UnitEntry l = list[lo];
-        const int place = b - (l.who & 0xffff);
-        if (place >= 0 && place < l.n) e = make_int4(l.at, tiles_of(l.len), l.n, place);
+        const int place = b - (l.who & 0xffff), m = place / a.nb;
+        if (place >= 0 && place < l.n) {
+          const UnitParts u = UnitParts::of(sh, l.at, tiles_of(l.len), m_tiles_of(l.n, a.nb), head, m);
+          r.parts = u.count();
+          r.two = u.planes == 2;
+          r.whole = u.whole;
+          r.place0 = (int)(u.whole ? whole_part(0, head, b - (place - m * a.nb), c, a.G) : cut_part(u.slot(0), u.plane));
+          r.place1 = u.whole ? 0 : (int)cut_part(u.slot(1), u.plane);
+          r.step = u.whole ? c.Hkv * c.B * a.G : 128;
+          r.rows = min(a.nb, l.n - m * a.nb) * a.G;
+          r.first = (place - m * a.nb) * a.G;
+        }
       }
-      a.rec[b] = e;
+      a.rec[x] = r;
     }
     if (lane == 0)
       for (int u = max(0, q - 2); u < q; ++u) mbar_wait_bounded(&ms.q_full[u & 1], (uint32_t)(u >> 1) & 1u);
@@ -679,10 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (quad * 32 < rows) {
-        // column by column, so that a warp's rows lie side by side
         const size_t place = whole ? whole_part(count == 2 ? 0 : plane, w.head, w.req + (2 * w.pair + m) * a.nb, c, a.G)
                                    : cut_part(2 * blockIdx.x + (t0 == 0), plane);
-        float *dst = (whole ? a.rows : a.parts) + place * D + row;
+        float *dst = (whole ? a.rows : a.parts) + place * D + row * 4;
         float2 *ml = (whole ? a.rows_ml : a.parts_ml) + place + row;
         if (any) {
 #pragma unroll 1
@@ -692,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_ld(o);
             if (row < rows) {
 #pragma unroll
-              for (int y = 0; y < 32; ++y) dst[(size_t)(32 * k + y) * rows] = __uint_as_float(o[y]);
+              for (int y = 0; y < 32; y += 4)
+                *reinterpret_cast<uint4 *>(dst + (size_t)(32 * k + y) * rows) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
             }
           }
         }
@@ -712,112 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
   griddep_wait();  // the join, which waits for this launch, reads what the one before wrote
-}
-
-// --------------------------------------------------------------------------- the join
-
-// A row's parts: its own slots', then those of its prefix in the order of their
-// keys.  A thread takes eight elements of a row, of every kSplit-th part; the
-// lanes of a warp are consecutive rows of a KV head, which lie side by side in the
-// parts.  First the parts' references, then, scaled by the largest, the rows, four
-// parts' loads in flight.
-template <bool kHalf, int D, int kSplit>
-__global__ void __launch_bounds__(256) paged_prefix_join(Paged c, PrefixArgs a) {
-  constexpr int kWide = 8 / kSplit;  // groups of eight elements of a CTA
-  __shared__ float s_ref[8][32], s_sum[8][32], s_o[8][8][32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part0 = warp % kSplit;
-  const int i = blockIdx.x * 32 + lane, head = blockIdx.y, d0 = 8 * (blockIdx.z * kWide + warp / kSplit);
-  const bool on = i < c.B * a.G;
-  const int b = on ? i / a.G : 0, h = on ? i - b * a.G : 0;
-  const size_t row = (size_t)b * a.Hq + head * a.G + h;
-  int np = 0, in_tile = 0, rows = 0, tile_req = 0;
-  UnitParts parts = {true, 0, 0, 1, 0};
-  const int4 e = on ? a.rec[b] : make_int4(0, 0, 0, 0);
-  if (e.y > 0) {
-    const int m = e.w / a.nb;
-    const int2 items = *a.shares;
-    parts = UnitParts::of(UnitShares::of(a.n_ctas, items.x, items.y), e.x, e.y, m_tiles_of(e.z, a.nb), head, m);
-    np = parts.count();
-    in_tile = (e.w - m * a.nb) * a.G + h;
-    rows = min(a.nb, e.z - m * a.nb) * a.G;
-    tile_req = b - (e.w - m * a.nb);
-  }
-  const bool whole = parts.whole;
-  auto place = [&](int p) {  // of part p >= 1
-    const int x = parts.planes == 2 ? (p - 1) >> 1 : p - 1, y = parts.planes == 2 ? (p - 1) & 1 : 0;
-    return whole ? whole_part(y, head, tile_req, c, a.G) : cut_part(parts.slot(x), parts.plane + y);
-  };
-  const float *part = whole ? a.rows : a.parts;
-  const float2 *part_ml = whole ? a.rows_ml : a.parts_ml;
-  auto ml_of = [&](int p) {
-    return p == 0 ? make_float2(a.own_lse[row], 1.f) : __ldcg(part_ml + place(p) + in_tile);
-  };
-  float o[8] = {}, ref = -INFINITY, l = 0.f;
-  if (on) {
-#pragma unroll 4
-    for (int p = part0; p <= np; p += kSplit) ref = fmaxf(ref, ml_of(p).x);
-    const float base = ref == -INFINITY ? 0.f : ref;
-    for (int p0 = part0; p0 <= np; p0 += 4 * kSplit) {
-      float v[4][8], f[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int p = p0 + u * kSplit;
-        f[u] = 0.f;
-        if (p > np) continue;
-        const float2 ml = ml_of(p);
-        if (ml.x == -INFINITY && ml.y == ml.y) continue;  // nothing was seen: what the rows hold does not count
-        f[u] = exp2f(ml.x == -INFINITY ? 0.f : ml.x - base);
-        l += f[u] * ml.y;
-        if (p == 0) {
-#pragma unroll
-          for (int y = 0; y < 8; y += 4)
-            *reinterpret_cast<float4 *>(&v[u][y]) = *reinterpret_cast<const float4 *>(a.own + row * D + d0 + y);
-        } else {
-          const float *src = part + place(p) * D + in_tile + (size_t)d0 * rows;
-#pragma unroll
-          for (int y = 0; y < 8; ++y) v[u][y] = __ldcg(src + (size_t)y * rows);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (f[u] != 0.f) {
-#pragma unroll
-          for (int y = 0; y < 8; ++y) o[y] += f[u] * v[u][y];
-        }
-    }
-  }
-  if (kSplit > 1) {
-    s_ref[warp][lane] = ref;
-    s_sum[warp][lane] = l;
-#pragma unroll
-    for (int y = 0; y < 8; ++y) s_o[warp][y][lane] = o[y];
-    __syncthreads();
-    if (part0 > 0) return;
-#pragma unroll
-    for (int x = 1; x < kSplit; ++x) ref = fmaxf(ref, s_ref[warp + x][lane]);
-    const float base = ref == -INFINITY ? 0.f : ref;
-    l = 0.f;
-#pragma unroll
-    for (int y = 0; y < 8; ++y) o[y] = 0.f;
-#pragma unroll
-    for (int x = 0; x < kSplit; ++x) {
-      const float r = s_ref[warp + x][lane], f = exp2f(r == -INFINITY ? 0.f : r - base);
-      l += f * s_sum[warp + x][lane];
-#pragma unroll
-      for (int y = 0; y < 8; ++y) o[y] += f * s_o[warp + x][y][lane];
-    }
-  }
-  if (!on) return;
-  uint32_t z[4];
-#pragma unroll
-  for (int y = 0; y < 8; y += 2) {
-    const float x0 = l == 0.f ? 0.f : __fdividef(o[y], l), x1 = l == 0.f ? 0.f : __fdividef(o[y + 1], l);
-    z[y / 2] = to16<kHalf>(x0) | (uint32_t)to16<kHalf>(x1) << 16;
-  }
-  *reinterpret_cast<uint4 *>(a.out + row * D + d0) = make_uint4(z[0], z[1], z[2], z[3]);
-  if (a.lse && d0 == 0) a.lse[row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -846,17 +721,9 @@ cudaError_t launch_parts(const CUtensorMap &mq, const CUtensorMap &mk, const CUt
   return launch_pdl(paged_prefix_kernel<kHalf, D>, dim3((unsigned)a.n_ctas), dim3(kThreads), smem, stream, mq, mk, mv, c, a);
 }
 
-template <bool kHalf, int D>
-cudaError_t launch_join(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  // eight warps to a row's parts where rows are few and their parts, then, many
-  const unsigned x = (unsigned)((c.B * a.G + 31) / 32), y = (unsigned)c.Hkv;
-  return c.B * a.Hq <= 16 * sms ? launch_pdl(paged_prefix_join<kHalf, D, 8>, dim3(x, y, D / 8), dim3(256), 0, stream, c, a)
-                                : launch_pdl(paged_prefix_join<kHalf, D, 2>, dim3(x, y, D / 32), dim3(256), 0, stream, c, a);
-}
-
 struct Sizes {
-  size_t own_ws, own, own_lse, rec, shares, rows, rows_ml, parts, parts_ml;
-  size_t all() const { return own_ws + own + own_lse + rec + shares + rows + rows_ml + parts + parts_ml; }
+  size_t own_ws, own, own_lse, rec, rows, rows_ml, parts, parts_ml;
+  size_t all() const { return own_ws + own + own_lse + rec + rows + rows_ml + parts + parts_ml; }
 };
 Sizes sizes_of(int B, int Hq, int Hkv, int D) {
   const size_t rows = (size_t)B * Hq, parts = (size_t)2 * kMaxParts * 2 * 128;
@@ -864,8 +731,7 @@ Sizes sizes_of(int B, int Hq, int Hkv, int D) {
   s.own_ws = up256(paged_attention_workspace_bytes(B, Hq, Hkv, D, 1, 0));
   s.own = up256(rows * D * 4);
   s.own_lse = up256(rows * 4);
-  s.rec = up256((size_t)B * 16);
-  s.shares = 256;
+  s.rec = up256((size_t)B * Hkv * sizeof(PartsRec));
   s.rows = 2 * rows * D * 4;
   s.rows_ml = up256(2 * rows * 8);
   s.parts = parts * D * 4;
@@ -905,8 +771,7 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
   };
   a.own = reinterpret_cast<float *>(take(sz.own));
   a.own_lse = reinterpret_cast<float *>(take(sz.own_lse));
-  a.rec = reinterpret_cast<int4 *>(take(sz.rec));
-  a.shares = reinterpret_cast<int2 *>(take(sz.shares));
+  a.rec = reinterpret_cast<PartsRec *>(take(sz.rec));
   a.rows = reinterpret_cast<float *>(take(sz.rows));
   a.rows_ml = reinterpret_cast<float2 *>(take(sz.rows_ml));
   a.parts = reinterpret_cast<float *>(take(sz.parts));
@@ -928,9 +793,7 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
   const bool wide = c.D == 128;
   cudaError_t e = half ? (wide ? launch_parts<true, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<true, 64>(mq, mk, mv, dev, c, a, stream))
                        : (wide ? launch_parts<false, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<false, 64>(mq, mk, mv, dev, c, a, stream));
-  if (e == cudaSuccess)
-    e = half ? (wide ? launch_join<true, 128>(sms, c, a, stream) : launch_join<true, 64>(sms, c, a, stream))
-             : (wide ? launch_join<false, 128>(sms, c, a, stream) : launch_join<false, 64>(sms, c, a, stream));
+  if (e == cudaSuccess) e = launch_prefix_join(half, sms, c, a, stream);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? BASTION_OK : BASTION_ERR_LAUNCH;
 }
 

@@ -1,0 +1,51 @@
+// What the two launches of shared-prefix attention share.
+#pragma once
+
+#include "paged.cuh"
+#include "paged_units.cuh"
+
+namespace bastion {
+
+// Where the join finds the parts of a request's rows of one KV head.  Part p is of
+// CTA x = p / planes, plane p % planes: at place0 + plane * step for x = 0 and at
+// place1 + (x - 1) * 512 + plane * step for the others (a CTA has two slots of two
+// planes of 128 rows).
+struct alignas(16) PartsRec {
+  int32_t parts, two;  // how many, and whether of two planes
+  int32_t place0, place1, step;
+  int32_t whole;       // in rows, not in parts
+  int32_t rows, first; // rows of the M tile and the request's first among them
+};
+
+struct PrefixArgs {
+  const int32_t *table, *len, *start;  // the groups' prefixes
+  int n_groups, max_pages, cap;
+  int Hq, G, nb;  // nb = 128 / G requests an M tile
+  float scale_log2;
+  int swap;
+  PartsRec *rec;   // [B, Hkv]
+  float *own;      // [B, Hq, D], normalised
+  float *own_lse;  // [B, Hq], base 2
+  float *rows;     // [2][B, Hq, D]: units of one CTA
+  float2 *rows_ml;
+  float *parts;    // [2 kMaxParts][2][128][D]: units of several
+  float2 *parts_ml;
+  int n_ctas;
+  uint16_t *out;
+  float *lse;
+  int32_t *status;
+};
+
+// --------------------------------------------------------------------------- parts
+
+// An M tile's part is its R rows, four elements of each side by side: element d of
+// row i at place * D + (d / 4 * R + i) * 4 + d % 4, so that a warp of rows writes,
+// and the join reads, whole sectors; reference and sum at place + i.
+__device__ __forceinline__ size_t whole_part(int plane, int head, int req, const Paged &c, int G) {
+  return (((size_t)plane * c.Hkv + head) * c.B + req) * G;
+}
+__device__ __forceinline__ size_t cut_part(int slot, int plane) { return ((size_t)slot * 2 + plane) * 128; }
+
+cudaError_t launch_prefix_join(bool half, int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream);
+
+}  // namespace bastion

@@ -290,3 +290,26 @@ def test_agrees_with_plain_paged_attention(cuda_lib):
     torch.cuda.synchronize()
     assert float((p.lse - lse).abs().max()) < 1e-5
     assert float((p.out.float() - out.float()).abs().max()) <= 2 ** -7 * float(out.float().abs().max())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (8, 1, 64), (12, 1, 128), (3, 1, 64)])
+@pytest.mark.parametrize("own", [900, 1008, 1009, 1025, 3000])
+def test_short_and_long_own_slots(cuda_lib, Hq, Hkv, D, own):
+    """On both sides of the size up to which the join attends to the own slots itself."""
+    lens = [own, 0, 1, own // 2, 129, own - 1, 64]
+    for dtype in (BF, HF):
+        Prefix([300, 1500], [3, 3], lens, Hq, Hkv, D, 16, "head", dtype, seed=own + Hq, poison=math.nan).run().check()
+
+
+def test_long_own_slots_in_graphs_and_in_place(cuda_lib):
+    a = Prefix([2000], [30], [50 * r for r in range(30)], 8, 2, seed=31)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.run()
+    a.q.normal_()
+    for _ in range(3):
+        g.replay()
+    a.check()
+    q = a.q.clone()
+    a.out = a.q
+    a.run().check(q)
