@@ -27,7 +27,7 @@ SOURCES = ["api.cu", "topk_marginals.cu", "build_tree.cu", "verify_greedy.cu", "
            "verify_noalloc.cu", "verify_sample.cu", "calibrate.cu",
            "build_tree_mixture.cu", "lm_head_topk.cu",
            "api_cache.cu", "paged_append.cu", "paged_attention.cu", "paged_evict.cu",
-           "paged_plan.cu", "qk_norm_rope.cu", "paged_prefix.cu", "paged_prefix_join.cu"]
+           "paged_plan.cu", "qk_norm_rope.cu", "paged_prefix.cu", "paged_prefix_join.cu", "paged_prefix_own.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -3,9 +3,10 @@
 //
 //   out = (sum_prefix exp(s_j) v_j + sum_own exp(s_j) v_j) / (sum_prefix exp(s_j) + sum_own exp(s_j))
 //
-// Three launches: the own slots, by the one-token kernel of paged_attention.cu, in
-// 32 bits; the prefixes, which begin on the SMs that the own slots leave free; and
-// the join of each row's parts (paged_prefix_join.cu).
+// Three launches: the own slots, in 32 bits, by the one-token kernel of
+// paged_attention.cu or, where they are few, by paged_prefix_own.cu; the prefixes,
+// which begin on the SMs that the own slots leave free; and the join of each row's
+// parts (paged_prefix_join.cu).
 //
 // The prefixes.  A group's n requests are n * G query rows of a KV head, which
 // read each key and value once per 256 rows: 512 flops a byte at 256 rows of
@@ -788,8 +789,15 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return BASTION_ERR_LAUNCH;
   a.n_ctas = sms < kMaxParts ? sms : kMaxParts;
-  const int rc = launch_paged_attention32(c, half, q, Hq, q_st_b, seq_len, scale, a.own, a.own_lse, ws, status, stream);
-  if (rc != BASTION_OK) return rc;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_st_b = q_st_b;
+  a.seq_len = seq_len;
+  if (c.cap <= own_slots(c.D)) {
+    if (launch_prefix_own(half, c, a, stream) != cudaSuccess) return BASTION_ERR_LAUNCH;
+  } else {
+    const int rc = launch_paged_attention32(c, half, q, Hq, q_st_b, seq_len, scale, a.own, a.own_lse, ws, status, stream);
+    if (rc != BASTION_OK) return rc;
+  }
   const bool wide = c.D == 128;
   cudaError_t e = half ? (wide ? launch_parts<true, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<true, 64>(mq, mk, mv, dev, c, a, stream))
                        : (wide ? launch_parts<false, 128>(mq, mk, mv, dev, c, a, stream) : launch_parts<false, 64>(mq, mk, mv, dev, c, a, stream));
