@@ -72,7 +72,8 @@ struct Misc {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], mma_done;  // p_full: of a warpgroup's upper, lower keys
   int2 warp_sum[kThreads / 32];
   int warp_max[kThreads / 32];
-  int li0, off0, f0, f1, groups;
+  int li0, f0, f1;
+  TilePlace from;
   uint32_t tmem;
   int abort;
 };
@@ -343,13 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
-        const int off = entry_boundary(f - at, tiles_of(len[i]), m_tiles_of(n_req[i], a.nb));
+        const TilePlace p = TilePlace::boundary(f - at, tiles_of(len[i]), m_tiles_of(n_req[i], a.nb));
         if (k) {
-          ms.f1 = at + off;
+          ms.f1 = at + p.off;
         } else {
-          ms.f0 = at + off;
-          ms.li0 = off == items[i] ? rank + 1 : rank;  // the next group's begin
-          ms.off0 = off == items[i] ? 0 : off;
+          const bool next = p.off == items[i];  // the next group's begin
+          ms.f0 = at + p.off;
+          ms.li0 = next ? rank + 1 : rank;
+          ms.from = next ? TilePlace{0, 0, 0, 0} : p;
         }
       }
     }
@@ -357,10 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     at = end;
   }
   __syncthreads();
-  const int share = __shfl_sync(kFull, busy ? ms.f1 - ms.f0 : 0, 0), li0 = __shfl_sync(kFull, ms.li0, 0),
-            off0 = __shfl_sync(kFull, ms.off0, 0);
+  const int share = __shfl_sync(kFull, busy ? ms.f1 - ms.f0 : 0, 0), li0 = __shfl_sync(kFull, ms.li0, 0);
+  const TilePlace from_here = {__shfl_sync(kFull, ms.from.head, 0), __shfl_sync(kFull, ms.from.pair, 0),
+                               __shfl_sync(kFull, ms.from.t, 0), 0};
   Units<true> w;
-  w.start(list, li0, off0, share, a.nb);
+  w.start(list, li0, from_here, share, a.nb);
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ TMA: warp 0 keys, warp 2 values
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // reads' latency never holds up the copies.  Lane: page lane % ppt of the batch's tile lane / ppt.
     const int psh = 7 - c.shift, ppt = 1 << psh, batch = min(kBatch, 32 >> psh);
     Units<false> lw;  // this lane's tile
-    lw.start(list, li0, off0, share, a.nb);
+    lw.start(list, li0, from_here, share, a.nb);
     int lead = lane >> psh;
     auto next_entry = [&]() {  // walks on by `lead` tiles and reads there
 #pragma unroll 1
@@ -401,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         in_batch = 0;
       }
       const int x = 2 * issued + odd, slot = x % kStages;
+      // the first keys alone at first: all SMs fill their rings at once, and products begin 1 us sooner
+      if (x == 1 || x == 2) wait_bar(&ms.full[0], 0, abort, &a.status[w.req]);
       if (!__all_sync(kFull, wait_bar(&ms.empty[slot], ((uint32_t)(x / kStages) & 1u) ^ 1u, abort, &a.status[w.req]))) break;
       const int np = (min(kTileKeys, w.len - w.t * kTileKeys) + c.page - 1) >> c.shift;
       if (one) mbar_arrive_expect_tx(&ms.full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
@@ -793,7 +798,7 @@ int launch_paged_prefix(const Paged &c, bool half, const int32_t *prefix_table, 
   a.q_st_b = q_st_b;
   a.seq_len = seq_len;
   if (c.cap <= own_slots(c.D)) {
-    if (launch_prefix_own(half, c, a, stream) != cudaSuccess) return BASTION_ERR_LAUNCH;
+    if (launch_prefix_own(half, sms, c, a, stream) != cudaSuccess) return BASTION_ERR_LAUNCH;
   } else {
     const int rc = launch_paged_attention32(c, half, q, Hq, q_st_b, seq_len, scale, a.own, a.own_lse, ws, status, stream);
     if (rc != BASTION_OK) return rc;

@@ -8,10 +8,10 @@ namespace bastion {
 
 // Own slots in tables of at most this many slots go to paged_prefix_own.cu, others to
 // the one-token kernel.  Whole calls behind 2,000 shared tokens, 32/8 heads, one way
-// and the other: D = 64, 64 requests: 32 slots 19.8 and 28.2 us, 512 31.4 and 40.1; one
-// request: 256 slots 14.3 and 15.0, 512 17.7 and 16.4, 1,000 25.8 and 19.4.  D = 128, whose
-// outputs take twice the registers, so that half as many warps are on an SM: 32 slots,
-// 64 requests 28.0 and 31.7, 200 47.2 and 48.5; 128 slots 33.3 and 34.3, 64.5 and 51.3.
+// and the other: D = 64, 8 requests: 16 slots 15.0 and 19.9 us, 256 20.0 and 22.7, 512 23.7 and
+// 23.9; 256 requests: 512 slots 73.8 and 83.0.  D = 128, whose outputs take twice the registers,
+// so that half as many warps are on an SM: 8 requests: 64 slots 17.0 and 21.7, 128 20.5 and
+// 21.9; 256 requests: 64 slots 53.0 and 58.0, 128 70.5 and 60.0.
 __host__ __device__ constexpr int own_slots(int D) { return D == 64 ? 512 : 64; }
 
 // Where the join finds the parts of a request's rows of one KV head.  Part p is of
@@ -57,7 +57,7 @@ __device__ __forceinline__ size_t whole_part(int plane, int head, int req, const
 }
 __device__ __forceinline__ size_t cut_part(int slot, int plane) { return ((size_t)slot * 2 + plane) * 128; }
 
-cudaError_t launch_prefix_own(bool half, const Paged &c, const PrefixArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix_own(bool half, int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream);
 cudaError_t launch_prefix_join(bool half, int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream);
 
 }  // namespace bastion

@@ -4,8 +4,8 @@
 //
 // Behind a long prefix the own slots are few, and what the one-token kernel does for
 // long rows (persistent CTAs, rings of 128-key tiles, parts) costs it 2 us a request
-// and KV head.  Here one CTA of four warps takes a request and KV head, and enough of
-// them are on an SM to keep HBM busy.  A tile of the tensor cores' asynchronous
+// and KV head.  Here a warp, or a CTA of four, takes a request and KV head (a unit), and
+// enough of them are on an SM to hide one another's latency.  A tile of the tensor cores' asynchronous
 // instructions (128 rows or keys) would be nearly empty, and its chain of copy, product,
 // softmax, product is latency that a few keys cannot hide: a warp takes 16 keys at a time
 // from global memory straight into the fragments of synchronous products, m16n8k16,
@@ -39,17 +39,21 @@ __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool kHalf, int D>
+template <bool kHalf, int D, int kShare>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Paged c, PrefixArgs a) {
   constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias: a low term ends at 2^-24
   constexpr int kQk = D / 32, kPv = D / 64;     // 16-byte pieces of a key, of a value row, that a thread has
-  __shared__ int s_page[own_slots(D) / 8];
-  __shared__ float2 s_ml[kWarps][16];
-  __shared__ __align__(16) float s_o[kWarps][16][D];
+  __shared__ int s_pages[kWarps / kShare][own_slots(D) / 8];
+  __shared__ float2 s_ml[kShare == 1 ? 1 : kWarps][16];
+  __shared__ __align__(16) float s_o[kShare == 1 ? 1 : kWarps][16][D];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.x / c.Hkv, head = blockIdx.x - b * c.Hkv;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = (threadIdx.x >> 5) % kShare, tid = threadIdx.x % (32 * kShare);  // of the unit's
+  const int place = threadIdx.x / (32 * kShare), unit = blockIdx.x * (kWarps / kShare) + place;
+  if (unit >= c.B * c.Hkv) return;  // with kShare == 1 only, where warps do not wait for one another
+  const int b = unit / c.Hkv, head = unit - b * c.Hkv;
+  int *s_page = s_pages[place];
   const int n_raw = a.seq_len[b], n = min(max(n_raw, 0), c.cap);
   if (tid == 0 && head == 0 && n != n_raw) atomicOr(&a.status[b], BASTION_STATUS_KV_OVERFLOW);
   // rows g and g + 8 of Q; k step 2 i + e: words 2 e and 2 e + 1 of piece i
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
       if (g + 8 * r < a.G)
         q[r][i] = *reinterpret_cast<const uint4 *>(a.q + b * a.q_st_b + ((int64_t)head * a.G + g + 8 * r) * D + i * 32 + t * 8);
     }
-  for (int i = tid; (i << c.shift) < n; i += kThreads) {
+  for (int i = tid; (i << c.shift) < n; i += 32 * kShare) {
     int p = c.table[(size_t)b * c.max_pages + i];
     if (p < 0 || p >= c.n_pages) {  // no page of the pool: page 0 stands in
       atomicOr(&a.status[b], BASTION_STATUS_BAD_PAGE);
@@ -72,9 +76,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
   }
   float o[kPv * 8][4] = {};  // [piece][element]: rows g (0, 1) and g + 8 (2, 3), columns 2 t and 2 t + 1
   float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  __syncthreads();
+  if (kShare == 1) __syncwarp(); else __syncthreads();
 #pragma unroll 1
-  for (int j0 = warp * kTurn; j0 < n; j0 += kWarps * kTurn) {
+  for (int j0 = warp * kTurn; j0 < n; j0 += kShare * kTurn) {
     uint4 kk[2][kQk], vv[4][kPv];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -158,6 +162,25 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(kFull, l[r], 1);
     l[r] += __shfl_xor_sync(kFull, l[r], 2);
+    if (kShare == 1) {  // the row is whole
+      if (g + 8 * r < a.G) {
+        const size_t row = (size_t)b * a.Hq + (size_t)head * a.G + g + 8 * r;
+        const float inv = l[r] == 0.f ? 0.f : __fdividef(1.f, l[r]);  // no key with a score above -inf: 0
+#pragma unroll
+        for (int i = 0; i < kPv; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              const int k = 2 * r + y;
+              float4 x = make_float4(o[i * 8 + e][k], o[i * 8 + e + 1][k], o[i * 8 + e + 2][k], o[i * 8 + e + 3][k]);
+              x = l[r] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+              *reinterpret_cast<float4 *>(a.own + row * D + i * 64 + (2 * t + y) * 8 + e) = x;
+            }
+        if (t == 0) a.own_lse[row] = l[r] == 0.f ? -INFINITY : ref[r] + log2f(l[r]);
+      }
+      continue;
+    }
     if (t == 0) s_ml[warp][g + 8 * r] = make_float2(ref[r], l[r]);
     // column 2 t + y of piece i, element e: element i * 64 + (2 t + y) * 8 + e of the head
     if (g + 8 * r < a.G) {
@@ -173,15 +196,16 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
           }
     }
   }
+  if (kShare == 1) return;
   __syncthreads();
   for (int i = tid; i < a.G * (D / 4); i += kThreads) {
     const int h = i / (D / 4), quad = i - h * (D / 4);
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][h].x);
+    for (int w = 0; w < kShare; ++w) top = fmaxf(top, s_ml[w][h].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kShare; ++w) {
       const float2 ml = s_ml[w][h];
       // a warp without a finite score: nothing, or NaN
       const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
@@ -198,16 +222,20 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
 }
 
 template <bool kHalf, int D>
-cudaError_t launch(const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  const dim3 grid((unsigned)(c.B * c.Hkv));
-  return launch_pdl(paged_prefix_own<kHalf, D>, grid, dim3(kThreads), 0, stream, c, a);
+cudaError_t launch(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
+  // A warp a unit where keys are few or units many (256 slots and requests, 32/8 heads of 64: 49.8 us for 54.6 with four;
+  // 16 slots, 150 requests: 22.9 for 27.0), else four (256 slots, 64 requests: 25.3 us for 35.7 with one).
+  const int units = c.B * c.Hkv;
+  if (c.cap <= 64 || units >= 12 * sms)
+    return launch_pdl(paged_prefix_own<kHalf, D, 1>, dim3((unsigned)((units + kWarps - 1) / kWarps)), dim3(kThreads), 0, stream, c, a);
+  return launch_pdl(paged_prefix_own<kHalf, D, kWarps>, dim3((unsigned)units), dim3(kThreads), 0, stream, c, a);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix_own(bool half, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  if (half) return c.D == 128 ? launch<true, 128>(c, a, stream) : launch<true, 64>(c, a, stream);
-  return c.D == 128 ? launch<false, 128>(c, a, stream) : launch<false, 64>(c, a, stream);
+cudaError_t launch_prefix_own(bool half, int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
+  if (half) return c.D == 128 ? launch<true, 128>(sms, c, a, stream) : launch<true, 64>(sms, c, a, stream);
+  return c.D == 128 ? launch<false, 128>(sms, c, a, stream) : launch<false, 64>(sms, c, a, stream);
 }
 
 }  // namespace bastion

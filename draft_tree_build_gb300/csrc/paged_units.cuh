@@ -32,7 +32,7 @@ struct UnitShares {
   // widest: the items of the heaviest tile, so that no two boundaries fall into one tile
   static __host__ __device__ __forceinline__ UnitShares of(int ctas, int total, int widest) {
     UnitShares s;
-    s.n = total == 0 ? 0 : imin(ctas, total / widest > 0 ? total / widest : 1);
+    s.n = total == 0 ? 0 : imin(ctas, total >= widest ? total >> (widest - 1) : 1);
     s.quot = s.n > 0 ? total / s.n : 0;
     s.big = total - s.quot * s.n;
     return s;
@@ -45,12 +45,36 @@ struct UnitShares {
   // The tile that a boundary `off` items into a unit moves to.
   static __host__ __device__ __forceinline__ int moved(int off, int tiles, int weight) {
     if (tiles <= kWhole) return 2 * off <= tiles * weight ? 0 : tiles;
-    const int t = off / weight;
+    const int t = off >> (weight - 1);
     return t <= kSnap ? 0 : tiles - t <= kSnap ? tiles : t;
   }
   // The CTAs of a unit of more than kWhole tiles, items [u0, u1): those with its first and its last tile.
   __host__ __device__ __forceinline__ int first_cta(int u0, int weight) const { return owner(u0 + (kSnap + 1) * weight - 1); }
   __host__ __device__ __forceinline__ int last_cta(int u1, int weight) const { return owner(u1 - kSnap * weight - 1); }
+};
+
+// A tile of an entry, `off` items into it.
+struct TilePlace {
+  int head, pair, t, off;
+  // Where a boundary `off` items into the entry falls.
+  static __host__ __device__ __forceinline__ TilePlace boundary(int off, int tiles, int m_tiles) {
+    const int per_head = tiles * m_tiles;
+    TilePlace p;
+    p.head = off / per_head;
+    const int rest = off - p.head * per_head;
+    p.pair = rest / (2 * tiles);
+    const int weight = imin(2, m_tiles - 2 * p.pair);
+    p.t = UnitShares::moved(rest - p.pair * 2 * tiles, tiles, weight);
+    p.off = p.head * per_head + p.pair * 2 * tiles + weight * p.t;
+    if (p.t == tiles) {  // the next unit's begin
+      p.t = 0;
+      if (2 * ++p.pair >= m_tiles) {
+        p.pair = 0;
+        ++p.head;
+      }
+    }
+    return p;
+  }
 };
 
 // A CTA's tiles, one after the other.  kUniform: all lanes of a warp walk together,
@@ -77,20 +101,16 @@ struct Units {
     m_tiles = m_tiles_of(n, nb);
   }
   __host__ __device__ __forceinline__ int ms() const { return imin(2, m_tiles - 2 * pair); }  // M tiles of the unit
-  // Entry `index`, `off` items into it (a tile's begin), `count` items in all.
-  __host__ __device__ __forceinline__ void start(const UnitEntry *l, int index, int off, int count, int nb) {
+  // From that tile of entry `index` on, `count` items in all.
+  __host__ __device__ __forceinline__ void start(const UnitEntry *l, int index, TilePlace from, int count, int nb) {
     list = l;
     li = index;
     left = count;
     first = true;
-    if (left > 0) {
-      load(nb);
-      const int per_head = tiles * m_tiles;
-      head = off / per_head;
-      off -= head * per_head;
-      pair = off / (2 * tiles);
-      t = (off - pair * 2 * tiles) / ms();
-    }
+    head = from.head;
+    pair = from.pair;
+    t = from.t;
+    if (left > 0) load(nb);
   }
   __host__ __device__ __forceinline__ void step(int heads, int nb) {
     first = false;
@@ -110,13 +130,6 @@ struct Units {
   }
   __host__ __device__ __forceinline__ bool last() const { return t == tiles - 1 || left == ms(); }
 };
-
-// Where boundary `off` items into an entry falls: items into the entry, tiles whole.
-__host__ __device__ __forceinline__ int entry_boundary(int off, int tiles, int m_tiles) {
-  const int per_head = tiles * m_tiles, h = off / per_head, rest = off - h * per_head, pair = rest / (2 * tiles);
-  const int weight = imin(2, m_tiles - 2 * pair);
-  return h * per_head + pair * 2 * tiles + weight * UnitShares::moved(rest - pair * 2 * tiles, tiles, weight);
-}
 
 // A unit's parts as the join sees them.  Each of its CTAs leaves one for every M
 // tile, or two for a unit of one M tile, whose key tiles the two warpgroups take

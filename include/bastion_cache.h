@@ -1,6 +1,8 @@
 /*
  * bastion_cache.h -- the paged key-value cache of the target model: append,
- * one-token attention and eviction by accumulated attention weight.
+ * one-token attention, eviction by accumulated attention weight, and what a step
+ * of a layer needs around them: pages and slots for new tokens, norm and rotation
+ * of queries and keys on their way into the cache, attention over shared prefixes.
  *
  * What bastion_tree_attention does for a drafted tree, these calls do for the
  * steps around it: the accepted path of a verified tree enters the cache
@@ -22,8 +24,8 @@
  * [B, L_cap, Hkv, D] whose L_cap is a multiple of page_size is such a pool
  * with page_table[r][i] = r * L_cap / page_size + i: the same memory serves
  * bastion_tree_attention.
- * One workspace that is large enough for each may serve all three calls, at
- * all sizes, one after the other.  A workspace that a call with
+ * One workspace that is large enough for each may serve all calls, at all
+ * sizes, one after the other.  A workspace that a call with
  * BASTION_STATUS_TIMEOUT has used is cleared before its next use.
  * Page table entries past a request's last used page are not read.  Slots at
  * or past seq_len[r] never affect a result (they may hold NaN) and are left as
@@ -250,19 +252,21 @@ int bastion_paged_plan(int32_t *page_table, int B, int max_pages, int page_size,
  * inv_freq      [rot_dim / 2] double (8-byte aligned), finite; scaled for a long
  *               context by the caller.  rot_dim a multiple of 16 in [0, D]; 0:
  *               nothing is turned, inv_freq may be NULL.
- * q_out, k_out  as q and k, or NULL: not written.  q_out may be q, k_out k, with
- *               the same strides; otherwise they lie apart from every input (not
- *               checked row by row: BASTION_ERR_UNSUPPORTED where the spans of
- *               two arrays overlap that are not slices of the same tokens' rows).
+ * q_out, k_out  as q and k (tokens' rows not overlapping), or NULL: not written.
+ *               q_out may be q, k_out k, with the same strides; otherwise they lie
+ *               apart from one another and from every input, as whole arrays or as
+ *               slices of tokens' rows of one stride (BASTION_ERR_UNSUPPORTED
+ *               otherwise).
  * cache, slots  NULL, or the cache and [T] int64: the token's key and value go to
  *               slot slots[t] (as bastion_paged_plan gives it); a negative slot
  *               stores nothing, one past the pools sets BASTION_STATUS_BAD_PAGE.
  *               A slot listed twice holds one of the two rows' values in each of
  *               its 16-byte pieces.  The cache's B, page_table and max_pages are
- *               checked and not used; its pools lie apart from the inputs.
+ *               checked and not used; its pools lie apart from the other arrays.
  * status        [1] int32.
  * Limits: D = 64 or 128 (BASTION_ERR_UNSUPPORTED); T, Hq, Hkv >= 1, Hq + 2 Hkv
- * <= 65535, T * (Hq + 2 Hkv) < 2^31; factor finite.  One launch.
+ * <= 65535, T * (Hq + 2 Hkv) < 2^31; factor finite.  One launch.  Serving only:
+ * the library trains nothing, and has no backward passes.
  */
 int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t,
                          int64_t q_st_h, const void *k, int64_t k_st_t, int64_t k_st_h,
@@ -299,7 +303,8 @@ int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q
  * Weights enter the products as there: as two 16-bit terms.  Results do not
  * depend on the order in which the parts of a split prefix finish.
  * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
- * n_groups) bytes.
+ * n_groups) bytes, about 16 bytes an element of q and 58 MB.  Three launches: own
+ * slots, prefixes, join.
  */
 size_t bastion_paged_prefix_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups);
 int bastion_paged_prefix_attention(const bastion_paged_cache *cache, const int32_t *prefix_table,

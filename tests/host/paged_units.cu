@@ -34,31 +34,32 @@ int main() {
       list.push_back(u);
     }
     const UnitShares sh = UnitShares::of(grid, total, widest);
-    auto boundary = [&](int cta, int &li, int &off) {  // where CTA cta's share begins
+    auto boundary = [&](int cta, int &li, TilePlace &from) {  // where CTA cta's share begins
       const int f = sh.begin(cta);
       li = (int)list.size();
-      off = 0;
+      from = TilePlace{0, 0, 0, 0};
       if (f == total) return f;
       li = 0;
       while (li + 1 < (int)list.size() && list[li + 1].at <= f) ++li;
       const int tiles = tiles_of(list[li].len), m = m_tiles_of(list[li].n, nb);
-      off = entry_boundary(f - list[li].at, tiles, m);
-      const int to = list[li].at + off;
-      if (off == tiles * m * heads) {
+      from = TilePlace::boundary(f - list[li].at, tiles, m);
+      const int to = list[li].at + from.off;
+      if (from.off == tiles * m * heads) {
         ++li;
-        off = 0;
+        from = TilePlace{0, 0, 0, 0};
       }
       return to;
     };
     using Key = std::tuple<int, int, int, int>;  // whole: plane, entry, head, M tile; else -1, slot, plane, 0
     std::map<Key, std::vector<int>> parts;       // the key tiles in it
     for (int cta = 0; cta < sh.n; ++cta) {
-      int li, off, li1, off1;
-      const int f0 = boundary(cta, li, off), f1 = boundary(cta + 1, li1, off1);
+      int li, li1;
+      TilePlace from, to;
+      const int f0 = boundary(cta, li, from), f1 = boundary(cta + 1, li1, to);
       if (f1 < f0) return printf("trial %d: CTA %d ends before it begins\n", trial, cta), 1;
       empty_shares += f1 == f0;
       Units<false> w;
-      w.start(list.data(), li, off, f1 - f0, nb);
+      w.start(list.data(), li, from, f1 - f0, nb);
       int t0 = 0, place = 0, segments = 0;
       std::map<int, std::vector<int>> open;  // plane -> tiles
       for (; w.left > 0; w.step(heads, nb)) {

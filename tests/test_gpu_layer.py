@@ -209,3 +209,39 @@ def test_the_cache_refuses(cuda_lib):
     slots, pos = c.reserve(2, stream=s)
     s.synchronize()
     assert pos.tolist() == [0, 1, 0, 1] and math.prod(slots.shape) == 4
+
+
+def test_one_workspace_serves_all_calls(cuda_lib):
+    """Plan, append, one-token attention, eviction and shared-prefix attention in turn on one workspace, in two orders."""
+    from draft_tree_build_gb300 import bastion
+    from test_gpu_paged import Case
+    from test_gpu_plan import EDGES, Plan
+    from test_gpu_prefix import Prefix
+    long_own, short_own = Prefix([9000, 40], [9, 30], [100] * 39, 8, 2, seed=1), Prefix([700], [5], [9] * 5, 8, 2, 64, seed=2)
+    plan, att = Plan(EDGES, 17), Case([5000, 20, 300], 8, 2, weights=True, seed=3)
+    ws = max((x.ws for x in (long_own, short_own, plan, att)), key=lambda t: t.numel())
+    ws = bastion.workspace(ws.numel(), dev())
+    plan.ws = ws
+    for turn in range(6):
+        calls = [lambda: long_own.run(ws), plan.run, lambda: att.run(ws), lambda: short_own.run(ws)]
+        for f in calls if turn % 2 else calls[::-1]:
+            f()
+        torch.cuda.synchronize()
+        for x in (long_own, short_own, att):
+            x.check()
+            x.out.fill_(7.0)
+        want = ref.plan(plan.table, stack=plan.stack, **plan.args)
+        assert plan.slots.tolist() == want["slots"] and plan.t["table"].tolist() == want["table"]
+        plan.slots.fill_(77)
+
+
+def test_many_calls_of_large_batches_agree(cuda_lib):
+    """Tiles overwritten while they are read would show as differences between calls: 1,024 rows a KV head, all SMs busy."""
+    from test_gpu_prefix import Prefix
+    p = Prefix([20000], [128], [32] * 128, 16, 2, 128, 64, "slot", seed=7)
+    p.run().check()
+    out, lse = p.out.clone(), p.lse.clone()
+    for i in range(50):
+        p.out.zero_()
+        p.run()
+        assert torch.equal(p.out, out) and torch.equal(p.lse, lse), i
