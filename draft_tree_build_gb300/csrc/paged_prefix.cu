@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {  // the share's begin and end
         const int f = k ? b1 : b0;
         if (f < at || f >= end) continue;
-        const TilePlace p = TilePlace::boundary(f - at, tiles_of(len[i]), m_tiles_of(n_req[i], a.nb));
+        const TilePlace p = TilePlace::boundary(sh, f - at, tiles_of(len[i]), m_tiles_of(n_req[i], a.nb));
         if (k) {
           ms.f1 = at + p.off;
         } else {

@@ -303,7 +303,7 @@ int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q
  * Weights enter the products as there: as two 16-bit terms.  Results do not
  * depend on the order in which the parts of a split prefix finish.
  * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
- * n_groups) bytes, about 16 bytes an element of q and 58 MB.  Three launches: own
+ * n_groups) bytes, about 12 bytes an element of q and 55 MB.  Three launches: own
  * slots, prefixes, join.
  */
 size_t bastion_paged_prefix_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups);

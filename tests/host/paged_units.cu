@@ -16,7 +16,7 @@ using namespace bastion;
 int main() {
   std::mt19937 rng(1);
   auto pick = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
-  long cut = 0, whole_units = 0, empty_shares = 0;
+  long cut = 0, whole_units = 0, fine = 0;
   for (int trial = 0; trial < 6000; ++trial) {
     const int heads = pick(1, 4), grid = pick(1, 40), nb = pick(1, 9), longest = pick(0, 3) ? 1200 : 9000;
     const bool single = pick(0, 3) == 0;
@@ -34,6 +34,7 @@ int main() {
       list.push_back(u);
     }
     const UnitShares sh = UnitShares::of(grid, total, widest);
+    fine += sh.fine;
     auto boundary = [&](int cta, int &li, TilePlace &from) {  // where CTA cta's share begins
       const int f = sh.begin(cta);
       li = (int)list.size();
@@ -42,7 +43,7 @@ int main() {
       li = 0;
       while (li + 1 < (int)list.size() && list[li + 1].at <= f) ++li;
       const int tiles = tiles_of(list[li].len), m = m_tiles_of(list[li].n, nb);
-      from = TilePlace::boundary(f - list[li].at, tiles, m);
+      from = TilePlace::boundary(sh, f - list[li].at, tiles, m);
       const int to = list[li].at + from.off;
       if (from.off == tiles * m * heads) {
         ++li;
@@ -57,7 +58,6 @@ int main() {
       TilePlace from, to;
       const int f0 = boundary(cta, li, from), f1 = boundary(cta + 1, li1, to);
       if (f1 < f0) return printf("trial %d: CTA %d ends before it begins\n", trial, cta), 1;
-      empty_shares += f1 == f0;
       Units<false> w;
       w.start(list.data(), li, from, f1 - f0, nb);
       int t0 = 0, place = 0, segments = 0;
@@ -109,6 +109,7 @@ int main() {
           if (p.count() > 2 * grid) return printf("trial %d: too many parts\n", trial), 1;
         }
   }
-  if (cut < 5000 || whole_units < 5000 || empty_shares < 100) return printf("%ld %ld %ld\n", cut, whole_units, empty_shares), 1;
+  if (cut < 5000 || whole_units < 5000 || fine < 300)
+    return printf("%ld %ld %ld\n", cut, whole_units, fine), 1;
   return 0;
 }
