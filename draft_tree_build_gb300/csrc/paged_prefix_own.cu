@@ -4,7 +4,7 @@
 //
 // Behind a long prefix the own slots are few, and what the one-token kernel does for
 // long rows (persistent CTAs, rings of 128-key tiles, parts) costs it 2 us a request
-// and KV head.  Here a warp, or a CTA of four, takes a request and KV head (a unit), and
+// and KV head.  Here a warp, or a CTA of four or eight, takes a request and KV head (a unit), and
 // enough of them are on an SM to hide one another's latency.  A tile of the tensor cores' asynchronous
 // instructions (128 rows or keys) would be nearly empty, and its chain of copy, product,
 // softmax, product is latency that a few keys cannot hide: a warp takes 16 keys at a time
@@ -23,7 +23,7 @@ namespace bastion {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int warps_of(int share) { return share > 4 ? share : 4; }  // of a CTA
 constexpr int kTurn = 16;  // keys of a warp's turn
 
 // D (16 x 8, 32 bits) += A (16 x 16) B (16 x 8), 16-bit A and B.
@@ -39,8 +39,8 @@ __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool kHalf, int D, int kShare>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Paged c, PrefixArgs a) {
+template <bool kHalf, int D, int kShare, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (D == 64 ? 16 : 8) / kWarps) paged_prefix_own(Paged c, PrefixArgs a) {
   constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias: a low term ends at 2^-24
   constexpr int kQk = D / 32, kPv = D / 64;     // 16-byte pieces of a key, of a value row, that a thread has
   __shared__ int s_pages[kWarps / kShare][own_slots(D) / 8];
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
   }
   if (kShare == 1) return;
   __syncthreads();
-  for (int i = tid; i < a.G * (D / 4); i += kThreads) {
+  for (int i = tid; i < a.G * (D / 4); i += 32 * kShare) {
     const int h = i / (D / 4), quad = i - h * (D / 4);
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -221,21 +221,29 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) paged_prefix_own(Pa
   }
 }
 
-template <bool kHalf, int D>
+template <bool kHalf, int D, int kShare>
+cudaError_t launch_share(const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
+  constexpr int kWarps = warps_of(kShare), kUnits = kWarps / kShare;
+  return launch_pdl(paged_prefix_own<kHalf, D, kShare, kWarps>, dim3((unsigned)((c.B * c.Hkv + kUnits - 1) / kUnits)),
+                    dim3(32 * kWarps), 0, stream, c, a);
+}
+
+// Warps of a unit: one where keys are few (16 slots, 150 requests of 32/8 heads of 64: 22.9 us for 27.0 with four) or
+// units many (256 slots, 256 requests: 49.8 for 54.6); eight where the units are one wave (512 slots, 8 requests: 20.5 for
+// 23.6); else four (256 slots, 64 requests: 25.3 for 35.7 with one, 33.6 with eight).
+template <bool kHalf>
 cudaError_t launch(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  // A warp a unit where keys are few or units many (256 slots and requests, 32/8 heads of 64: 49.8 us for 54.6 with four;
-  // 16 slots, 150 requests: 22.9 for 27.0), else four (256 slots, 64 requests: 25.3 us for 35.7 with one).
+  static_assert(own_slots(128) <= 64, "D = 128: one warp");
+  if (c.D == 128) return launch_share<kHalf, 128, 1>(c, a, stream);
   const int units = c.B * c.Hkv;
-  if (c.cap <= 64 || units >= 12 * sms)
-    return launch_pdl(paged_prefix_own<kHalf, D, 1>, dim3((unsigned)((units + kWarps - 1) / kWarps)), dim3(kThreads), 0, stream, c, a);
-  return launch_pdl(paged_prefix_own<kHalf, D, kWarps>, dim3((unsigned)units), dim3(kThreads), 0, stream, c, a);
+  if (c.cap <= 64 || units >= 12 * sms) return launch_share<kHalf, 64, 1>(c, a, stream);
+  return units <= 2 * sms ? launch_share<kHalf, 64, 8>(c, a, stream) : launch_share<kHalf, 64, 4>(c, a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_own(bool half, int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  if (half) return c.D == 128 ? launch<true, 128>(sms, c, a, stream) : launch<true, 64>(sms, c, a, stream);
-  return c.D == 128 ? launch<false, 128>(sms, c, a, stream) : launch<false, 64>(sms, c, a, stream);
+  return half ? launch<true>(sms, c, a, stream) : launch<false>(sms, c, a, stream);
 }
 
 }  // namespace bastion
