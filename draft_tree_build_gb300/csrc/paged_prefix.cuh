@@ -8,11 +8,12 @@ namespace bastion {
 
 // Own slots in tables of at most this many slots go to paged_prefix_own.cu, others to
 // the one-token kernel.  Whole calls behind 2,000 shared tokens, 32/8 heads, one way
-// and the other: D = 64, 8 requests: 16 slots 15.0 and 19.9 us, 256 20.0 and 22.7, 512 23.7 and
-// 23.9; 256 requests: 512 slots 73.8 and 83.0.  D = 128, whose outputs take twice the registers,
-// so that half as many warps are on an SM: 8 requests: 64 slots 17.0 and 21.7, 128 20.5 and
-// 21.9; 256 requests: 64 slots 53.0 and 58.0, 128 70.5 and 60.0.
-__host__ __device__ constexpr int own_slots(int D) { return D == 64 ? 512 : 64; }
+// and the other: D = 64: 500 slots, 1, 8, 64, 200 requests: 14.4 and 16.3 us, 19.6 and 23.7,
+// 29.4 and 38.2, 62.7 and 71.1; 1,000 slots 19.1 and 19.1, 24.2 and 24.6, 41.1 and 50.1, 99 and 123;
+// 2,000 slots 27.9 and 20.0, 32.8 and 29.3, 64 and 80, 170 and 222.  D = 128, whose outputs take
+// twice the registers, so that half as many warps are on an SM: 64 slots, 8 requests 17.0
+// and 21.7, 256 53.0 and 58.0; 128 slots 23.5 and 21.9, 70.5 and 60.0.
+__host__ __device__ constexpr int own_slots(int D) { return D == 64 ? 1024 : 64; }
 
 // Where the join finds the parts of a request's rows of one KV head.  Part p is of
 // CTA x = p / planes, plane p % planes: at place0 + plane * step for x = 0 and at

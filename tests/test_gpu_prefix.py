@@ -293,7 +293,7 @@ def test_agrees_with_plain_paged_attention(cuda_lib):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (8, 1, 64), (12, 1, 128), (3, 1, 64)])
-@pytest.mark.parametrize("own", [40, 48, 49, 64, 65, 300, 480, 496, 497, 513, 3000])
+@pytest.mark.parametrize("own", [40, 48, 49, 64, 65, 300, 512, 1008, 1009, 1025, 3000])
 def test_short_and_long_own_slots(cuda_lib, Hq, Hkv, D, own):
     """On both sides of the sizes up to which own slots have a kernel of their own."""
     lens = [own, 0, 1, own // 2, min(own, 129), own - 1, min(own, 17)]
