@@ -30,9 +30,13 @@
 // Rows of a unit are whole requests (floor(128 / G) of them an M tile), so that a
 // box of the query tensor is an M tile, whatever G is.
 //
-// A part is the unnormalised row in 32 bits with its reference and sum.  Units
-// that one CTA finishes go to a row of their own, others to a slot of the CTA;
-// the join's warps work out from the shares where a row's parts are.
+// A part is an M tile's unnormalised rows in 32 bits with their references and sums.
+// Units that one CTA finishes have places of their own, others slots of the CTAs;
+// warp 3 works out from the shares where the join finds each request's.
+//
+// Measured in graphs, 32/8 heads, D = 128: 64 requests over 16,384 shared tokens (own slots up
+// to 512) 55 us, 256 over 32,768 157 us (131 of them products at 85% of the tensor cores' rate),
+// 4 over 300 11.8 us; 61 in 8 groups, 14/2 heads, D = 64, 22.5 us.
 //
 // Every wait is bounded (~1 s); after one ran out the CTA flags the requests of
 // its remaining tiles, waits for its own copies and products (bounded), frees its
