@@ -42,6 +42,7 @@
 // its remaining tiles, waits for its own copies and products (bounded), frees its
 // TMEM and returns.
 #include "paged_prefix.cuh"
+#include "paged_ring.cuh"
 #include "paged_tc.cuh"
 
 namespace bastion {
@@ -74,6 +75,7 @@ struct Layout {
 struct Misc {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2], mma_done;  // p_full: of a warpgroup's upper, lower keys
+  uint64_t begun;  // the first keys have landed; completes once
   int2 warp_sum[kThreads / 32];
   int warp_max[kThreads / 32];
   int li0, f0, f1;
@@ -88,6 +90,23 @@ constexpr uint32_t smem_bytes() {
   static_assert(n <= 227 * 1024, "shared memory of one CTA");
   return n;
 }
+
+// The ring's barriers as the warp that fills it has them (paged_ring.cuh).
+struct RingBars {
+  Misc &ms;
+  volatile int *abort;
+  int32_t *status;
+  int lane;
+  __device__ __forceinline__ bool wait(uint64_t &bar, uint32_t parity) {
+    return __all_sync(kFull, wait_bar(&bar, parity, abort, status));
+  }
+  __device__ __forceinline__ bool wait_full(int stage, uint32_t parity) { return wait(ms.full[stage], parity); }
+  __device__ __forceinline__ bool wait_empty(int stage, uint32_t parity) { return wait(ms.empty[stage], parity); }
+  __device__ __forceinline__ bool wait_begun() { return wait(ms.begun, 0); }
+  __device__ __forceinline__ void arrive_begun() {
+    if (lane == 0) mbar_arrive(&ms.begun);
+  }
+};
 
 // --------------------------------------------------------------------------- tensor memory
 
@@ -224,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_v, Paged c, PrefixArgs a) {
   using Lay = Layout<D>;
   constexpr int kStages = Lay::kStages, kBlocks = Lay::kBlocks;
+  using Tiles = Ring<kStages>;
   constexpr float kBias = kHalf ? 6.0f : 0.0f;  // weights are scaled by 2^kBias
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem =
@@ -250,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.pv_done[s], 1);
     }
     mbar_init(&ms.mma_done, 1);
+    mbar_init(&ms.begun, 1);
     ms.abort = 0;
     fence_mbar_init();
   }
@@ -407,10 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         entry_n = next_entry();
         in_batch = 0;
       }
-      const int x = 2 * issued + odd, slot = x % kStages;
-      // the first keys alone at first: all SMs fill their rings at once, and products begin 1 us sooner
-      if (x == 1 || x == 2) wait_bar(&ms.full[0], 0, abort, &a.status[w.req]);
-      if (!__all_sync(kFull, wait_bar(&ms.empty[slot], ((uint32_t)(x / kStages) & 1u) ^ 1u, abort, &a.status[w.req]))) break;
+      const int x = 2 * issued + odd, slot = Tiles::stage(x);
+      RingBars bars{ms, abort, &a.status[w.req], lane};
+      if (!Tiles::before(bars, x)) break;
       const int np = (min(kTileKeys, w.len - w.t * kTileKeys) + c.page - 1) >> c.shift;
       if (one) mbar_arrive_expect_tx(&ms.full[slot], (uint32_t)(np << c.shift) * (uint32_t)(D * 2));
       uint32_t dst = ring32 + (uint32_t)slot * Lay::kTile;
@@ -427,10 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++issued;
       ++in_batch;
     }
+    if (odd == 0 && issued > 0 && w.left == 0) {
+      RingBars bars{ms, abort, &a.status[w.req], lane};
+      Tiles::after_keys(bars, issued);
+    }
     // our last copies have landed (bounded) before the CTA may exit
     if (lane == 0) {
       for (int u = max(0, issued - kStages / 2); u < issued; ++u)
-        mbar_wait_bounded(&ms.full[(2 * u + odd) % kStages], (uint32_t)((2 * u + odd) / kStages) & 1u);
+        mbar_wait_bounded(&ms.full[Tiles::stage(2 * u + odd)], Tiles::full_parity(2 * u + odd));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
@@ -444,10 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int i_s = 0, m_s = 0, x_s = 0, q_s = 0;        // of the next S: visit, M tile, key tile, M tiles of segments before
     int i_p = 0, m_p = 0, x_p = 0, seg_p = 0;      // of the next P V: ..., key tile of its segment
     auto scores = [&]() {
-      const int wg = i_s & 1, x = 2 * x_s, slot = x % kStages, q = q_s + m_s, count = w.ms();
+      const int wg = i_s & 1, x = 2 * x_s, slot = Tiles::stage(x), q = q_s + m_s, count = w.ms();
       int32_t *st = &a.status[w.req];
       if (!__all_sync(kFull, (!w.first || wait_bar(&ms.q_full[q & 1], (uint32_t)(q >> 1) & 1u, abort, st)) &&
-                                 wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st)))
+                                 wait_bar(&ms.full[slot], Tiles::full_parity(x), abort, st)))
         return false;
       tc_fence_after();
       const uint64_t dk = d_ring + (uint32_t)slot * (Lay::kTile >> 4), dq = d_q + (uint32_t)(q & 1) * (Lay::kTile >> 4);
@@ -469,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto values = [&]() {
-      const int wg = i_p & 1, x = 2 * x_p + 1, slot = x % kStages, count = pw.ms();
+      const int wg = i_p & 1, x = 2 * x_p + 1, slot = Tiles::stage(x), count = pw.ms();
       int32_t *st = &a.status[pw.req];
       const bool fresh = seg_p < 3 - count;  // the segment's first visit of this warpgroup: key tile 0, or 0 and 1
       const uint64_t dv = d_v + (uint32_t)slot * (Lay::kTile >> 4);
@@ -477,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int part = 0; part < 2; ++part) {  // the upper 64 keys, whose weights are formed first, then the lower
         if (!__all_sync(kFull, wait_bar(&ms.p_full[wg][part], (uint32_t)(i_p >> 1) & 1u, abort, st) &&
-                                   (part > 0 || wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st))))
+                                   (part > 0 || wait_bar(&ms.full[slot], Tiles::full_parity(x), abort, st))))
           return false;
         tc_fence_after();
 #pragma unroll
@@ -581,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (valid < kTileKeys && (count == 1 || m == 0)) {  // value rows past the end: zeros, whatever the page holds there
-          const int x = 2 * x_t + 1, slot = x % kStages;
-          ok = __all_sync(kFull, wait_bar(&ms.full[slot], (uint32_t)(x / kStages) & 1u, abort, st));
+          const int x = 2 * x_t + 1, slot = Tiles::stage(x);
+          ok = __all_sync(kFull, wait_bar(&ms.full[slot], Tiles::full_parity(x), abort, st));
           if (!ok) break;
           unsigned char *tile = smem + slot * Lay::kTile;
 #pragma unroll 1
