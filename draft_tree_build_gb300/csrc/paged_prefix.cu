@@ -279,7 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   // No wait for the launch before: it attends to the own slots, of which nothing is read here, and let this one begin
-  // after everything before it was complete.  This launch ends after it (below), and the join waits for this one.
+  // after everything before it was complete (both kernels that do so wait first).  This launch ends after it (below), and
+  // the join waits for this one.  But what earlier launches wrote is certain to be in L2 alone: this SM's L1 may hold
+  // lines from before, which a wait here would have dropped.  So the groups and their tables are read past L1 (__ldcg),
+  // as the copies are by themselves.
   griddep_launch_dependents();
 
   // ------------------------------------------------------------ this CTA's share
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = g0 + i;
     from[i] = n_req[i] = len[i] = 0;
     if (i >= chunk || g >= a.n_groups) continue;
-    const int x = a.start[g], y = a.start[g + 1], n = a.len[g];
+    const int x = __ldcg(a.start + g), y = __ldcg(a.start + g + 1), n = __ldcg(a.len + g);
     if (x >= 0 && x <= y && y <= c.B) {
       from[i] = x;
       n_req[i] = y;  // for now, the end
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       lead = batch;
       const int pg = (lw.t << psh) + (lane & (ppt - 1));
       const bool on = (lane >> psh) < batch && lw.left > 0 && (pg << c.shift) < lw.len;
-      int e = on ? a.table[(size_t)lw.group * a.max_pages + pg] : 0;
+      int e = on ? __ldcg(a.table + (size_t)lw.group * a.max_pages + pg) : 0;
       if (e < 0 || e >= c.n_pages) {  // no page of the pool: page 0 stands in
         atomicOr(&a.status[lw.req], BASTION_STATUS_BAD_PAGE);
         e = 0;
