@@ -58,6 +58,17 @@ constexpr int kPer = (kMaxRequests + kThreads - 1) / kThreads;  // groups of a t
 constexpr int kBatch = 4;      // tiles whose table entries are read together
 constexpr float kGrow = 8.0f;  // a score may exceed its row's reference by 2^8
 
+// The tensor cores cut a sum to 32 bits where others round: O comes out too small by
+// half a unit of 2^-24 a product instruction on average, 16 instructions a key tile, and
+// half of that as it grows (54 tiles: 1.2e-5 of itself; 164 tiles, 800,000 tokens of 8 heads and
+// two M tiles: 8.8e-5, a third of half a step of half precision).  So a chain of products has
+// at most kChain visits, after which a warpgroup adds O, rounded, to what is in its part's
+// place: 2^-15 at most, whatever the length.  256 requests over 32,768 tokens (54 tiles a
+// CTA): 172 us without a limit and with 64, 176 with 32 (error 6e-6), 183 with 16 (2.5e-6).
+constexpr int kChain = 64;
+// Key tile x of a segment, counted from its chain's first.  A unit of one M tile deals its tiles to both warpgroups.
+__device__ __forceinline__ int chain_place(int x, int m_tiles) { return x & (kChain * (3 - m_tiles) - 1); }
+
 // --------------------------------------------------------------------------- shared memory
 
 // The value tiles' operand has D = N rows of MN-major blocks, all inside the stage.
@@ -498,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto values = [&]() {
       const int wg = i_p & 1, x = 2 * x_p + 1, slot = Tiles::stage(x), count = pw.ms();
       int32_t *st = &a.status[pw.req];
-      const bool fresh = seg_p < 3 - count;  // the segment's first visit of this warpgroup: key tile 0, or 0 and 1
+      const bool fresh = chain_place(seg_p, count) < 3 - count;  // a chain's first visit of this warpgroup: key tile 0, or 0 and 1
       const uint64_t dv = d_v + (uint32_t)slot * (Lay::kTile >> 4);
       const uint32_t p_col = tmem + 128u * (uint32_t)wg, o_col = tmem + 256u + 128u * (uint32_t)wg;
 #pragma unroll
@@ -588,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + ((uint32_t)(quad * 32) << 16) + 128u * (uint32_t)wg, o_col = s_col + 256u;
     int visits = 0, x_t = 0;  // this warpgroup's visits; the share's key tiles
     int par = 0, par0 = 0, t0 = 0, rows = 0, m = 0;
-    bool any = false, ok = true;
-    float ref = -INFINITY, l = 0.f;
+    bool any = false, stored = false, ok = true;  // something in O; in the part's place
+    float ref = -INFINITY, ref_stored = 0.f, l = 0.f;
     for (; w.left > 0; w.step(c.Hkv, a.nb), ++x_t) {
       const int count = w.ms();
       int32_t *st = &a.status[w.req];
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         t0 = w.t;
         m = count == 2 ? wg ^ par : 0;
         rows = min(a.nb, w.n - (2 * w.pair + m) * a.nb) * a.G;
-        any = false;
+        any = stored = false;
         ref = -INFINITY;
         l = 0.f;
       }
@@ -686,10 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++visits;
       }
       if (count == 1) par ^= 1;
-      if (!w.last()) continue;
+      const bool last = w.last();
+      if (!last && chain_place(w.t - t0 + 1, count) != 0) continue;
 
-      // ---------------------------------------------------------- the segment's end
-      const bool whole = t0 == 0 && w.t == w.tiles - 1;
+      // ---------------------------------------------------------- the end of a chain, or of the segment
+      const bool whole = t0 == 0 && w.t + w.left / count >= w.tiles;
       const int plane = count == 2 ? m : wg ^ par0;
       if (any) {
         ok = __all_sync(kFull, wait_bar(&ms.pv_done[wg], (uint32_t)(visits - 1) & 1u, abort, st));
@@ -702,21 +714,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *dst = (whole ? a.rows : a.parts) + place * D + row * 4;
         float2 *ml = (whole ? a.rows_ml : a.parts_ml) + place + row;
         if (any) {
+          const float before = ref_stored == ref ? 1.f : ex2f(ref_stored - ref);
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t o[32];
             ld32(o_col + 32u * (uint32_t)k, o);
             wait_ld(o);
             if (row < rows) {
+              if (stored) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 4) {
+                  const float4 x = *reinterpret_cast<const float4 *>(dst + (size_t)(32 * k + y) * rows);
+                  o[y] = __float_as_uint(fmaf(x.x, before, __uint_as_float(o[y])));
+                  o[y + 1] = __float_as_uint(fmaf(x.y, before, __uint_as_float(o[y + 1])));
+                  o[y + 2] = __float_as_uint(fmaf(x.z, before, __uint_as_float(o[y + 2])));
+                  o[y + 3] = __float_as_uint(fmaf(x.w, before, __uint_as_float(o[y + 3])));
+                }
+              }
 #pragma unroll
               for (int y = 0; y < 32; y += 4)
                 *reinterpret_cast<uint4 *>(dst + (size_t)(32 * k + y) * rows) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
             }
           }
         }
-        if (row < rows) *ml = make_float2(ref, l);
-        tc_fence_before();  // the next segment's products overwrite O after this warp's next arrival
+        if (row < rows && last) *ml = make_float2(ref, l);
+        tc_fence_before();  // the next chain's products overwrite O after this warp's next arrival
       }
+      if (any) ref_stored = ref;
+      stored = stored || any;
+      any = false;
     }
     if (!ok) {  // a wait ran out, of which only one request has been told
       for (; w.left > 0; w.step(c.Hkv, a.nb))

@@ -300,7 +300,10 @@ int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q
  * Limits: as bastion_paged_attention; 1 <= n_groups <= 1024, max_prefix_pages *
  * page_size <= 2^28, Hkv * ceil(max_prefix_pages * page_size / 128) * (n_groups +
  * B * Hq / Hkv / 112) < 2^31 (BASTION_ERR_SIZE).
- * Weights enter the products as there: as two 16-bit terms.  Results do not
+ * Weights enter the products as there: as two 16-bit terms.  The prefix's sums
+ * are formed in 32 bits by instructions that cut where others round, in chains of
+ * at most 8,192 keys a row (16,384 in two interleaved halves): an output lacks 2^-15
+ * of itself at most on average, whatever the prefix's length.  Results do not
  * depend on the order in which the parts of a split prefix finish.
  * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
  * n_groups) bytes, about 12 bytes an element of q and 55 MB.  Three launches: own
