@@ -618,20 +618,27 @@ def bastion_paged_plan(page_table, page_size, seq_len, m, held, held_out, free_p
     _check(rc, "bastion_paged_plan")
 
 
-def rope_frequencies(rot_dim, base=10000.0, device="cuda", scaling=None, factor=1.0, low=1.0, high=4.0, length=8192):
+def rope_frequencies(rot_dim, base=10000.0, device="cuda", scaling=None, factor=1.0, low=None, high=None, length=8192):
     """(inv_freq [rot_dim / 2] float64, the factor of cosines and sines) for bastion_qk_norm_rope.
 
     scaling None: base ** (-2 i / rot_dim).  For contexts `factor` times longer than the `length` that a model was
     trained on: "linear" divides every frequency by it; "base" raises the base so that the slowest pair is slowed by
-    it and the fastest not at all; "bands" divides the frequencies that turn fewer than `low` times over the length,
-    keeps those that turn more than `high` times, and goes over evenly in between; "yarn" does so by the pairs' number
-    instead (low and high the turns, 1 and 32 by default in that method), and scales cosines and sines by
-    0.1 log(factor) + 1."""
+    it and the fastest not at all (rot_dim above 2); "bands" divides the frequencies that turn fewer than `low` (1) times
+    over the length, keeps those that turn more than `high` (4) times, and goes over evenly in between; "yarn" does so by
+    the pairs' number instead, from the pair that turns `high` (32) times to the one that turns `low` (1) times, and
+    scales cosines and sines by 0.1 log(factor) + 1."""
+    low, high = 1.0 if low is None else low, (32.0 if scaling == "yarn" else 4.0) if high is None else high
+    if rot_dim < 0 or rot_dim % 2 or not (base > 0 and factor > 0):
+        raise BastionError("rope frequencies: rot_dim must be even, base and factor positive")
+    if scaling in ("bands", "yarn") and not (0 < low < high and length > 0 and base > 1):
+        raise BastionError("rope frequencies: bands and yarn take low in (0, high), length above 0 and base above 1")
     i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
-    f, size = base ** (-i / rot_dim), 1.0
+    f, size = base ** (-i / rot_dim) if rot_dim else i, 1.0
     if scaling == "linear":
         f = f / factor
     elif scaling == "base":
+        if rot_dim < 4:
+            raise BastionError("rope frequencies: one pair cannot be the slowest and the fastest")
         f = (base * factor ** (rot_dim / (rot_dim - 2))) ** (-i / rot_dim)
     elif scaling == "bands":
         turns = length * f / (2 * math.pi)
