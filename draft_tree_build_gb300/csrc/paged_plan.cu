@@ -197,10 +197,14 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   }
   __syncthreads();
 
-  // the y-th page given back; the page of entry idx >= held of request r
-  auto given = [&](int64_t y) {
-    const int r = last_at_most(s_back, a.B, y);
+  // the y-th page given back, and the request that gives it; the page of entry idx >= held of request r
+  auto given_by = [&](int64_t y, int &r) {
+    r = last_at_most(s_back, a.B, y);
     return a.table[(int64_t)r * a.max_pages + s_need[r] + (y - s_back[r])];
+  };
+  auto given = [&](int64_t y) {
+    int r;
+    return given_by(y, r);
   };
   auto taken = [&](int r, int idx) {
     const int64_t x = s_more[r] + (idx - s_held[r]);
@@ -275,7 +279,12 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   int64_t used = all_more;
   if (all_more > there) used = s_more[last_at_most(s_more, a.B + 1, there)];
   const int64_t left = there - used;
-  for (int64_t y = first; n_free + y < left && n_free + y < a.n_pages; y += stride) a.free_pages[n_free + y] = given(y);
+  for (int64_t y = first; y < all_back; y += stride) {  // those that other requests take at once are looked at, too
+    int r;
+    const int p = given_by(y, r);
+    if (p < 0 || p >= a.n_pages) atomicOr(&a.status[r], BASTION_STATUS_BAD_PAGE);
+    if (n_free + y < left && n_free + y < a.n_pages) a.free_pages[n_free + y] = p;
+  }
   if (s_last) {
     for (int r = tid; r < a.B; r += kThreads) {
       a.held_out[r] = s_need[r];

@@ -213,8 +213,9 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
  * (BASTION_STATUS_BAD_PAGE); too few free pages (BASTION_STATUS_NO_PAGE: first
  * come, first served; after the first such request none that needs a page gets
  * one).  Packed rows are first come, first served too.
- * A page number outside [0, n_pages) sets BASTION_STATUS_BAD_PAGE; its rows'
- * slots are -1.  n_free is taken as lying in [0, n_pages]; where it does not
+ * A page number outside [0, n_pages) sets BASTION_STATUS_BAD_PAGE, for the request
+ * whose rows it would hold, whose slots are -1 there, and for one that gives it back
+ * (it goes on the list as it is).  n_free is taken as lying in [0, n_pages]; where it does not
  * status[0] gets BASTION_STATUS_BAD_PAGE.
  * Limits: as the cache's; 1 <= m <= max_pages * page_size, 1 <= n_rows < 2^31.
  * Apart from the pairs above no output overlaps another array
