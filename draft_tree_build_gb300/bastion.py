@@ -946,8 +946,9 @@ class PagedCache:
     weights: keep the accumulated attention weight and the position of every slot, which evict() needs.
     new_tokens: the cache gives its requests their pages itself, out of n_pages (less the first `reserved`, which
     are the caller's, for prefixes say): reserve() finds pages and slots for up to new_tokens tokens a request and
-    write() fills them.  prefixes: the most groups that attend_shared() will be given.
-    After STATUS_TIMEOUT in status, zero ws_attend before the next attend()."""
+    write() fills them.  prefixes: the most groups that attend_shared() will be given (0: it is not used).
+    status [B] holds what the calls set but write()'s, which write_status [1] does.
+    After STATUS_TIMEOUT in status, call clear_workspaces() before the next call."""
 
     def __init__(self, B, Hq, Hkv, D, page_size, max_pages, device, dtype=torch.bfloat16, page_table=None,
                  n_pages=None, weights=False, new_tokens=0, reserved=0, prefixes=0):
@@ -976,7 +977,7 @@ class PagedCache:
         self.ws_append = workspace(bastion_paged_append_workspace_bytes(B), device)
         self.ws_attend = workspace(bastion_paged_attention_workspace_bytes(B, Hq, Hkv, D, self.cap, weights), device)
         self.ws_evict = workspace(bastion_paged_evict_workspace_bytes(B, Hkv, self.cap), device) if weights else None
-        self.new_tokens = new_tokens
+        self.new_tokens, self.ws_plan = new_tokens, None
         if new_tokens:
             self.held, self.n_free = i32(B), torch.full((1,), n_pages - reserved, dtype=torch.int32, device=device)
             self.free_pages = torch.zeros(n_pages, dtype=torch.int32, device=device)
@@ -986,6 +987,13 @@ class PagedCache:
             self.ws_plan, self.write_status = workspace(bastion_paged_plan_workspace_bytes(B), device), i32(1)
         self.ws_prefix = workspace(bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D, prefixes), device) \
             if prefixes else None
+
+    def clear_workspaces(self):
+        """Zeroes all workspaces, on the current stream: a call with STATUS_TIMEOUT leaves counters in the one that it
+        used, which the next one would count on from."""
+        for ws in (self.ws_append, self.ws_attend, self.ws_evict, self.ws_plan, self.ws_prefix):
+            if ws is not None:
+                ws.zero_()
 
     def contiguous(self):
         """(k, v) [B, cap, Hkv, D]: the same memory as a contiguous cache."""
