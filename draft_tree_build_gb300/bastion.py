@@ -51,7 +51,7 @@ SYMBOLS = (
 
 # the exported C symbols of the paged cache (include/bastion_cache.h), in header order
 CACHE_SYMBOLS = (
-    "bastion_paged_append_workspace_bytes", "bastion_paged_append",
+    "bastion_paged_append_workspace_bytes", "bastion_paged_append", "bastion_paged_append_held",
     "bastion_paged_attention_workspace_bytes", "bastion_paged_attention",
     "bastion_paged_evict_workspace_bytes", "bastion_paged_evict",
     "bastion_paged_plan_workspace_bytes", "bastion_paged_plan", "bastion_qk_norm_rope",
@@ -82,6 +82,7 @@ def _load_marshal(L):
            address(L.bastion_paged_evict))
     m.init_layer(torch.int64, torch.float64, address(L.bastion_paged_plan), address(L.bastion_qk_norm_rope),
                  address(L.bastion_paged_prefix_attention))
+    m.init_held(address(L.bastion_paged_append_held))
     return m
 
 
@@ -156,6 +157,8 @@ def lib(build_if_missing: bool = True):
     L.bastion_paged_append.restype = i32
     L.bastion_paged_append.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                        vp, sz, vp, vp]
+    L.bastion_paged_append_held.restype = i32
+    L.bastion_paged_append_held.argtypes = [vp, vp] + L.bastion_paged_append.argtypes[1:]
     L.bastion_paged_attention_workspace_bytes.restype = sz
     L.bastion_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i64, i32]
     L.bastion_paged_attention.restype = i32
@@ -481,13 +484,14 @@ def bastion_paged_append_workspace_bytes(B: int) -> int:
 
 
 def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, workspace, status,
-                         rows=None, n_new=None, acc=None, pos=None, n_seen=None, n_seen_out=None, stream=None):
+                         rows=None, n_new=None, acc=None, pos=None, n_seen=None, n_seen_out=None, stream=None, held=None):
     """k_new/v_new [B, n_rows, Hkv, D] (equal strides, last dim contiguous) enter the cache's next slots: the
     rows listed in rows [B, m] (a negative entry ends a list; Verify.accept_nodes fits), or the first n_new [B].
-    seq_len_out may be seq_len, n_seen_out n_seen."""
+    seq_len_out may be seq_len, n_seen_out n_seen.  held [B]: the pages that each request holds of a table that
+    bastion_paged_plan keeps (bastion_paged_append_held); rows that would reach past them are refused by status."""
     if _marshal is not None:
         rc = _marshal.append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, workspace, status, rows,
-                             n_new, acc, pos, n_seen, n_seen_out, stream)
+                             n_new, acc, pos, n_seen, n_seen_out, stream, held)
         if rc is not None:
             return _check(rc, "bastion_paged_append")
     dev, B, Hkv, D, cap, cache = _cache(k_pool, v_pool, page_table)
@@ -505,16 +509,17 @@ def bastion_paged_append(k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_
             raise BastionError("paged append: rows must be [B, m]")
         m = rows.shape[1]
         _need("rows", dev, torch.int32, (B, m), rows)
-    _need("seq_len seq_len_out status n_new n_seen n_seen_out", dev, torch.int32, (B,), seq_len, seq_len_out, status,
-          n_new, n_seen, n_seen_out)
+    _need("seq_len seq_len_out status n_new n_seen n_seen_out held", dev, torch.int32, (B,), seq_len, seq_len_out, status,
+          n_new, n_seen, n_seen_out, held)
     if acc is not None or pos is not None:
         _need("acc", dev, torch.float32, (B, Hkv, cap), acc)
         _need("pos", dev, torch.int32, (B, Hkv, cap), pos)
     st_cuda = _launch_on(dev, stream, workspace)
-    rc = lib().bastion_paged_append(cache, k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2],
-                                    _ptr(rows), m, _ptr(n_new), seq_len.data_ptr(), seq_len_out.data_ptr(),
-                                    _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos), workspace.data_ptr(),
-                                    workspace.numel(), status.data_ptr(), st_cuda)
+    args = (k_new.data_ptr(), v_new.data_ptr(), n_rows, st[0], st[1], st[2], _ptr(rows), m, _ptr(n_new),
+            seq_len.data_ptr(), seq_len_out.data_ptr(), _ptr(n_seen), _ptr(n_seen_out), _ptr(acc), _ptr(pos),
+            workspace.data_ptr(), workspace.numel(), status.data_ptr(), st_cuda)
+    rc = lib().bastion_paged_append(cache, *args) if held is None else \
+        lib().bastion_paged_append_held(cache, held.data_ptr(), *args)
     _check(rc, "bastion_paged_append")
 
 
@@ -1004,10 +1009,11 @@ class PagedCache:
 
     def append(self, k_new, v_new, rows=None, n_new=None, stream=None):
         """The rows of k_new/v_new [B, n_rows, Hkv, D] (all, the first n_new, or those listed in rows) enter the
-        next slots; rows = Verify.accept_nodes commits the accepted path of a verified tree."""
+        next slots; rows = Verify.accept_nodes commits the accepted path of a verified tree.  With new_tokens they
+        enter pages that reserve(advance=False) found; rows past a request's pages set STATUS_NO_PAGE."""
         bastion_paged_append(k_new, v_new, self.k_pool, self.v_pool, self.page_table, self.seq_len, self.seq_len,
                              self.ws_append, self.status, rows, n_new, self.acc, self.pos, self.n_seen, self.n_seen,
-                             stream)
+                             stream, self.held if self.new_tokens else None)
 
     def attend(self, q, scale, out, lse=None, stream=None):
         """out [B, Hq, D] = attention of q over the used slots; adds the weights to acc where they are kept."""
@@ -1022,17 +1028,18 @@ class PagedCache:
                             budget, n_sink, n_recent, self.seq_len, self.acc, self.pos, self.ws_evict, self.status,
                             stream)
 
-    def reserve(self, m, n_new=None, packed=False, n_rows=None, trim=False, stream=None):
+    def reserve(self, m, n_new=None, packed=False, n_rows=None, trim=False, stream=None, advance=True):
         """Pages and slots for the next n_new [B] (all: m) tokens of every request, whose lengths grow by them: (slots,
         positions), rows r * m + i for request r's token i, or packed, n_rows (all: B * m) of them from row_start[r]
-        on; -1 in rows without a token.  trim: pages that a request holds beyond its tokens go back (seq_len 0: all)."""
+        on; -1 in rows without a token.  trim: pages that a request holds beyond its tokens go back (seq_len 0: all).
+        advance False: the lengths stay as they are, and append() brings the rows (of a tree, those accepted)."""
         rows = self.B * m if n_rows is None or not packed else n_rows
         if not self.new_tokens or rows > self.slots.numel():
             raise BastionError("paged cache: reserve needs new_tokens of that many rows")
         slots, pos = self.slots[:rows], self.slot_pos[:rows]
         bastion_paged_plan(self.page_table, self.page_size, self.seq_len, m, self.held, self.held, self.free_pages,
                            self.n_free, self.n_free, slots, pos, self.ws_plan, self.status, n_new,
-                           self.row_start if packed else None, self.seq_len, trim, stream)
+                           self.row_start if packed else None, self.seq_len if advance else None, trim, stream)
         return slots, pos
 
     def write(self, q, k, v, pos, slots, inv_freq, q_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,

@@ -8,7 +8,7 @@
 
 namespace bastion {
 
-int launch_paged_append(const Paged &c, const void *k_new, const void *v_new, int n_rows, int64_t st_b,
+int launch_paged_append(const Paged &c, const int32_t *held, const void *k_new, const void *v_new, int n_rows, int64_t st_b,
                         int64_t st_row, int64_t st_head, const int32_t *rows, int m, const int32_t *n_new,
                         const int32_t *seq_len, int32_t *seq_len_out, const int32_t *n_seen,
                         int32_t *n_seen_out, float *acc, int32_t *pos, void *ws, int32_t *status,
@@ -149,22 +149,11 @@ int check_cache(const bastion_paged_cache *c) {
   return BASTION_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t bastion_paged_append_workspace_bytes(int B) {
-  if (B < 1 || B > kMaxB) return 0;
-  return (size_t)kMaxB * sizeof(uint32_t);  // arrival counters
-}
-
-int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, const void *v_new,
-                         int n_rows, int64_t new_stride_b, int64_t new_stride_row,
-                         int64_t new_stride_head, const int32_t *rows, int m,
-                         const int32_t *n_new, const int32_t *seq_len, int32_t *seq_len_out,
-                         const int32_t *n_seen, int32_t *n_seen_out, float *acc, int32_t *pos,
-                         void *workspace, size_t workspace_bytes, int32_t *status,
-                         bastion_stream_t stream) {
+// held: null, or the pages that each request holds.
+int append(const bastion_paged_cache *cache, const int32_t *held, const void *k_new, const void *v_new, int n_rows,
+           int64_t new_stride_b, int64_t new_stride_row, int64_t new_stride_head, const int32_t *rows, int m,
+           const int32_t *n_new, const int32_t *seq_len, int32_t *seq_len_out, const int32_t *n_seen, int32_t *n_seen_out,
+           float *acc, int32_t *pos, void *workspace, size_t workspace_bytes, int32_t *status, bastion_stream_t stream) {
   if (!k_new || !v_new || !seq_len || !seq_len_out || !workspace || !status) return BASTION_ERR_NULL;
   if ((acc == nullptr) != (pos == nullptr) || (n_seen == nullptr) != (n_seen_out == nullptr) || (acc && !n_seen))
     return BASTION_ERR_NULL;
@@ -187,16 +176,47 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
   // a request's last CTA writes its lengths while others still read their lists
   const size_t slots = slots_bytes(cache);
   const Array table = table_of(cache), list = {rows, (size_t)cache->B * m * 4}, weights = {acc, slots}, places = {pos, slots},
-              flags = {status, lens};
-  if (!all_apart({{seq_len_out, lens}, {n_seen_out, lens}}, {list, table, weights, places, flags}) ||
-      !all_apart({weights, places, flags}, {{seq_len, lens}, {n_seen, lens}, {n_new, lens}, list, table}) ||
+              flags = {status, lens}, have = {held, lens};
+  if (!all_apart({{seq_len_out, lens}, {n_seen_out, lens}}, {list, table, weights, places, flags, have}) ||
+      !all_apart({weights, places, flags}, {{seq_len, lens}, {n_seen, lens}, {n_new, lens}, list, table, have}) ||
       !all_apart({weights}, {places, flags}) || !all_apart({places}, {flags}))
     return BASTION_ERR_UNSUPPORTED;
   if (workspace_bytes < bastion_paged_append_workspace_bytes(cache->B)) return BASTION_ERR_WORKSPACE;
-  return bastion::launch_paged_append(bastion::paged_args(*cache), k_new, v_new, n_rows,
+  return bastion::launch_paged_append(bastion::paged_args(*cache), held, k_new, v_new, n_rows,
                                       cache->B > 1 ? new_stride_b : 0, n_rows > 1 ? new_stride_row : 0,
                                       cache->Hkv > 1 ? new_stride_head : 0, rows, m, n_new, seq_len, seq_len_out,
                                       n_seen, n_seen_out, acc, pos, workspace, status, (cudaStream_t)stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bastion_paged_append_workspace_bytes(int B) {
+  if (B < 1 || B > kMaxB) return 0;
+  return (size_t)kMaxB * sizeof(uint32_t);  // arrival counters
+}
+
+int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, const void *v_new,
+                         int n_rows, int64_t new_stride_b, int64_t new_stride_row,
+                         int64_t new_stride_head, const int32_t *rows, int m,
+                         const int32_t *n_new, const int32_t *seq_len, int32_t *seq_len_out,
+                         const int32_t *n_seen, int32_t *n_seen_out, float *acc, int32_t *pos,
+                         void *workspace, size_t workspace_bytes, int32_t *status,
+                         bastion_stream_t stream) {
+  return append(cache, nullptr, k_new, v_new, n_rows, new_stride_b, new_stride_row, new_stride_head, rows, m, n_new, seq_len,
+                seq_len_out, n_seen, n_seen_out, acc, pos, workspace, workspace_bytes, status, stream);
+}
+
+int bastion_paged_append_held(const bastion_paged_cache *cache, const int32_t *held, const void *k_new,
+                              const void *v_new, int n_rows, int64_t new_stride_b, int64_t new_stride_row,
+                              int64_t new_stride_head, const int32_t *rows, int m, const int32_t *n_new,
+                              const int32_t *seq_len, int32_t *seq_len_out, const int32_t *n_seen,
+                              int32_t *n_seen_out, float *acc, int32_t *pos, void *workspace,
+                              size_t workspace_bytes, int32_t *status, bastion_stream_t stream) {
+  if (!held) return BASTION_ERR_NULL;
+  return append(cache, held, k_new, v_new, n_rows, new_stride_b, new_stride_row, new_stride_head, rows, m, n_new, seq_len,
+                seq_len_out, n_seen, n_seen_out, acc, pos, workspace, workspace_bytes, status, stream);
 }
 
 size_t bastion_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int64_t cap, int weights) {

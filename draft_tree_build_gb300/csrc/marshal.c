@@ -22,6 +22,7 @@
 #include "bastion_cache.h"
 
 typedef __typeof__(&bastion_paged_append) append_fn;
+typedef __typeof__(&bastion_paged_append_held) append_held_fn;
 typedef __typeof__(&bastion_paged_attention) attention_fn;
 typedef __typeof__(&bastion_paged_evict) evict_fn;
 typedef __typeof__(&bastion_paged_plan) plan_fn;
@@ -29,6 +30,7 @@ typedef __typeof__(&bastion_qk_norm_rope) rope_fn;
 typedef __typeof__(&bastion_paged_prefix_attention) prefix_fn;
 
 static append_fn f_append;
+static append_held_fn f_append_held;
 static attention_fn f_attention;
 static evict_fn f_evict;
 static plan_fn f_plan;
@@ -179,17 +181,17 @@ static PyObject *declined(void) {
 }
 
 /* k_new, v_new, k_pool, v_pool, page_table, seq_len, seq_len_out, workspace, status, rows, n_new, acc, pos, n_seen,
- * n_seen_out, stream */
+ * n_seen_out, stream, and held or None, which may be left out */
 static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   bastion_paged_cache c;
   tensor k, v, rows;
   PyObject *dtype;
   long dev;
-  void *len, *len_out, *st, *n_new, *seen, *seen_out, *acc, *pos, *ws;
+  void *len, *len_out, *st, *n_new, *seen, *seen_out, *acc, *pos, *ws, *held = NULL;
   size_t bytes;
   bastion_stream_t stream;
-  if (n != 16 || !f_append || !cache_of(a[2], a[3], a[4], &c, &dev, &dtype)) return declined();
+  if ((n != 16 && n != 17) || !f_append || (n == 17 && !f_append_held) || !cache_of(a[2], a[3], a[4], &c, &dev, &dtype)) return declined();
   if (!look_strided(a[0], &k) || !look_strided(a[1], &v) || k.dim != 4 || v.dim != 4 || k.dtype != dtype ||
       v.dtype != dtype || k.dev != dev || v.dev != dev || k.stride[3] != 1)
     return declined();
@@ -210,12 +212,14 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       !contiguous_or_none(a[10], dev, dt_i32, 1, B, &n_new) ||
       !contiguous_or_none(a[11], dev, dt_f32, 3, slots, &acc) || !contiguous_or_none(a[12], dev, dt_i32, 3, slots, &pos) ||
       !contiguous_or_none(a[13], dev, dt_i32, 1, B, &seen) || !contiguous_or_none(a[14], dev, dt_i32, 1, B, &seen_out) ||
-      !stream_on(a[15], dev, &stream))
+      !stream_on(a[15], dev, &stream) || (n == 17 && !contiguous_or_none(a[16], dev, dt_i32, 1, B, &held)))
     return declined();
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = f_append(&c, k.ptr, v.ptr, (int)k.shape[1], k.stride[0], k.stride[1], k.stride[2], rows.ptr, (int)m, n_new, len,
-                len_out, seen, seen_out, acc, pos, ws, bytes, st, stream);
+  rc = held ? f_append_held(&c, held, k.ptr, v.ptr, (int)k.shape[1], k.stride[0], k.stride[1], k.stride[2], rows.ptr, (int)m,
+                            n_new, len, len_out, seen, seen_out, acc, pos, ws, bytes, st, stream)
+            : f_append(&c, k.ptr, v.ptr, (int)k.shape[1], k.stride[0], k.stride[1], k.stride[2], rows.ptr, (int)m, n_new, len,
+                       len_out, seen, seen_out, acc, pos, ws, bytes, st, stream);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
@@ -451,6 +455,15 @@ static PyObject *init_layer(PyObject *self, PyObject *args) {
   Py_RETURN_NONE;
 }
 
+/* The address of the append into held pages. */
+static PyObject *init_held(PyObject *self, PyObject *args) {
+  (void)self;
+  unsigned long long f;
+  if (!PyArg_ParseTuple(args, "K", &f)) return NULL;
+  f_append_held = (append_held_fn)(uintptr_t)f;
+  Py_RETURN_NONE;
+}
+
 /* bfloat16, float16, float32, int32, uint8, current device, raw stream of a device, and the addresses of the
  * library's three functions */
 static PyObject *init(PyObject *self, PyObject *args) {
@@ -475,6 +488,7 @@ static PyMethodDef methods[] = {{"init", init, METH_VARARGS, NULL},
                                 {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, NULL},
                                 {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
                                 {"init_layer", init_layer, METH_VARARGS, NULL},
+                                {"init_held", init_held, METH_VARARGS, NULL},
                                 {"plan", (PyCFunction)(void (*)(void))plan, METH_FASTCALL, NULL},
                                 {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, NULL},
                                 {"prefix", (PyCFunction)(void (*)(void))prefix, METH_FASTCALL, NULL},

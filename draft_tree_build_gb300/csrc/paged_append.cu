@@ -21,6 +21,7 @@ struct AppendArgs {
   const uint16_t *k_new, *v_new;
   int64_t st_b, st_row, st_head;
   const int32_t *rows, *n_new, *seq_len, *n_seen;
+  const int32_t *held;  // null, or the pages that each request holds: the table's later entries may be others' pages
   int32_t *seq_len_out, *n_seen_out;
   float *acc;
   int32_t *pos;
@@ -52,6 +53,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(Paged c, AppendA
   if (start < 0 || (int64_t)start + count > c.cap) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(&a.status[r], BASTION_STATUS_KV_OVERFLOW);
     count = 0;
+  } else if (a.held && count > 0) {
+    const int held = a.held[r];
+    const bool bad = held < 0 || held > c.max_pages;
+    if (bad || start + count > held << c.shift) {
+      if (tid == 0 && blockIdx.x == 0) atomicOr(&a.status[r], bad ? BASTION_STATUS_BAD_PAGE : BASTION_STATUS_NO_PAGE);
+      count = 0;
+    }
   }
   const int i0 = blockIdx.x * a.T, n = min(a.T, count - i0);
   if (tid < n) {
@@ -120,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(Paged c, AppendA
 
 }  // namespace
 
-int launch_paged_append(const Paged &c, const void *k_new, const void *v_new, int n_rows, int64_t st_b,
+int launch_paged_append(const Paged &c, const int32_t *held, const void *k_new, const void *v_new, int n_rows, int64_t st_b,
                         int64_t st_row, int64_t st_head, const int32_t *rows, int m, const int32_t *n_new,
                         const int32_t *seq_len, int32_t *seq_len_out, const int32_t *n_seen,
                         int32_t *n_seen_out, float *acc, int32_t *pos, void *ws, int32_t *status,
@@ -135,6 +143,7 @@ int launch_paged_append(const Paged &c, const void *k_new, const void *v_new, in
   a.n_new = n_new;
   a.seq_len = seq_len;
   a.n_seen = n_seen;
+  a.held = held;
   a.seq_len_out = seq_len_out;
   a.n_seen_out = n_seen_out;
   a.acc = acc;

@@ -96,6 +96,19 @@ int bastion_paged_append(const bastion_paged_cache *cache, const void *k_new, co
                          const int32_t *n_seen, int32_t *n_seen_out, float *acc, int32_t *pos,
                          void *workspace, size_t workspace_bytes, int32_t *status,
                          bastion_stream_t stream);
+/* The same into a table that bastion_paged_plan keeps: request r holds the pages of
+ * its first held[r] entries, and later entries may name pages that it gave back and
+ * that are others' now.  A request whose rows would reach past them sets
+ * BASTION_STATUS_NO_PAGE, one whose held[r] is outside [0, max_pages]
+ * BASTION_STATUS_BAD_PAGE: it gets nothing and keeps its lengths.  held [B] int32
+ * (BASTION_ERR_NULL without it), apart from the outputs. */
+int bastion_paged_append_held(const bastion_paged_cache *cache, const int32_t *held,
+                              const void *k_new, const void *v_new, int n_rows, int64_t new_stride_b,
+                              int64_t new_stride_row, int64_t new_stride_head, const int32_t *rows,
+                              int m, const int32_t *n_new, const int32_t *seq_len,
+                              int32_t *seq_len_out, const int32_t *n_seen, int32_t *n_seen_out,
+                              float *acc, int32_t *pos, void *workspace, size_t workspace_bytes,
+                              int32_t *status, bastion_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Attention of one new token per request over its used slots.
@@ -194,9 +207,11 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
  * order of its table, then new pages are popped, requests in order.
  *
  * page_table    [B, max_pages] int32: entries [held[r], ceil((n + c) /
- *               page_size)) are written, the others left as they are.
+ *               page_size)) are written, the others left as they are (those of
+ *               pages given back among them, which are no longer the request's).
  * seq_len, n_new, seq_len_out  [B] int32; n_new may be NULL (m for each) and
- *               seq_len_out NULL or seq_len: n + c.
+ *               seq_len_out NULL or seq_len: n + c.  NULL where the pages are for
+ *               rows that bastion_paged_append_held brings, which counts them.
  * held, held_out  [B] int32: pages held before and after; may be one array.
  * free_pages    [n_pages] int32, n_free, n_free_out [1] int32 (may be one).
  *               Entries at or past n_free are written where more pages come
