@@ -54,7 +54,7 @@ CACHE_SYMBOLS = (
     "bastion_paged_append_workspace_bytes", "bastion_paged_append", "bastion_paged_append_held",
     "bastion_paged_attention_workspace_bytes", "bastion_paged_attention",
     "bastion_paged_evict_workspace_bytes", "bastion_paged_evict",
-    "bastion_paged_plan_workspace_bytes", "bastion_paged_plan", "bastion_qk_norm_rope",
+    "bastion_paged_plan_workspace_bytes", "bastion_paged_plan", "bastion_paged_plan_offset", "bastion_qk_norm_rope",
     "bastion_paged_prefix_attention_workspace_bytes", "bastion_paged_prefix_attention",
 )
 
@@ -83,6 +83,7 @@ def _load_marshal(L):
     m.init_layer(torch.int64, torch.float64, address(L.bastion_paged_plan), address(L.bastion_qk_norm_rope),
                  address(L.bastion_paged_prefix_attention))
     m.init_held(address(L.bastion_paged_append_held))
+    m.init_offset(address(L.bastion_paged_plan_offset))
     return m
 
 
@@ -172,6 +173,8 @@ def lib(build_if_missing: bool = True):
     L.bastion_paged_plan.restype = i32
     L.bastion_paged_plan.argtypes = [vp, i32, i32, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp,
                                      vp, sz, vp, vp]
+    L.bastion_paged_plan_offset.restype = i32
+    L.bastion_paged_plan_offset.argtypes = L.bastion_paged_plan.argtypes[:-4] + [vp] + L.bastion_paged_plan.argtypes[-4:]
     L.bastion_qk_norm_rope.restype = i32
     L.bastion_qk_norm_rope.argtypes = [i32] * 5 + [vp, i64, i64] * 3 + [vp, vp, f32, vp, vp, i32, i32, f32] \
         + [vp, i64, i64] * 2 + [vp, vp, vp, vp]
@@ -591,13 +594,15 @@ def bastion_paged_plan_workspace_bytes(B: int) -> int:
 
 
 def bastion_paged_plan(page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos,
-                       workspace, status, n_new=None, row_start=None, seq_len_out=None, trim=False, stream=None):
+                       workspace, status, n_new=None, row_start=None, seq_len_out=None, trim=False, stream=None,
+                       pos_offset=None):
     """Pages and slots for the next n_new (all: m) tokens of every request.  page_table [B, max_pages]; held [B] pages
     in it; free_pages [n_pages] a stack of n_free [1]; slots int64 and pos int32 of B * m rows (request by request), or,
-    with row_start [B + 1], of any number of rows, packed.  held_out, n_free_out and seq_len_out may be their inputs."""
+    with row_start [B + 1], of any number of rows, packed.  held_out, n_free_out and seq_len_out may be their inputs.
+    pos_offset [B]: where each request's positions begin, behind a shared prefix (bastion_paged_plan_offset)."""
     if _marshal is not None:
         rc = _marshal.plan(page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos,
-                           workspace, status, n_new, row_start, seq_len_out, trim, stream)
+                           workspace, status, n_new, row_start, seq_len_out, trim, stream, pos_offset)
         if rc is not None:
             return _check(rc, "bastion_paged_plan")
     table, dev = page_table.shape, page_table.get_device()
@@ -607,19 +612,20 @@ def bastion_paged_plan(page_table, page_size, seq_len, m, held, held_out, free_p
         raise BastionError("paged plan: page_size and m must fit 32 bits")
     B, max_pages = table
     n_rows = slots.numel()
-    _need("seq_len held held_out status n_new seq_len_out", dev, torch.int32, (B,), seq_len, held, held_out, status, n_new,
-          seq_len_out)
+    _need("seq_len held held_out status n_new seq_len_out pos_offset", dev, torch.int32, (B,), seq_len, held, held_out, status,
+          n_new, seq_len_out, pos_offset)
     _need("n_free n_free_out", dev, torch.int32, (1,), n_free, n_free_out)
     _need("free_pages", dev, torch.int32, (free_pages.numel(),), free_pages)
     _need("slots", dev, torch.int64, slots.shape, slots)
     _need("pos", dev, torch.int32, slots.shape, pos)
     _need("row_start", dev, torch.int32, (B + 1,), row_start)
     st_cuda = _launch_on(dev, stream, workspace)
-    rc = lib().bastion_paged_plan(page_table.data_ptr(), B, max_pages, page_size, free_pages.numel(), seq_len.data_ptr(),
-                                  _ptr(n_new), m, _ptr(seq_len_out), held.data_ptr(), held_out.data_ptr(),
-                                  free_pages.data_ptr(), n_free.data_ptr(), n_free_out.data_ptr(), 1 if trim else 0,
-                                  slots.data_ptr(), pos.data_ptr(), n_rows, _ptr(row_start), workspace.data_ptr(),
-                                  workspace.numel(), status.data_ptr(), st_cuda)
+    args = (page_table.data_ptr(), B, max_pages, page_size, free_pages.numel(), seq_len.data_ptr(), _ptr(n_new), m,
+            _ptr(seq_len_out), held.data_ptr(), held_out.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+            n_free_out.data_ptr(), 1 if trim else 0, slots.data_ptr(), pos.data_ptr(), n_rows, _ptr(row_start))
+    last = (workspace.data_ptr(), workspace.numel(), status.data_ptr(), st_cuda)
+    rc = lib().bastion_paged_plan(*args, *last) if pos_offset is None else \
+        lib().bastion_paged_plan_offset(*args, pos_offset.data_ptr(), *last)
     _check(rc, "bastion_paged_plan")
 
 
@@ -1028,18 +1034,21 @@ class PagedCache:
                             budget, n_sink, n_recent, self.seq_len, self.acc, self.pos, self.ws_evict, self.status,
                             stream)
 
-    def reserve(self, m, n_new=None, packed=False, n_rows=None, trim=False, stream=None, advance=True):
+    def reserve(self, m, n_new=None, packed=False, n_rows=None, trim=False, stream=None, advance=True,
+                pos_offset=None):
         """Pages and slots for the next n_new [B] (all: m) tokens of every request, whose lengths grow by them: (slots,
         positions), rows r * m + i for request r's token i, or packed, n_rows (all: B * m) of them from row_start[r]
         on; -1 in rows without a token.  trim: pages that a request holds beyond its tokens go back (seq_len 0: all).
-        advance False: the lengths stay as they are, and append() brings the rows (of a tree, those accepted)."""
+        advance False: the lengths stay as they are, and append() brings the rows (of a tree, those accepted).
+        pos_offset [B]: the length of each request's shared prefix, where its positions begin (None: 0)."""
         rows = self.B * m if n_rows is None or not packed else n_rows
         if not self.new_tokens or rows > self.slots.numel():
             raise BastionError("paged cache: reserve needs new_tokens of that many rows")
         slots, pos = self.slots[:rows], self.slot_pos[:rows]
         bastion_paged_plan(self.page_table, self.page_size, self.seq_len, m, self.held, self.held, self.free_pages,
                            self.n_free, self.n_free, slots, pos, self.ws_plan, self.status, n_new,
-                           self.row_start if packed else None, self.seq_len if advance else None, trim, stream)
+                           self.row_start if packed else None, self.seq_len if advance else None, trim, stream,
+                           pos_offset)
         return slots, pos
 
     def write(self, q, k, v, pos, slots, inv_freq, q_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -1050,7 +1059,8 @@ class PagedCache:
                              factor, v, self.k_pool, self.v_pool, slots, stream)
 
     def attend_shared(self, q, prefix_table, prefix_len, group_start, scale, out, lse=None, stream=None):
-        """attend() over the groups' prefixes, in pages of this cache, and then over the requests' own slots."""
+        """attend() over the groups' prefixes, in pages of this cache, and then over the requests' own slots, whose keys
+        are turned by positions behind the prefix (reserve's pos_offset)."""
         if self.ws_prefix is None:
             raise BastionError("paged cache: attend_shared needs prefixes")
         bastion_paged_prefix_attention(q, self.k_pool, self.v_pool, self.page_table, self.seq_len, prefix_table, prefix_len,

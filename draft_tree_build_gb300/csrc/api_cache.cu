@@ -24,8 +24,8 @@ int launch_paged_evict(const Paged &c, const int32_t *seq_len, const int32_t *n_
 int launch_paged_plan(int32_t *table, int B, int max_pages, int page, int64_t n_pages, const int32_t *seq_len,
                       const int32_t *n_new, int m, int32_t *seq_len_out, const int32_t *held, int32_t *held_out,
                       int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
-                      int32_t *pos, int64_t n_rows, int32_t *row_start, void *ws, int32_t *status,
-                      cudaStream_t stream);
+                      int32_t *pos, int64_t n_rows, int32_t *row_start, const int32_t *pos_offset, void *ws,
+                      int32_t *status, cudaStream_t stream);
 int launch_qk_norm_rope(bool half, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t, int64_t q_st_h,
                         const void *k, int64_t k_st_t, int64_t k_st_h, const void *v, int64_t v_st_t, int64_t v_st_h,
                         const void *q_weight, const void *k_weight, float eps, const int32_t *pos,
@@ -188,6 +188,46 @@ int append(const bastion_paged_cache *cache, const int32_t *held, const void *k_
                                       n_seen, n_seen_out, acc, pos, workspace, status, (cudaStream_t)stream);
 }
 
+// pos_offset: null, or what is added to each request's positions.
+int plan(int32_t *page_table, int B, int max_pages, int page_size, int64_t n_pages, const int32_t *seq_len,
+         const int32_t *n_new, int m, int32_t *seq_len_out, const int32_t *held, int32_t *held_out, int32_t *free_pages,
+         const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots, int32_t *pos, int64_t n_rows,
+         int32_t *row_start, const int32_t *pos_offset, void *workspace, size_t workspace_bytes, int32_t *status,
+         bastion_stream_t stream) {
+  if (!page_table || !seq_len || !held || !held_out || !free_pages || !n_free || !n_free_out || !slots || !pos ||
+      !workspace || !status)
+    return BASTION_ERR_NULL;
+  const int64_t cap = (int64_t)max_pages * page_size;
+  if (B < 1 || B > kMaxB || max_pages < 1 || page_size < 1 || cap > kMaxCap || n_pages < 1 || n_pages >= (1LL << 31) ||
+      m < 1 || m > cap || n_rows < 1 || n_rows >= (1LL << 31) || (!row_start && n_rows != (int64_t)B * m))
+    return BASTION_ERR_SIZE;
+  if (page_size < 8 || page_size > 128 || (page_size & (page_size - 1))) return BASTION_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256) || !aligned(slots, 8) || !aligned(pos, 4) || !aligned(page_table, 4)) return BASTION_ERR_ALIGN;
+  const size_t lens = (size_t)B * 4;
+  if ((seq_len_out && !same_or_apart(seq_len, seq_len_out, lens)) || !same_or_apart(held, held_out, lens) ||
+      !same_or_apart(n_free, n_free_out, 4))
+    return BASTION_ERR_UNSUPPORTED;
+  const Array table = {page_table, (size_t)B * max_pages * 4}, stack = {free_pages, (size_t)n_pages * 4},
+              len = {seq_len, lens}, len_out = {seq_len_out, lens}, add = {n_new, lens}, have = {held, lens},
+              have_out = {held_out, lens}, left = {n_free, 4}, left_out = {n_free_out, 4},
+              at = {slots, (size_t)n_rows * 8}, place = {pos, (size_t)n_rows * 4}, begin = {row_start, lens + 4},
+              flags = {status, lens}, shift = {pos_offset, lens};
+  // every output against every other array but its own pair's
+  if (!all_apart({table}, {shift, stack, len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
+      !all_apart({stack}, {shift, len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
+      !all_apart({at}, {shift, len, len_out, add, have, have_out, left, left_out, place, begin, flags}) ||
+      !all_apart({place}, {shift, len, len_out, add, have, have_out, left, left_out, begin, flags}) ||
+      !all_apart({begin}, {shift, len, len_out, add, have, have_out, left, left_out, flags}) ||
+      !all_apart({flags}, {shift, len, len_out, add, have, have_out, left, left_out}) ||
+      !all_apart({len_out}, {shift, add, have, have_out, left, left_out}) ||
+      !all_apart({have_out}, {shift, len, add, left, left_out}) || !all_apart({left_out}, {shift, len, add, have}))
+    return BASTION_ERR_UNSUPPORTED;
+  if (workspace_bytes < bastion_paged_plan_workspace_bytes(B)) return BASTION_ERR_WORKSPACE;
+  return bastion::launch_paged_plan(page_table, B, max_pages, page_size, n_pages, seq_len, n_new, m, seq_len_out, held,
+                                    held_out, free_pages, n_free, n_free_out, trim, slots, pos, n_rows, row_start,
+                                    pos_offset, workspace, status, (cudaStream_t)stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -308,38 +348,20 @@ int bastion_paged_plan(int32_t *page_table, int B, int max_pages, int page_size,
                        const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
                        int32_t *pos, int64_t n_rows, int32_t *row_start, void *workspace,
                        size_t workspace_bytes, int32_t *status, bastion_stream_t stream) {
-  if (!page_table || !seq_len || !held || !held_out || !free_pages || !n_free || !n_free_out || !slots || !pos ||
-      !workspace || !status)
-    return BASTION_ERR_NULL;
-  const int64_t cap = (int64_t)max_pages * page_size;
-  if (B < 1 || B > kMaxB || max_pages < 1 || page_size < 1 || cap > kMaxCap || n_pages < 1 || n_pages >= (1LL << 31) ||
-      m < 1 || m > cap || n_rows < 1 || n_rows >= (1LL << 31) || (!row_start && n_rows != (int64_t)B * m))
-    return BASTION_ERR_SIZE;
-  if (page_size < 8 || page_size > 128 || (page_size & (page_size - 1))) return BASTION_ERR_UNSUPPORTED;
-  if (!aligned(workspace, 256) || !aligned(slots, 8) || !aligned(pos, 4) || !aligned(page_table, 4)) return BASTION_ERR_ALIGN;
-  const size_t lens = (size_t)B * 4;
-  if ((seq_len_out && !same_or_apart(seq_len, seq_len_out, lens)) || !same_or_apart(held, held_out, lens) ||
-      !same_or_apart(n_free, n_free_out, 4))
-    return BASTION_ERR_UNSUPPORTED;
-  const Array table = {page_table, (size_t)B * max_pages * 4}, stack = {free_pages, (size_t)n_pages * 4},
-              len = {seq_len, lens}, len_out = {seq_len_out, lens}, add = {n_new, lens}, have = {held, lens},
-              have_out = {held_out, lens}, left = {n_free, 4}, left_out = {n_free_out, 4},
-              at = {slots, (size_t)n_rows * 8}, place = {pos, (size_t)n_rows * 4}, begin = {row_start, lens + 4},
-              flags = {status, lens};
-  // every output against every other array but its own pair's
-  if (!all_apart({table}, {stack, len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
-      !all_apart({stack}, {len, len_out, add, have, have_out, left, left_out, at, place, begin, flags}) ||
-      !all_apart({at}, {len, len_out, add, have, have_out, left, left_out, place, begin, flags}) ||
-      !all_apart({place}, {len, len_out, add, have, have_out, left, left_out, begin, flags}) ||
-      !all_apart({begin}, {len, len_out, add, have, have_out, left, left_out, flags}) ||
-      !all_apart({flags}, {len, len_out, add, have, have_out, left, left_out}) ||
-      !all_apart({len_out}, {add, have, have_out, left, left_out}) ||
-      !all_apart({have_out}, {len, add, left, left_out}) || !all_apart({left_out}, {len, add, have}))
-    return BASTION_ERR_UNSUPPORTED;
-  if (workspace_bytes < bastion_paged_plan_workspace_bytes(B)) return BASTION_ERR_WORKSPACE;
-  return bastion::launch_paged_plan(page_table, B, max_pages, page_size, n_pages, seq_len, n_new, m, seq_len_out, held,
-                                    held_out, free_pages, n_free, n_free_out, trim, slots, pos, n_rows, row_start,
-                                    workspace, status, (cudaStream_t)stream);
+  return plan(page_table, B, max_pages, page_size, n_pages, seq_len, n_new, m, seq_len_out, held, held_out, free_pages, n_free,
+              n_free_out, trim, slots, pos, n_rows, row_start, nullptr, workspace, workspace_bytes, status, stream);
+}
+
+int bastion_paged_plan_offset(int32_t *page_table, int B, int max_pages, int page_size, int64_t n_pages,
+                              const int32_t *seq_len, const int32_t *n_new, int m, int32_t *seq_len_out,
+                              const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                              const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
+                              int32_t *pos, int64_t n_rows, int32_t *row_start, const int32_t *pos_offset,
+                              void *workspace, size_t workspace_bytes, int32_t *status,
+                              bastion_stream_t stream) {
+  if (!pos_offset) return BASTION_ERR_NULL;
+  return plan(page_table, B, max_pages, page_size, n_pages, seq_len, n_new, m, seq_len_out, held, held_out, free_pages, n_free,
+              n_free_out, trim, slots, pos, n_rows, row_start, pos_offset, workspace, workspace_bytes, status, stream);
 }
 
 int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q, int64_t q_st_t,

@@ -26,6 +26,7 @@ typedef __typeof__(&bastion_paged_append_held) append_held_fn;
 typedef __typeof__(&bastion_paged_attention) attention_fn;
 typedef __typeof__(&bastion_paged_evict) evict_fn;
 typedef __typeof__(&bastion_paged_plan) plan_fn;
+typedef __typeof__(&bastion_paged_plan_offset) plan_offset_fn;
 typedef __typeof__(&bastion_qk_norm_rope) rope_fn;
 typedef __typeof__(&bastion_paged_prefix_attention) prefix_fn;
 
@@ -34,6 +35,7 @@ static append_held_fn f_append_held;
 static attention_fn f_attention;
 static evict_fn f_evict;
 static plan_fn f_plan;
+static plan_offset_fn f_plan_offset;
 static rope_fn f_rope;
 static prefix_fn f_prefix;
 static PyObject *dt_i64, *dt_f64;
@@ -294,15 +296,15 @@ static int is_current(long dev) {
 }
 
 /* page_table, page_size, seq_len, m, held, held_out, free_pages, n_free, n_free_out, slots, pos, workspace, status, n_new,
- * row_start, seq_len_out, trim, stream */
+ * row_start, seq_len_out, trim, stream, and pos_offset or None, which may be left out */
 static PyObject *plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   tensor table, stack, slots;
-  void *at, *len, *held, *held_out, *pages, *left, *left_out, *slot, *pos, *ws, *st, *n_new, *start, *len_out;
+  void *at, *len, *held, *held_out, *pages, *left, *left_out, *slot, *pos, *ws, *st, *n_new, *start, *len_out, *offset = NULL;
   int page, m;
   size_t bytes;
   bastion_stream_t stream;
-  if (n != 18 || !f_plan || !look(a[0], &table) || table.dim != 2 || !is_current(table.dev)) return declined();
+  if ((n != 18 && n != 19) || !f_plan || (n == 19 && !f_plan_offset) || !look(a[0], &table) || table.dim != 2 || !is_current(table.dev)) return declined();
   const long dev = table.dev;
   if (!contiguous(a[0], dev, dt_i32, 2, table.shape, &at) || table.shape[0] > INT32_MAX - 1 || table.shape[1] > INT32_MAX ||
       !int32_of(a[1], &page) || !int32_of(a[3], &m) || !look(a[6], &stack) || stack.dim != 1 || !look(a[9], &slots) ||
@@ -322,12 +324,14 @@ static PyObject *plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       !contiguous(a[10], dev, dt_i32, slots.dim, slots.shape, &pos) || !workspace_of(a[11], dev, &ws, &bytes) ||
       !contiguous(a[12], dev, dt_i32, 1, B, &st) || !contiguous_or_none(a[13], dev, dt_i32, 1, B, &n_new) ||
       !contiguous_or_none(a[14], dev, dt_i32, 1, more, &start) || !contiguous_or_none(a[15], dev, dt_i32, 1, B, &len_out) ||
-      !stream_on(a[17], dev, &stream))
+      !stream_on(a[17], dev, &stream) || (n == 19 && !contiguous_or_none(a[18], dev, dt_i32, 1, B, &offset)))
     return declined();
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = f_plan(at, (int)table.shape[0], (int)table.shape[1], page, stack.shape[0], len, n_new, m, len_out, held, held_out,
-              pages, left, left_out, trim, slot, pos, rows, start, ws, bytes, st, stream);
+  rc = offset ? f_plan_offset(at, (int)table.shape[0], (int)table.shape[1], page, stack.shape[0], len, n_new, m, len_out, held,
+                              held_out, pages, left, left_out, trim, slot, pos, rows, start, offset, ws, bytes, st, stream)
+              : f_plan(at, (int)table.shape[0], (int)table.shape[1], page, stack.shape[0], len, n_new, m, len_out, held, held_out,
+                       pages, left, left_out, trim, slot, pos, rows, start, ws, bytes, st, stream);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
@@ -464,6 +468,15 @@ static PyObject *init_held(PyObject *self, PyObject *args) {
   Py_RETURN_NONE;
 }
 
+/* The address of the page plan whose positions begin at offsets. */
+static PyObject *init_offset(PyObject *self, PyObject *args) {
+  (void)self;
+  unsigned long long f;
+  if (!PyArg_ParseTuple(args, "K", &f)) return NULL;
+  f_plan_offset = (plan_offset_fn)(uintptr_t)f;
+  Py_RETURN_NONE;
+}
+
 /* bfloat16, float16, float32, int32, uint8, current device, raw stream of a device, and the addresses of the
  * library's three functions */
 static PyObject *init(PyObject *self, PyObject *args) {
@@ -489,6 +502,7 @@ static PyMethodDef methods[] = {{"init", init, METH_VARARGS, NULL},
                                 {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
                                 {"init_layer", init_layer, METH_VARARGS, NULL},
                                 {"init_held", init_held, METH_VARARGS, NULL},
+                                {"init_offset", init_offset, METH_VARARGS, NULL},
                                 {"plan", (PyCFunction)(void (*)(void))plan, METH_FASTCALL, NULL},
                                 {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, NULL},
                                 {"prefix", (PyCFunction)(void (*)(void))prefix, METH_FASTCALL, NULL},

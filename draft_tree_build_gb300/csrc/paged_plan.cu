@@ -29,6 +29,7 @@ struct PlanArgs {
   int B, max_pages, page, shift, cap, m, trim;
   int64_t n_pages, n_rows;
   const int32_t *seq_len, *n_new, *held, *n_free;
+  const int32_t *offset;  // null, or what is added to each request's positions
   int32_t *seq_len_out, *held_out, *n_free_out, *free_pages;
   int64_t *slots;
   int32_t *pos, *row_start;
@@ -83,7 +84,7 @@ __device__ __forceinline__ int last_at_most(const T *a, int n, T x) {
 __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   // per request: used slots, pages held, pages needed, new rows, and what comes before it of
   // pages given back, pages taken and packed rows (one more entry: the totals)
-  __shared__ int s_n[kMaxRequests], s_held[kMaxRequests], s_need[kMaxRequests], s_count[kMaxRequests];
+  __shared__ int s_n[kMaxRequests], s_held[kMaxRequests], s_need[kMaxRequests], s_count[kMaxRequests], s_offset[kMaxRequests];
   __shared__ int64_t s_back[kMaxRequests + 1], s_more[kMaxRequests + 1];
   __shared__ int s_row[kMaxRequests + 1];
   __shared__ int64_t sums[4][kThreads / 32];
@@ -92,16 +93,17 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   griddep_launch_dependents();
   const int tid = threadIdx.x, chunk = (a.B + kThreads - 1) / kThreads, r0 = tid * chunk;
   const bool tell = blockIdx.x == 0;
-  int n[kPer], held[kPer], need[kPer], count[kPer], bad[kPer];
+  int n[kPer], held[kPer], need[kPer], count[kPer], offset[kPer], bad[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = r0 + i;
     bad[i] = 0;
-    n[i] = held[i] = need[i] = count[i] = 0;
+    n[i] = held[i] = need[i] = count[i] = offset[i] = 0;
     if (i >= chunk || r >= a.B) continue;
     n[i] = a.seq_len[r];
     held[i] = a.held[r];
     count[i] = a.n_new ? min(a.m, max(a.n_new[r], 0)) : a.m;
+    if (a.offset) offset[i] = a.offset[r];
   }
   const int free_in = *a.n_free;
   const int64_t n_free = min((int64_t)max(free_in, 0), a.n_pages);
@@ -119,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
   int64_t rows[1] = {0}, all[1];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (n[i] < 0 || (int64_t)n[i] + count[i] > a.cap) bad[i] = BASTION_STATUS_KV_OVERFLOW;
+    if (n[i] < 0 || (int64_t)n[i] + count[i] > a.cap || offset[i] < 0 || offset[i] > INT32_MAX - a.cap)
+      bad[i] = BASTION_STATUS_KV_OVERFLOW;
     else if (held[i] < 0 || held[i] > a.max_pages || ((int64_t)held[i] << a.shift) < n[i]) bad[i] = BASTION_STATUS_BAD_PAGE;
     need[i] = bad[i] ? held[i] : (n[i] + count[i] + a.page - 1) >> a.shift;
     rows[0] += bad[i] ? 0 : count[i];
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
     s_held[r] = held[i];
     s_need[r] = need[i];
     s_count[r] = count[i];
+    s_offset[r] = offset[i];
     if (bad[i] && tell) atomicOr(&a.status[r], bad[i]);
   }
   int total_rows = 0;  // at most n_rows
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
               page = -1;
             }
           }
-          pos[u] = j;
+          pos[u] = s_offset[r] + j;
           if (page >= 0) slot[u] = ((int64_t)page << a.shift) + (j & (a.page - 1));
         }
         ++i;
@@ -302,9 +306,10 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a) {
 int launch_paged_plan(int32_t *table, int B, int max_pages, int page, int64_t n_pages, const int32_t *seq_len,
                       const int32_t *n_new, int m, int32_t *seq_len_out, const int32_t *held, int32_t *held_out,
                       int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
-                      int32_t *pos, int64_t n_rows, int32_t *row_start, void *ws, int32_t *status,
-                      cudaStream_t stream) {
+                      int32_t *pos, int64_t n_rows, int32_t *row_start, const int32_t *pos_offset, void *ws,
+                      int32_t *status, cudaStream_t stream) {
   PlanArgs a;
+  a.offset = pos_offset;
   a.table = table;
   a.B = B;
   a.max_pages = max_pages;

@@ -221,6 +221,9 @@ int bastion_paged_evict(const bastion_paged_cache *cache, const int32_t *seq_len
  *               none.  row_start NULL: request r's are rows r * m + i, and
  *               n_rows = B * m (BASTION_ERR_SIZE otherwise).  row_start [B+1]
  *               int32: they are packed, request r's are rows row_start[r] + i.
+ *               Positions count the request's own slots: behind a shared prefix
+ *               of P tokens a model's is P + n + i, which
+ *               bastion_paged_plan_offset gives.
  * A request that cannot be served gets no rows and no pages, gives none back and
  * keeps its length: seq_len outside [0, max_pages * page_size] or n + c beyond
  * it, or packed rows that would end past n_rows (BASTION_STATUS_KV_OVERFLOW);
@@ -244,6 +247,18 @@ int bastion_paged_plan(int32_t *page_table, int B, int max_pages, int page_size,
                        const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
                        int32_t *pos, int64_t n_rows, int32_t *row_start, void *workspace,
                        size_t workspace_bytes, int32_t *status, bastion_stream_t stream);
+/* The same with positions pos_offset[r] + n + i, -1 in rows without a token as
+ * before: own slots behind a shared prefix of pos_offset[r] tokens.  pos_offset [B]
+ * int32 (BASTION_ERR_NULL without it), apart from the outputs; a request whose
+ * offset is outside [0, 2^31 - 1 - max_pages * page_size] cannot be served and sets
+ * BASTION_STATUS_KV_OVERFLOW. */
+int bastion_paged_plan_offset(int32_t *page_table, int B, int max_pages, int page_size, int64_t n_pages,
+                              const int32_t *seq_len, const int32_t *n_new, int m, int32_t *seq_len_out,
+                              const int32_t *held, int32_t *held_out, int32_t *free_pages,
+                              const int32_t *n_free, int32_t *n_free_out, int trim, int64_t *slots,
+                              int32_t *pos, int64_t n_rows, int32_t *row_start,
+                              const int32_t *pos_offset, void *workspace, size_t workspace_bytes,
+                              int32_t *status, bastion_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Norm and rotation of T tokens' queries and keys, in one pass that may also
