@@ -744,9 +744,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       stored = stored || any;
       any = false;
     }
-    if (!ok) {  // a wait ran out, of which only one request has been told
-      for (; w.left > 0; w.step(c.Hkv, a.nb))
-        for (int b = w.req + row; b < w.req + w.n; b += 128) atomicOr(&a.status[b], BASTION_STATUS_TIMEOUT);
+    // A warp may give up alone, the others' waits ending just in time: it flags every request itself, not its rows' share.
+    const Units<true> stop = w;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int row = 32 * k + lane;
+      Units<true> w = stop;
+      if (!ok) {  // a wait ran out, of which only one request has been told
+        for (; w.left > 0; w.step(c.Hkv, a.nb))
+          for (int b = w.req + row; b < w.req + w.n; b += 128) atomicOr(&a.status[b], BASTION_STATUS_TIMEOUT);
+      }
     }
   }
   tc_fence_before();
