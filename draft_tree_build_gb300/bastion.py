@@ -1038,7 +1038,7 @@ class PagedCache:
                 pos_offset=None):
         """Pages and slots for the next n_new [B] (all: m) tokens of every request, whose lengths grow by them: (slots,
         positions), rows r * m + i for request r's token i, or packed, n_rows (all: B * m) of them from row_start[r]
-        on; -1 in rows without a token.  trim: pages that a request holds beyond its tokens go back (seq_len 0: all).
+        on; -1 in rows without a token.  Both are the cache's own, until the next reserve().  trim: pages that a request holds beyond its tokens go back (seq_len 0: all).
         advance False: the lengths stay as they are, and append() brings the rows (of a tree, those accepted).
         pos_offset [B]: the length of each request's shared prefix, where its positions begin (None: 0)."""
         rows = self.B * m if n_rows is None or not packed else n_rows
@@ -1054,7 +1054,7 @@ class PagedCache:
     def write(self, q, k, v, pos, slots, inv_freq, q_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
               factor=1.0, stream=None):
         """Norms and turns the queries and keys of reserve()'s rows and stores keys and values into their slots: q
-        [T, Hq, D], k and v [T, Hkv, D], q_out [T, Hq, D] or q."""
+        [T, Hq, D], k and v [T, Hkv, D], q_out [T, Hq, D] or q; rows without a token are left as they were."""
         bastion_qk_norm_rope(q, k, pos, inv_freq, q_out, self.write_status, None, q_weight, k_weight, eps, interleaved,
                              factor, v, self.k_pool, self.v_pool, slots, stream)
 

@@ -9,8 +9,8 @@
 namespace bastion {
 
 // Every call's arrival counters lie in the first bytes of its workspace and
-// nothing else does, so that calls of all sizes, and of all three kinds, can
-// share one: 2 * kMaxParts counters of groups, then one per (request, KV head).
+// nothing else does, so that calls of all sizes, and of all kinds, can share
+// one: 2 * kMaxParts counters of groups, then one per (request, KV head).
 constexpr int kMaxParts = 192;      // CTAs of an attention launch, at most
 constexpr int kMaxUnits = 65536;    // B * Hkv
 constexpr int kMaxRequests = 1024;  // B

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 64;" ::"r"(smem_u32(&ms.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // the wait first: the prefix launch of paged_prefix.cu, which may follow, counts on it
   griddep_wait();
   griddep_launch_dependents();
 

@@ -35,8 +35,8 @@
 // warp 3 works out from the shares where the join finds each request's.
 //
 // Measured in graphs, 32/8 heads, D = 128: 64 requests over 16,384 shared tokens (own slots up
-// to 512) 55 us, 256 over 32,768 157 us (131 of them products at 85% of the tensor cores' rate),
-// 4 over 300 11.8 us; 61 in 8 groups, 14/2 heads, D = 64, 22.5 us.
+// to 512) 55 us, 256 over 32,768 163 us (131 of them products at 85% of the tensor cores' rate;
+// a call from Python 168-173), 4 over 300 11.8 us; 61 in 8 groups, 14/2 heads, D = 64, 22.3 us.
 //
 // Every wait is bounded (~1 s); after one ran out the CTA flags the requests of
 // its remaining tiles, waits for its own copies and products (bounded), frees its

@@ -7,10 +7,13 @@
 namespace bastion {
 
 // Own slots in tables of at most this many slots go to paged_prefix_own.cu, others to
-// the one-token kernel.  Whole calls behind 2,000 shared tokens, 32/8 heads, one way
+// the one-token kernel.  By the table's width, as the lengths are known on the GPU alone: a table
+// much wider than its requests loses what short slots gain (tables of 4,096 slots for 33, 512, 257 and
+// 64: 4 requests 11.8 -> 14.0 us, 64 55 -> 55, 61 of 64-element heads 22.3 -> 28.4, 256 163 -> 180).  Whole calls behind 2,000 shared tokens, 32/8 heads, one way
 // and the other: D = 64: 500 slots, 1, 8, 64, 200 requests: 14.4 and 16.3 us, 19.6 and 23.7,
 // 29.4 and 38.2, 62.7 and 71.1; 1,000 slots 19.1 and 19.1, 24.2 and 24.6, 41.1 and 50.1, 99 and 123;
-// 2,000 slots 27.9 and 20.0, 32.8 and 29.3, 64 and 80, 170 and 222.  D = 128, whose outputs take
+// 2,000 slots 27.9 and 20.0, 32.8 and 29.3, 64 and 80, 170 and 222 (few requests lose where many gain; the limit is
+// where a single one no longer gains).  D = 128, whose outputs take
 // twice the registers, so that half as many warps are on an SM: 64 slots, 8 requests 17.0
 // and 21.7, 256 53.0 and 58.0; 128 slots 23.5 and 21.9, 70.5 and 60.0.
 __host__ __device__ constexpr int own_slots(int D) { return D == 64 ? 1024 : 64; }

@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(kThreads, 3) paged_prefix_join(Paged c, Prefix
 
 template <bool kHalf, int D>
 cudaError_t launch(int sms, const Paged &c, const PrefixArgs &a, cudaStream_t stream) {
-  // eight warps to a row's parts where rows are few and their parts, then, many
+  // Eight warps to a row's parts where rows are few and their parts, then, many; else two.  Whole calls over 16,384 shared
+  // tokens, 32/8 heads of 128, eight and two: 1,024 rows 31 and 40 us, 2,048 39.8 and 41.8, 2,560 48.7 and 49.5, 4,096 60.8 and
+  // 59.4, 8,192 103 and 99.  (64-element heads over 2,048 tokens: 17.6 and 21.0 at 2,560 rows, 21.3 and 21.4 at 4,096.)
   const unsigned x = (unsigned)((c.B * a.G + 31) / 32), y = (unsigned)c.Hkv;
   return c.B * a.Hq <= 16 * sms ? launch_pdl(paged_prefix_join<kHalf, D, 8>, dim3(x, y, D / kWide), dim3(kThreads), 0, stream, c, a)
                                 : launch_pdl(paged_prefix_join<kHalf, D, 2>, dim3(x, y, D / (4 * kWide)), dim3(kThreads), 0, stream, c, a);

@@ -135,7 +135,9 @@ int bastion_paged_append_held(const bastion_paged_cache *cache, const int32_t *h
  * NaN in a used key or query gives NaN in the heads that see it.
  * A request that BASTION_STATUS_TIMEOUT flags may lack the outputs of some or
  * all of its heads; acc_out is acc where a group's were not finished.
- * Scores, sums and outputs are accumulated in 32 bits.  A weight exp(s_j - lse)
+ * Scores, sums and outputs are accumulated in 32 bits, the outputs' sums by
+ * instructions that cut where others round: an output lacks about 1e-5 of itself at
+ * 16,384 slots in one CTA's share (64 requests of them), 1e-4 at 131,072.  A weight exp(s_j - lse)
  * enters the product with v_j as two 16-bit terms: off by 2^-17 of itself with
  * bf16, by 2^-22 of itself or 2^-31 of the row's largest weight with half
  * precision.  Results do not depend on the order in which the parts of a split
@@ -338,7 +340,13 @@ int bastion_qk_norm_rope(int dtype, int T, int Hq, int Hkv, int D, const void *q
  * depend on the order in which the parts of a split prefix finish.
  * Workspace: bastion_paged_prefix_attention_workspace_bytes(B, Hq, Hkv, D,
  * n_groups) bytes, about 12 bytes an element of q and 55 MB.  Three launches: own
- * slots, prefixes, join.
+ * slots, prefixes, join, 10 us at the least.  bastion_paged_attention with the
+ * prefix's pages in every request's table, one launch that reads them once a
+ * request, is faster where requests are few or the prefix is short: with 8 KV
+ * heads of 128, 4 queries each and 32 own slots up to a prefix of 16,384 slots for 2
+ * requests, 4,096 for 4, 1,024 for 8, 512 for 16 and 320 for 64 (512 own slots:
+ * 16,384, 8,192, 4,096, 2,048 and 512); with 2 KV heads of 64, 7 queries each, past
+ * 16,384 for up to 8 requests, to 2,048 for 16 and 320 for 64.
  */
 size_t bastion_paged_prefix_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int n_groups);
 int bastion_paged_prefix_attention(const bastion_paged_cache *cache, const int32_t *prefix_table,
