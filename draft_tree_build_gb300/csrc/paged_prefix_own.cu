@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kWarps, (D == 64 ? 16 : 8) / kWarps) page
   __shared__ int s_pages[kWarps / kShare][own_slots(D) / 8];
   __shared__ float2 s_ml[kShare == 1 ? 1 : kWarps][16];
   __shared__ __align__(16) float s_o[kShare == 1 ? 1 : kWarps][16][D];
-  griddep_wait();
+  griddep_wait();  // first: the prefix launch, which follows, counts on it
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int warp = (threadIdx.x >> 5) % kShare, tid = threadIdx.x % (32 * kShare);  // of the unit's
